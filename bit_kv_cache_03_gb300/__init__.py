@@ -48,6 +48,7 @@ class KVNVFP4Error(RuntimeError):
 
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
+_I64 = ctypes.c_int64
 _F64 = ctypes.c_double
 _SIG = {
     "kv_nvfp4_status_string": ([_I32], ctypes.c_char_p),
@@ -78,6 +79,17 @@ _SIG = {
                                    _P], _I32),
     "kv_nvfp4_decode_attn_noalloc": ([ctypes.POINTER(Layout), _P, _I32, _I32, _I32, _I32, _P, _P,
                                       ctypes.c_float, _P, _I32, _P, _I32, _P, _P, _P], _I32),
+    "kv_nvfp4_append_slots": ([ctypes.POINTER(Layout), _P, _P, _P, _P, _P, _P, _I32, _P, _I32, _P,
+                               _I32, _I32, _I32, _P, _P, _P, _P, _P], _I32),
+    "kv_nvfp4_weights_workspace_bytes": ([ctypes.POINTER(Layout), ctypes.POINTER(PlanInfo),
+                                          ctypes.POINTER(ctypes.c_size_t)], _I32),
+    "kv_nvfp4_decode_attn_weights": ([ctypes.POINTER(Layout), ctypes.POINTER(PlanInfo), _P, _P,
+                                      ctypes.c_size_t, _P, _P, ctypes.c_float, _P, _I32, _P, _I32,
+                                      _P, _P, _P, _I64, _P, _P], _I32),
+    "kv_nvfp4_evict_select": ([ctypes.POINTER(Layout), _P, _I64, _P, _P, _I32, _I32, _I32, _I32,
+                               _P, _I64, _P, _P], _I32),
+    "kv_nvfp4_evict_compact": ([ctypes.POINTER(Layout), _P, _I64, _I32, _P, _P, _I32, _P, _I32,
+                                _I32, _P, _P, _I32, _P, _I64, _P, _P], _I32),
     "kv_cmp_page_bytes": ([ctypes.POINTER(Layout), _I32], ctypes.c_size_t),
     "kv_cmp_append": ([ctypes.POINTER(Layout), _I32, _P, _P, _P, _P, _P, _I32, _P, _I32, _P, _I32,
                        _I32, _I32, _P, _P, _P, _P], _I32),
@@ -192,6 +204,17 @@ def kv_nvfp4_append(layout, q, k, v, seq_ids, positions, T, rope_table, rope_max
         "kv_nvfp4_append")
 
 
+def kv_nvfp4_append_slots(layout, q, k, v, seq_ids, slots, positions, T, rope_table, rope_max_pos,
+                          block_table, num_seqs, max_pages, num_pages, pool, q_codes=None,
+                          q_scales=None, status=None, stream=None):
+    """kv_nvfp4_append with each token's cache slot given apart from its position."""
+    _check(lib().kv_nvfp4_append_slots(
+        ctypes.byref(layout), _ptr(q), _ptr(k), _ptr(v), _ptr(seq_ids), _ptr(slots),
+        _ptr(positions), T, _ptr(rope_table), rope_max_pos, _ptr(block_table), num_seqs, max_pages,
+        num_pages, _ptr(pool), _ptr(q_codes), _ptr(q_scales), _ptr(status), _stream(stream)),
+        "kv_nvfp4_append_slots")
+
+
 def kv_nvfp4_plan_workspace_bytes(layout, seq_lens, q_len, causal, chunk_tokens) -> int:
     import numpy as np
     sl = np.ascontiguousarray(seq_lens, np.int32)
@@ -244,6 +267,49 @@ def kv_nvfp4_decode_attn(layout, plan: PlanInfo, workspace, q_codes, q_scales, s
         ctypes.byref(layout), ctypes.byref(plan), _ptr(workspace), _ptr(q_codes), _ptr(q_scales),
         float(sm_scale), _ptr(pool), num_pages, _ptr(block_table), max_pages, _ptr(out),
         _ptr(status), _stream(stream)), "kv_nvfp4_decode_attn")
+
+
+def kv_nvfp4_weights_workspace_bytes(layout, plan: PlanInfo) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().kv_nvfp4_weights_workspace_bytes(ctypes.byref(layout), ctypes.byref(plan),
+                                                  ctypes.byref(n)),
+           "kv_nvfp4_weights_workspace_bytes")
+    return n.value
+
+
+def kv_nvfp4_decode_attn_weights(layout, plan: PlanInfo, workspace, weights_workspace, ww_bytes,
+                                 q_codes, q_scales, sm_scale, pool, num_pages, block_table,
+                                 max_pages, out, weights_in, weights_out, weights_stride,
+                                 status=None, stream=None):
+    """Decode attention (bf16 output) that adds each key's attention weight to fp32 accounts
+    [num_seqs][num_kv_heads][weights_stride] (weights_in may be None: zeros, or weights_out)."""
+    _check(lib().kv_nvfp4_decode_attn_weights(
+        ctypes.byref(layout), ctypes.byref(plan), _ptr(workspace), _ptr(weights_workspace),
+        ww_bytes, _ptr(q_codes), _ptr(q_scales), float(sm_scale), _ptr(pool), num_pages,
+        _ptr(block_table), max_pages, _ptr(out), _ptr(weights_in), _ptr(weights_out),
+        weights_stride, _ptr(status), _stream(stream)), "kv_nvfp4_decode_attn_weights")
+
+
+def kv_nvfp4_evict_select(layout, weights, weights_stride, seq_lens, keep, num_seqs, per_head,
+                          sink, recent, index, index_stride, status=None, stream=None):
+    """The slots to keep by accumulated weight, ascending (seq_lens, keep: device int32)."""
+    _check(lib().kv_nvfp4_evict_select(
+        ctypes.byref(layout), _ptr(weights), weights_stride, _ptr(seq_lens), _ptr(keep), num_seqs,
+        int(per_head), sink, recent, _ptr(index), index_stride, _ptr(status), _stream(stream)),
+        "kv_nvfp4_evict_select")
+
+
+def kv_nvfp4_evict_compact(layout, index, index_stride, per_head, seq_lens, keep, num_seqs,
+                           block_table, max_pages, num_pages, pool, dst_block_table=None,
+                           dst_max_pages=0, weights=None, weights_stride=0, status=None,
+                           stream=None):
+    """Rows of the kept slots moved to the front of each sequence's cache (in place, or into the
+    pages of dst_block_table), the weights with them."""
+    _check(lib().kv_nvfp4_evict_compact(
+        ctypes.byref(layout), _ptr(index), index_stride, int(per_head), _ptr(seq_lens), _ptr(keep),
+        num_seqs, _ptr(block_table), max_pages, num_pages, _ptr(pool), _ptr(dst_block_table),
+        dst_max_pages, _ptr(weights), weights_stride, _ptr(status), _stream(stream)),
+        "kv_nvfp4_evict_compact")
 
 
 def kv_nvfp4_decode_step(layout, plan: PlanInfo, workspace, q, k, v, rope, rope_max_pos,

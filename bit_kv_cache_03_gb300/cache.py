@@ -9,9 +9,11 @@ import math
 import numpy as np
 import torch
 
-from . import (kv_nvfp4_append, kv_nvfp4_decode_attn, kv_nvfp4_decode_step,
-               kv_nvfp4_decode_step_host, kv_nvfp4_plan, kv_nvfp4_plan_workspace_bytes,
-               kv_nvfp4_pool_bytes, kv_nvfp4_rope_table_init, make_layout)
+from . import (kv_nvfp4_append, kv_nvfp4_append_slots, kv_nvfp4_decode_attn,
+               kv_nvfp4_decode_attn_weights, kv_nvfp4_decode_step, kv_nvfp4_decode_step_host,
+               kv_nvfp4_evict_compact, kv_nvfp4_evict_select, kv_nvfp4_plan,
+               kv_nvfp4_plan_workspace_bytes, kv_nvfp4_pool_bytes, kv_nvfp4_rope_table_init,
+               kv_nvfp4_weights_workspace_bytes, make_layout)
 
 
 class PagedNVFP4Cache:
@@ -35,11 +37,20 @@ class PagedNVFP4Cache:
             kv_nvfp4_rope_table_init(self.rope, self.max_pos, rot_dim, theta, pos_scale)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.workspace = None
+        self.weights_workspace = None
         self.plan_info = None
 
     # -- fused quantize-append --------------------------------------------------------------
-    def append(self, k, v, seq_ids, positions, q=None, q_codes=None, q_scales=None, stream=None):
+    def append(self, k, v, seq_ids, positions, q=None, q_codes=None, q_scales=None, stream=None,
+               slots=None):
+        """slots: int32 cache slots of the tokens where they differ from the positions (behind an
+        eviction)."""
         T = int(k.shape[0])
+        if slots is not None:
+            kv_nvfp4_append_slots(self.layout, q, k, v, seq_ids, slots, positions, T, self.rope,
+                                  self.max_pos, self.block_table, self.num_seqs, self.max_pages,
+                                  self.num_pages, self.pool, q_codes, q_scales, self.status, stream)
+            return
         kv_nvfp4_append(self.layout, q, k, v, seq_ids, positions, T, self.rope, self.max_pos,
                         self.block_table, self.num_seqs, self.max_pages, self.num_pages,
                         self.pool, q_codes, q_scales, self.status, stream)
@@ -64,6 +75,54 @@ class PagedNVFP4Cache:
         kv_nvfp4_decode_attn(self.layout, self.plan_info, self.workspace, q_codes, q_scales,
                              sm_scale, self.pool, self.num_pages, self.block_table, self.max_pages,
                              out, self.status, stream)
+
+    # -- attention that accounts for each key's weight, and eviction by it -----------------------
+    def weight_accounts(self):
+        """Zeroed accounts [num_seqs, num_kv_heads, slots] for attend_weights and evict."""
+        return torch.zeros(self.num_seqs, self.layout.num_kv_heads, self.max_pages * 64,
+                           dtype=torch.float32, device=self.device)
+
+    def attend_weights(self, q_codes, q_scales, out, weights, weights_in=None, sm_scale=None,
+                       stream=None):
+        """attend() with a bf16 `out`, adding every key's attention weight to `weights` (or writing
+        weights_in plus them). On the plan of the last plan()."""
+        self._check_accounts(weights, weights_in)
+        if out.dtype != torch.bfloat16 or not out.is_contiguous():
+            raise ValueError("out must be a contiguous bfloat16 tensor")
+        if sm_scale is None:
+            sm_scale = 1.0 / math.sqrt(128)
+        need = kv_nvfp4_weights_workspace_bytes(self.layout, self.plan_info)
+        if self.weights_workspace is None or self.weights_workspace.numel() < need:
+            self.weights_workspace = torch.empty(max(need, 256), dtype=torch.uint8,
+                                                 device=self.device)
+        kv_nvfp4_decode_attn_weights(
+            self.layout, self.plan_info, self.workspace, self.weights_workspace,
+            self.weights_workspace.numel(), q_codes, q_scales, sm_scale, self.pool, self.num_pages,
+            self.block_table, self.max_pages, out, weights if weights_in is None else weights_in,
+            weights, weights.shape[2], self.status, stream)
+
+    def evict(self, weights, seq_lens, keep, index, sink=0, recent=0, stream=None):
+        """Keeps min(seq_len, keep) tokens of each sequence by accumulated weight, the first `sink`
+        and the last `recent` ahead of the others, and compacts the cache and the weights to them
+        in place. seq_lens, keep: device int32 [num_seqs]; index: device int32
+        [num_seqs, num_kv_heads, n] (every KV head keeps its own tokens) or [num_seqs, 1, n] (one
+        set for all), n at least the largest kept count; receives the kept slots, ascending."""
+        self._check_accounts(weights)
+        if index.dtype != torch.int32 or not index.is_contiguous() or index.dim() != 3 or \
+                index.shape[0] != self.num_seqs or index.shape[1] not in (1, self.layout.num_kv_heads):
+            raise ValueError("index must be a contiguous int32 [num_seqs, num_kv_heads or 1, n]")
+        per_head = index.shape[1] != 1
+        kv_nvfp4_evict_select(self.layout, weights, weights.shape[2], seq_lens, keep, self.num_seqs,
+                              per_head, sink, recent, index, index.shape[2], self.status, stream)
+        kv_nvfp4_evict_compact(self.layout, index, index.shape[2], per_head, seq_lens, keep,
+                               self.num_seqs, self.block_table, self.max_pages, self.num_pages,
+                               self.pool, None, 0, weights, weights.shape[2], self.status, stream)
+
+    def _check_accounts(self, *tensors):
+        for w in tensors:
+            if w is not None and (w.dtype != torch.float32 or not w.is_contiguous() or w.dim() != 3 or
+                                  tuple(w.shape[:2]) != (self.num_seqs, self.layout.num_kv_heads)):
+                raise ValueError("weights must be contiguous float32 [num_seqs, num_kv_heads, slots]")
 
     # -- append of the step's new tokens + attention, one launch ------------------------------
     def decode_step(self, q, k, v, out, q_codes=None, q_scales=None, sm_scale=None, stream=None):

@@ -13,8 +13,8 @@
 
 namespace kvnvfp4 {
 cudaError_t launch_append(const uint16_t* q, const uint16_t* k, const uint16_t* v,
-                          const int32_t* seq_ids, const int32_t* positions, int64_t T,
-                          const float* rope, int32_t rope_max_pos, int32_t rot_dim,
+                          const int32_t* seq_ids, const int32_t* positions, const int32_t* slots,
+                          int64_t T, const float* rope, int32_t rope_max_pos, int32_t rot_dim,
                           const int32_t* block_table, int32_t num_seqs, int32_t max_pages,
                           int32_t num_pages, uint8_t* pool, uint8_t* q_codes,
                           uint8_t* q_scales, int32_t Hq, int32_t Hkv, int32_t* status,
@@ -28,7 +28,8 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
                           float sm_scale, const uint16_t* q_new, const uint16_t* k_new,
                           const uint16_t* v_new, const float* rope, int32_t rope_max_pos,
                           int32_t rot_dim, uint8_t* pool_w, uint8_t* q_codes_out,
-                          uint8_t* q_scales_out, bool late_tables, cudaStream_t stream);
+                          uint8_t* q_scales_out, bool late_tables, uint16_t* out16, float2* stats,
+                          cudaStream_t stream);
 int cmp_chunk_bytes(int fmt);
 cudaError_t launch_cmp_append(int fmt, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                               const int32_t* seq_ids, const int32_t* positions, int64_t T,
@@ -47,7 +48,25 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
                         const void* groups, const void* segments, const int32_t* cta_seg,
                         const int32_t* split_groups, int32_t num_split, float* partials,
                         float* out, int32_t* status, int32_t Hq, int32_t Hkv, int32_t q_len,
-                        int32_t causal, int32_t grid, float sm_scale, cudaStream_t stream);
+                        int32_t causal, int32_t grid, float sm_scale, uint16_t* out16,
+                        float2* stats, float* part_l, cudaStream_t stream);
+cudaError_t launch_weights(const uint8_t* q_codes, const uint8_t* q_scales, const uint8_t* pool,
+                           const int32_t* block_table, int32_t max_pages, int32_t num_pages,
+                           const void* groups, int32_t groups_per_seq, int32_t num_seqs,
+                           int32_t max_seq_len, int64_t total_tokens, const float2* stats,
+                           const float* w_in, float* w_out, int64_t w_stride, int32_t Hq,
+                           int32_t Hkv, int32_t q_len, int32_t causal, float sm_scale,
+                           int32_t num_sms, int32_t* status, cudaStream_t stream);
+cudaError_t launch_evict_select(const float* weights, int64_t w_stride, const int32_t* seq_lens,
+                                const int32_t* keep, int32_t num_seqs, int32_t per_head,
+                                int32_t sink, int32_t recent, int32_t* index, int64_t index_stride,
+                                int32_t Hkv, int32_t* status, cudaStream_t stream);
+cudaError_t launch_evict_compact(const int32_t* index, int64_t index_stride, int32_t per_head,
+                                 const int32_t* seq_lens, const int32_t* keep, int32_t num_seqs,
+                                 const int32_t* block_table, int32_t max_pages, int32_t num_pages,
+                                 uint8_t* pool, const int32_t* dst_table, int32_t dst_max_pages,
+                                 float* weights, int64_t w_stride, int32_t Hkv, int32_t* status,
+                                 cudaStream_t stream);
 cudaError_t launch_page_copy(bool spill, const uint8_t* src, uint8_t* dst, const int32_t* ids,
                              int32_t n, int32_t num_pages, uint32_t page_bytes, int sms,
                              int32_t* status, cudaStream_t stream);
@@ -453,11 +472,66 @@ static kv_nvfp4_status decode_step_impl(const kv_nvfp4_layout* L, const kv_nvfp4
       (float*)(ws + plan->off_partials), out, d_status,
       L->num_q_heads, L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
       (const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, d_rope_table, rope_max_pos,
-      L->rot_dim, pool, q_codes_out, q_scales_out, late_tables, (cudaStream_t)stream);
+      L->rot_dim, pool, q_codes_out, q_scales_out, late_tables, nullptr, nullptr,
+      (cudaStream_t)stream);
   return cuda_status(e);
 }
 
+// The append; d_slots null: every token's slot is its position.
+static kv_nvfp4_status append_impl(const kv_nvfp4_layout* L, const void* q, const void* k,
+                                   const void* v, const int32_t* d_seq_ids, const int32_t* d_slots,
+                                   const int32_t* d_positions, int32_t T,
+                                   const float* d_rope_table, int32_t rope_max_pos,
+                                   const int32_t* d_block_table, int32_t num_seqs,
+                                   int32_t max_pages, int32_t num_pages, uint8_t* pool,
+                                   uint8_t* q_codes, uint8_t* q_scales, int32_t* d_status,
+                                   void* stream) {
+  if (kv_nvfp4_layout_check(L) != KV_NVFP4_OK) return KV_NVFP4_EINVAL;
+  if (T < 0 || num_seqs <= 0 || max_pages <= 0 || num_pages <= 0) return KV_NVFP4_EINVAL;
+  if (T == 0) return KV_NVFP4_OK;
+  if (!k || !v || !d_seq_ids || !d_positions || !d_block_table || !pool) return KV_NVFP4_EINVAL;
+  if (q && (!q_codes || !q_scales)) return KV_NVFP4_EINVAL;
+  if (L->rot_dim > 0 && (!d_rope_table || rope_max_pos <= 0 || !aligned16(d_rope_table)))
+    return KV_NVFP4_EINVAL;
+  if (!aligned16(k) || !aligned16(v) || (q && !aligned16(q)) || !aligned16(pool))
+    return KV_NVFP4_EINVAL;
+  const cudaError_t e = kvnvfp4::launch_append(
+      (const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, d_seq_ids, d_positions, d_slots, T,
+      d_rope_table, rope_max_pos, L->rot_dim, d_block_table, num_seqs, max_pages, num_pages,
+      pool, q_codes, q_scales, L->num_q_heads, L->num_kv_heads,
+      d_status, num_sms_current_device(), (cudaStream_t)stream);
+  return cuda_status(e);
+}
 
+// Whether a plan's tiling and groups are those of this layout's attention kernel.
+static bool plan_matches(const kv_nvfp4_layout* L, const kv_nvfp4_plan_info* plan) {
+  if (kv_nvfp4_layout_check(L) != KV_NVFP4_OK || plan == nullptr) return false;
+  if (plan->num_kv_heads != L->num_kv_heads || plan->num_seqs <= 0 || plan->q_len <= 0 ||
+      plan->grid <= 0)
+    return false;
+  const int64_t rows = (int64_t)(L->num_q_heads / L->num_kv_heads) * plan->q_len;
+  const bool tile = tile_mode(L, plan->q_len);
+  const int64_t tile_rows = tile ? kTileRows : kRowsPerItem;
+  return plan->num_row_groups == (rows + tile_rows - 1) / tile_rows &&
+         plan->num_groups ==
+             (int64_t)plan->num_seqs * plan->num_row_groups * (tile ? L->num_kv_heads : 1);
+}
+
+// The second workspace of kv_nvfp4_decode_attn_weights: each row's softmax statistics, and on the
+// tile kernel the fp32 row sums of the split groups' partials.
+struct WeightsWorkspace {
+  uint64_t off_stats, off_part_l, bytes;
+};
+static WeightsWorkspace weights_workspace(const kv_nvfp4_layout* L, const kv_nvfp4_plan_info* plan) {
+  WeightsWorkspace w;
+  const uint64_t rows = (uint64_t)plan->num_seqs * (uint64_t)plan->q_len * L->num_q_heads;
+  w.off_stats = 0;
+  w.off_part_l = align_up(8 * rows, 256);
+  w.bytes = w.off_part_l;
+  if (tile_mode(L, plan->q_len))
+    w.bytes += align_up((uint64_t)plan->num_partials * kTileRows * 4, 256);
+  return w;
+}
 
 extern "C" {
 
@@ -547,21 +621,23 @@ kv_nvfp4_status kv_nvfp4_append(const kv_nvfp4_layout* L, const void* q, const v
                                 int32_t num_seqs, int32_t max_pages, int32_t num_pages,
                                 uint8_t* pool, uint8_t* q_codes, uint8_t* q_scales,
                                 int32_t* d_status, void* stream) {
-  if (kv_nvfp4_layout_check(L) != KV_NVFP4_OK) return KV_NVFP4_EINVAL;
-  if (T < 0 || num_seqs <= 0 || max_pages <= 0 || num_pages <= 0) return KV_NVFP4_EINVAL;
-  if (T == 0) return KV_NVFP4_OK;
-  if (!k || !v || !d_seq_ids || !d_positions || !d_block_table || !pool) return KV_NVFP4_EINVAL;
-  if (q && (!q_codes || !q_scales)) return KV_NVFP4_EINVAL;
-  if (L->rot_dim > 0 && (!d_rope_table || rope_max_pos <= 0 || !aligned16(d_rope_table)))
-    return KV_NVFP4_EINVAL;
-  if (!aligned16(k) || !aligned16(v) || (q && !aligned16(q)) || !aligned16(pool))
-    return KV_NVFP4_EINVAL;
-  const cudaError_t e = kvnvfp4::launch_append(
-      (const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, d_seq_ids, d_positions, T,
-      d_rope_table, rope_max_pos, L->rot_dim, d_block_table, num_seqs, max_pages, num_pages,
-      pool, q_codes, q_scales, L->num_q_heads, L->num_kv_heads,
-      d_status, num_sms_current_device(), (cudaStream_t)stream);
-  return cuda_status(e);
+  return append_impl(L, q, k, v, d_seq_ids, nullptr, d_positions, T, d_rope_table, rope_max_pos,
+                     d_block_table, num_seqs, max_pages, num_pages, pool, q_codes, q_scales,
+                     d_status, stream);
+}
+
+kv_nvfp4_status kv_nvfp4_append_slots(const kv_nvfp4_layout* L, const void* q, const void* k,
+                                      const void* v, const int32_t* d_seq_ids,
+                                      const int32_t* d_slots, const int32_t* d_positions,
+                                      int32_t T, const float* d_rope_table, int32_t rope_max_pos,
+                                      const int32_t* d_block_table, int32_t num_seqs,
+                                      int32_t max_pages, int32_t num_pages, uint8_t* pool,
+                                      uint8_t* q_codes, uint8_t* q_scales, int32_t* d_status,
+                                      void* stream) {
+  if (T > 0 && d_slots == nullptr) return KV_NVFP4_EINVAL;
+  return append_impl(L, q, k, v, d_seq_ids, d_slots, d_positions, T, d_rope_table, rope_max_pos,
+                     d_block_table, num_seqs, max_pages, num_pages, pool, q_codes, q_scales,
+                     d_status, stream);
 }
 
 kv_nvfp4_status kv_nvfp4_plan_workspace_bytes(const kv_nvfp4_layout* L, const int32_t* h_seq_lens,
@@ -646,7 +722,7 @@ kv_nvfp4_status kv_nvfp4_decode_attn(const kv_nvfp4_layout* L, const kv_nvfp4_pl
                              (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
                              (float*)(ws + plan->off_partials), out, d_status, L->num_q_heads,
                              L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
-                             (cudaStream_t)stream);
+                             nullptr, nullptr, nullptr, (cudaStream_t)stream);
   } else {
     e = kvnvfp4::launch_decode(
         q_codes, q_scales, pool, d_block_table, max_pages, num_pages, ws + plan->off_groups,
@@ -654,10 +730,110 @@ kv_nvfp4_status kv_nvfp4_decode_attn(const kv_nvfp4_layout* L, const kv_nvfp4_pl
         (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
         (float*)(ws + plan->off_partials), out, d_status,
         L->num_q_heads, L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
-        nullptr, nullptr, nullptr, nullptr, 0, 0, nullptr, nullptr, nullptr, false,
-        (cudaStream_t)stream);
+        nullptr, nullptr, nullptr, nullptr, 0, 0, nullptr, nullptr, nullptr, false, nullptr,
+        nullptr, (cudaStream_t)stream);
   }
   return cuda_status(e);
+}
+
+// ---- attention with per-key weights -----------------------------------------------------------
+kv_nvfp4_status kv_nvfp4_weights_workspace_bytes(const kv_nvfp4_layout* L,
+                                                 const kv_nvfp4_plan_info* plan, size_t* bytes) {
+  if (bytes == nullptr || !plan_matches(L, plan)) return KV_NVFP4_EINVAL;
+  *bytes = (size_t)weights_workspace(L, plan).bytes;
+  return KV_NVFP4_OK;
+}
+
+kv_nvfp4_status kv_nvfp4_decode_attn_weights(
+    const kv_nvfp4_layout* L, const kv_nvfp4_plan_info* plan, void* d_workspace,
+    void* d_weights_workspace, size_t ww_bytes, const uint8_t* q_codes, const uint8_t* q_scales,
+    float sm_scale, const uint8_t* pool, int32_t num_pages, const int32_t* d_block_table,
+    int32_t max_pages, void* out, const float* weights_in, float* weights_out,
+    int64_t weights_stride, int32_t* d_status, void* stream) {
+  if (!plan_matches(L, plan)) return KV_NVFP4_EINVAL;
+  if (!d_workspace || !d_weights_workspace || !q_codes || !q_scales || !pool || !d_block_table ||
+      !out || !weights_out || num_pages <= 0 || max_pages <= 0)
+    return KV_NVFP4_EINVAL;
+  if ((int64_t)plan->max_seq_len > (int64_t)max_pages * L->page_size ||
+      (int64_t)plan->max_seq_len > weights_stride)
+    return KV_NVFP4_EINVAL;
+  const void* ptrs[] = {d_workspace, d_weights_workspace, q_codes, q_scales, pool, out};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return KV_NVFP4_EINVAL;
+  const WeightsWorkspace w = weights_workspace(L, plan);
+  if (ww_bytes < w.bytes) return KV_NVFP4_ENOSPACE;
+  const int num_sms = num_sms_current_device();
+  if (num_sms <= 0) return cuda_status(cudaErrorNoDevice);
+  if (!(sm_scale > 0.0f)) sm_scale = 1.0f / std::sqrt((float)L->head_dim);
+  char* ws = (char*)d_workspace;
+  char* ww = (char*)d_weights_workspace;
+  float2* stats = (float2*)(ww + w.off_stats);
+  const bool tile = tile_mode(L, plan->q_len);
+  cudaError_t e;
+  if (tile) {
+    e = kvnvfp4::launch_tile(q_codes, q_scales, pool, d_block_table, max_pages, num_pages,
+                             ws + plan->off_groups, ws + plan->off_segments,
+                             (const int32_t*)(ws + plan->off_cta),
+                             (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
+                             (float*)(ws + plan->off_partials), nullptr, d_status, L->num_q_heads,
+                             L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
+                             (uint16_t*)out, stats, (float*)(ww + w.off_part_l),
+                             (cudaStream_t)stream);
+  } else {
+    e = kvnvfp4::launch_decode(
+        q_codes, q_scales, pool, d_block_table, max_pages, num_pages, ws + plan->off_groups,
+        ws + plan->off_segments, (const int32_t*)(ws + plan->off_cta),
+        (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
+        (float*)(ws + plan->off_partials), nullptr, d_status, L->num_q_heads, L->num_kv_heads,
+        plan->q_len, plan->causal, plan->grid, sm_scale, nullptr, nullptr, nullptr, nullptr, 0, 0,
+        nullptr, nullptr, nullptr, false, (uint16_t*)out, stats, (cudaStream_t)stream);
+  }
+  if (e != cudaSuccess) return cuda_status(e);
+  return cuda_status(kvnvfp4::launch_weights(
+      q_codes, q_scales, pool, d_block_table, max_pages, num_pages, ws + plan->off_groups,
+      plan->num_groups / plan->num_seqs, plan->num_seqs, plan->max_seq_len, plan->total_kv_tokens,
+      stats, weights_in, weights_out, weights_stride, L->num_q_heads, L->num_kv_heads, plan->q_len,
+      plan->causal, sm_scale, num_sms, d_status, (cudaStream_t)stream));
+}
+
+// ---- eviction by accumulated weight -----------------------------------------------------------
+kv_nvfp4_status kv_nvfp4_evict_select(const kv_nvfp4_layout* L, const float* weights,
+                                      int64_t weights_stride, const int32_t* d_seq_lens,
+                                      const int32_t* d_keep, int32_t num_seqs, int32_t per_head,
+                                      int32_t sink, int32_t recent, int32_t* d_index,
+                                      int64_t index_stride, int32_t* d_status, void* stream) {
+  if (kv_nvfp4_layout_check(L) != KV_NVFP4_OK || num_seqs < 0) return KV_NVFP4_EINVAL;
+  if (num_seqs == 0) return KV_NVFP4_OK;
+  if (!weights || !d_seq_lens || !d_keep || !d_index || weights_stride <= 0 || index_stride <= 0 ||
+      sink < 0 || recent < 0)
+    return KV_NVFP4_EINVAL;
+  return cuda_status(kvnvfp4::launch_evict_select(
+      weights, weights_stride, d_seq_lens, d_keep, num_seqs, per_head, sink, recent, d_index,
+      index_stride, L->num_kv_heads, d_status, (cudaStream_t)stream));
+}
+
+kv_nvfp4_status kv_nvfp4_evict_compact(const kv_nvfp4_layout* L, const int32_t* d_index,
+                                       int64_t index_stride, int32_t per_head,
+                                       const int32_t* d_seq_lens, const int32_t* d_keep,
+                                       int32_t num_seqs, const int32_t* d_block_table,
+                                       int32_t max_pages, int32_t num_pages, uint8_t* pool,
+                                       const int32_t* d_dst_block_table, int32_t dst_max_pages,
+                                       float* weights, int64_t weights_stride, int32_t* d_status,
+                                       void* stream) {
+  if (kv_nvfp4_layout_check(L) != KV_NVFP4_OK || num_seqs < 0) return KV_NVFP4_EINVAL;
+  if (num_seqs == 0) return KV_NVFP4_OK;
+  if (!d_index || !d_seq_lens || !d_keep || !d_block_table || !pool || index_stride <= 0 ||
+      max_pages <= 0 || num_pages <= 0 || !aligned16(pool))
+    return KV_NVFP4_EINVAL;
+  if (d_dst_block_table != nullptr ? dst_max_pages <= 0 : dst_max_pages != 0)
+    return KV_NVFP4_EINVAL;
+  if (weights != nullptr && weights_stride <= 0) return KV_NVFP4_EINVAL;
+  const bool in_place = d_dst_block_table == nullptr;
+  return cuda_status(kvnvfp4::launch_evict_compact(
+      d_index, index_stride, per_head, d_seq_lens, d_keep, num_seqs, d_block_table, max_pages,
+      num_pages, pool, in_place ? d_block_table : d_dst_block_table,
+      in_place ? max_pages : dst_max_pages, weights, weights_stride, L->num_kv_heads, d_status,
+      (cudaStream_t)stream));
 }
 
 kv_nvfp4_status kv_nvfp4_decode_step(const kv_nvfp4_layout* L, const kv_nvfp4_plan_info* plan,

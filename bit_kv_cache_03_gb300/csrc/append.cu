@@ -42,6 +42,7 @@ struct AppendParams {
   const uint16_t* v;
   const int32_t* seq_ids;
   const int32_t* positions;
+  const int32_t* slots;  // cache slot of each token, or null: its position
   int32_t T;             // tokens of this launch
   int32_t per_tok;       // rows per token: Hq + 2 Hkv (Hq = 0 without Q)
   const float* rope;
@@ -72,7 +73,7 @@ struct RowMeta {
 static_assert(sizeof(RowMeta) == 32, "metadata slot");
 
 // Resolves row w (Q heads, then K heads, then V heads) of token t: source row and destination,
-// with the checks and status bits of the call's definition (a bad sequence id or position skips
+// with the checks and status bits of the call's definition (a bad sequence id, position or slot skips
 // every row of the token; a bad page skips the K/V row; a rotated row past the RoPE table is
 // skipped). Status bits are set only when `report` (one caller per row).
 __device__ __forceinline__ const uint16_t* locate_row(const AppendParams& p, int32_t t, int32_t w,
@@ -81,12 +82,13 @@ __device__ __forceinline__ const uint16_t* locate_row(const AppendParams& p, int
   if (t >= p.T) return nullptr;
   const int32_t seq = p.seq_ids[t];
   const int32_t pos = p.positions[t];
+  const int32_t slot = p.slots != nullptr ? p.slots[t] : pos;
   bool bad = false;
   if (seq < 0 || seq >= p.num_seqs) {
     if (report) flag_status(p.status, KV_NVFP4_DEV_BAD_SEQ);
     bad = true;
   }
-  if (pos < 0 || pos >= p.max_pages * kPage) {
+  if (pos < 0 || slot < 0 || slot >= p.max_pages * kPage) {
     if (report) flag_status(p.status, KV_NVFP4_DEV_BAD_POS);
     bad = true;
   }
@@ -104,7 +106,7 @@ __device__ __forceinline__ const uint16_t* locate_row(const AppendParams& p, int
     const int32_t kv = w - p.Hq;
     const bool is_k = kv < p.Hkv;
     const int32_t h = is_k ? kv : kv - p.Hkv;
-    const int32_t page = p.block_table[(int64_t)seq * p.max_pages + pos / kPage];
+    const int32_t page = p.block_table[(int64_t)seq * p.max_pages + slot / kPage];
     if (page < 0 || page >= p.num_pages) {
       if (report) flag_status(p.status, KV_NVFP4_DEV_BAD_PAGE);
       return nullptr;
@@ -112,7 +114,7 @@ __device__ __forceinline__ const uint16_t* locate_row(const AppendParams& p, int
     // page block: [K codes H*4096 (tile order)][K scales H*512 (scale-copy order)][V codes
     // H*4096][V scales H*512]
     uint8_t* blk = p.pool + (int64_t)page * p.Hkv * 9216;
-    const int k = pos % kPage;
+    const int k = slot % kPage;
     src = (is_k ? p.k : p.v) + ((int64_t)t * p.Hkv + h) * kHeadDim;
     if (is_k) {
       m.codes = blk + h * 4096 + (k >> 3) * 512 + (k & 7) * 16;
@@ -428,8 +430,8 @@ constexpr int64_t kSmallRows = 8192;
 }  // namespace
 
 cudaError_t launch_append(const uint16_t* q, const uint16_t* k, const uint16_t* v,
-                          const int32_t* seq_ids, const int32_t* positions, int64_t T,
-                          const float* rope, int32_t rope_max_pos, int32_t rot_dim,
+                          const int32_t* seq_ids, const int32_t* positions, const int32_t* slots,
+                          int64_t T, const float* rope, int32_t rope_max_pos, int32_t rot_dim,
                           const int32_t* block_table, int32_t num_seqs, int32_t max_pages,
                           int32_t num_pages, uint8_t* pool, uint8_t* q_codes,
                           uint8_t* q_scales, int32_t Hq, int32_t Hkv, int32_t* status,
@@ -457,6 +459,7 @@ cudaError_t launch_append(const uint16_t* q, const uint16_t* k, const uint16_t* 
                    v + t0 * Hkv * kHeadDim,
                    seq_ids + t0,
                    positions + t0,
+                   slots != nullptr ? slots + t0 : nullptr,
                    (int32_t)n,
                    per_tok,
                    rope,

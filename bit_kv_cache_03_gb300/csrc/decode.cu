@@ -142,6 +142,9 @@ struct DecodeParams {
   // 1 when the plan tables (cta_seg, segments, groups) were written before the launch (not by the
   // kernel this one depends on), so that they may be read before the dependency wait
   int32_t early_tables;
+  // attention with per-key weights: bf16 rows instead of `out`, and each row's (m, 1 / l)
+  uint16_t* out16;         // [num_seqs * q_len][Hq][128]
+  float2* stats;           // [num_seqs][Hkv][G * q_len]
 };
 
 struct SegInfo {
@@ -727,7 +730,7 @@ __device__ __forceinline__ void fused_prologue(const DecodeParams& p, const SegI
   if (nrows > 0 && aw == 0 && lane == 0) mbar_arrive(bars + 8 * kBarKvReady);
 }
 
-template <int NR, bool FUSED>
+template <int NR, bool FUSED, bool ACC>
 __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t tbase, int warp,
                                 int lane) {
   AttnCtx c;
@@ -933,6 +936,17 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
               part[kRows * 128 + i] = M[hh];
               part[kRows * 128 + kRows + i] = L[hh];
             }
+          } else if (ACC) {
+            if (r < rows_total) {
+              const int tok = r / p.G, qh = c.head * p.G + r % p.G;
+              const float inv = L[hh] > 0.f ? 1.f / L[hh] : 0.f;
+              store_bf16x16(
+                  p.out16 + (((int64_t)sg.seq * p.q_len + tok) * p.Hq + qh) * 128 + 16 * g, o[hh],
+                  inv);
+              if (g == 0)
+                p.stats[((int64_t)sg.seq * p.Hkv + c.head) * rows_total + r] =
+                    make_float2(M[hh], inv);
+            }
           } else if (r < rows_total && L[hh] > 0.f) {
             const int tok = r / p.G, qh = c.head * p.G + r % p.G;
             float4* dst = reinterpret_cast<float4*>(
@@ -951,8 +965,9 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
 }
 
 // NR: query rows computed per head (6 when no tile has more real rows, else all 8); FUSED: the
-// step's append is done in the kernel (kv_nvfp4_decode_step)
-template <int NR, bool FUSED>
+// step's append is done in the kernel (kv_nvfp4_decode_step); ACC: rows go out in bf16 with their
+// softmax statistics, for the weight pass after it (kv_nvfp4_decode_attn_weights)
+template <int NR, bool FUSED, bool ACC>
 __global__ void __launch_bounds__(kBoundThreads, 1) decode_kernel(const DecodeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1005,7 +1020,7 @@ __global__ void __launch_bounds__(kBoundThreads, 1) decode_kernel(const DecodePa
   } else if (warp == kWarpMma) {
     qk_warp<FUSED>(p, smem, tbase, lane);
   } else {
-    attention_warps<NR, FUSED>(p, smem, tbase, warp, lane);
+    attention_warps<NR, FUSED, ACC>(p, smem, tbase, warp, lane);
   }
 
   if (warp == kWarpMma) {
@@ -1036,6 +1051,8 @@ struct MergeParams {
   float* out;
   int32_t Hq, Hkv, G, q_len;
   float c2;
+  uint16_t* out16;         // ACC: bf16 rows and (m, 1 / l) per row, as in DecodeParams
+  float2* stats;
 };
 
 constexpr int kMergeSlices = 8;
@@ -1043,7 +1060,7 @@ constexpr int kMergePerRound = 8;  // partials a slice requests at once (64 per 
 
 // LATE_TABLES: the plan tables were written by a kernel earlier in the same step (not by a copy
 // before the attention launch), so they are read only after the wait as well.
-template <bool LATE_TABLES>
+template <bool LATE_TABLES, bool ACC>
 __global__ void __launch_bounds__(32 * kMergeSlices, 2) merge_kernel(const MergeParams p) {
   __shared__ float s_m[kMergeSlices], s_l[kMergeSlices];
   __shared__ float4 s_o[kMergeSlices][32];
@@ -1115,7 +1132,15 @@ __global__ void __launch_bounds__(32 * kMergeSlices, 2) merge_kernel(const Merge
       Lt += f * s_l[j];
       Ot.x += f * v.x; Ot.y += f * v.y; Ot.z += f * v.z; Ot.w += f * v.w;
     }
-    if (Lt > 0.f) {
+    if (ACC) {
+      const int tok = r / p.G, qh = h * p.G + r % p.G;
+      const float inv = Lt > 0.f ? 1.f / Lt : 0.f;
+      *reinterpret_cast<uint2*>(
+          p.out16 + (((int64_t)g0.x * p.q_len + tok) * p.Hq + qh) * 128 + 4 * d4) =
+          make_uint2(pack_bf16x2(Ot.x * inv, Ot.y * inv), pack_bf16x2(Ot.z * inv, Ot.w * inv));
+      if (d4 == 0)
+        p.stats[((int64_t)g0.x * p.Hkv + h) * (p.G * p.q_len) + r] = make_float2(Mt, inv);
+    } else if (Lt > 0.f) {
       const int tok = r / p.G, qh = h * p.G + r % p.G;
       float4* dst = reinterpret_cast<float4*>(
           p.out + (((int64_t)g0.x * p.q_len + tok) * p.Hq + qh) * 128 + 4 * d4);
@@ -1134,6 +1159,9 @@ cudaError_t launch_split_merge(const void* groups, const int32_t* split_groups,
                                int32_t G, int32_t q_len, float c2, int32_t num_split,
                                bool late_tables, cudaStream_t stream);
 
+static cudaError_t launch_merge(const MergeParams& mp, int32_t num_split, bool late_tables,
+                                cudaStream_t stream);
+
 cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const uint8_t* pool,
                           const int32_t* block_table, int32_t max_pages, int32_t num_pages,
                           const void* groups, const void* segments, const int32_t* cta_seg,
@@ -1143,15 +1171,18 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
                           float sm_scale, const uint16_t* q_new, const uint16_t* k_new,
                           const uint16_t* v_new, const float* rope, int32_t rope_max_pos,
                           int32_t rot_dim, uint8_t* pool_w, uint8_t* q_codes_out,
-                          uint8_t* q_scales_out, bool late_tables, cudaStream_t stream) {
+                          uint8_t* q_scales_out, bool late_tables, uint16_t* out16, float2* stats,
+                          cudaStream_t stream) {
   // the attribute belongs to each instantiation and each device: set once per device
   static bool attr_done[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
   if (dev < 0 || dev >= 64 || !attr_done[dev]) {
     cudaError_t e = cudaSuccess;
-    const void* kernels[] = {(const void*)decode_kernel<8, false>, (const void*)decode_kernel<6, false>,
-                             (const void*)decode_kernel<8, true>, (const void*)decode_kernel<6, true>};
+    const void* kernels[] = {
+        (const void*)decode_kernel<8, false, false>, (const void*)decode_kernel<6, false, false>,
+        (const void*)decode_kernel<8, true, false>,  (const void*)decode_kernel<6, true, false>,
+        (const void*)decode_kernel<8, false, true>,  (const void*)decode_kernel<6, false, true>};
     for (const void* kf : kernels)
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kf, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
@@ -1172,6 +1203,7 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
   p.rope_max_pos = rope_max_pos; p.rot_dim = rot_dim; p.pool_w = pool_w;
   p.q_codes_out = q_codes_out; p.q_scales_out = q_scales_out;
   p.early_tables = late_tables ? 0 : 1;
+  p.out16 = out16; p.stats = stats;
   const bool fused = q_new != nullptr;
   if (grid <= 0) return cudaSuccess;
   // programmatic dependent launch: the kernel is set up while the previous kernel on the stream
@@ -1190,16 +1222,21 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
     // every tile has at most G * q_len real rows: with six or fewer, rows 6 and 7 are never computed
     const bool six = p.G * q_len <= 6;
     const cudaError_t le =
-        fused ? (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, true>, p)
-                     : cudaLaunchKernelEx(&dc, decode_kernel<8, true>, p))
-              : (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, false>, p)
-                     : cudaLaunchKernelEx(&dc, decode_kernel<8, false>, p));
+        out16 ? (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, false, true>, p)
+                     : cudaLaunchKernelEx(&dc, decode_kernel<8, false, true>, p))
+        : fused ? (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, true, false>, p)
+                       : cudaLaunchKernelEx(&dc, decode_kernel<8, true, false>, p))
+                : (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, false, false>, p)
+                       : cudaLaunchKernelEx(&dc, decode_kernel<8, false, false>, p));
     if (le != cudaSuccess) return le;
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || num_split <= 0) return e;
-  return launch_split_merge(p.groups, split_groups, partials, out, Hq, Hkv, p.G, q_len, p.c2,
-                            num_split, late_tables, stream);
+  MergeParams mp;
+  mp.groups = p.groups; mp.split = split_groups; mp.partials = partials; mp.out = out;
+  mp.Hq = Hq; mp.Hkv = Hkv; mp.G = p.G; mp.q_len = q_len; mp.c2 = p.c2;
+  mp.out16 = out16; mp.stats = stats;
+  return launch_merge(mp, num_split, late_tables, stream);
 }
 
 // The split-K merge launch (also used by the comparator decode): one CTA per (split group, KV
@@ -1213,8 +1250,14 @@ cudaError_t launch_split_merge(const void* groups, const int32_t* split_groups,
   MergeParams mp;
   mp.groups = static_cast<const int4*>(groups); mp.split = split_groups; mp.partials = partials;
   mp.out = out; mp.Hq = Hq; mp.Hkv = Hkv; mp.G = G; mp.q_len = q_len; mp.c2 = c2;
+  mp.out16 = nullptr; mp.stats = nullptr;
+  return launch_merge(mp, num_split, late_tables, stream);
+}
+
+static cudaError_t launch_merge(const MergeParams& mp, int32_t num_split, bool late_tables,
+                                cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)num_split, (unsigned)(Hkv * kRows));
+  cfg.gridDim = dim3((unsigned)num_split, (unsigned)(mp.Hkv * kRows));
   cfg.blockDim = dim3(32 * kMergeSlices);
   cfg.dynamicSmemBytes = 0;
   cfg.stream = stream;
@@ -1223,8 +1266,9 @@ cudaError_t launch_split_merge(const void* groups, const int32_t* split_groups,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return late_tables ? cudaLaunchKernelEx(&cfg, merge_kernel<true>, mp)
-                     : cudaLaunchKernelEx(&cfg, merge_kernel<false>, mp);
+  if (mp.out16 != nullptr) return cudaLaunchKernelEx(&cfg, merge_kernel<false, true>, mp);
+  return late_tables ? cudaLaunchKernelEx(&cfg, merge_kernel<true, false>, mp)
+                     : cudaLaunchKernelEx(&cfg, merge_kernel<false, false>, mp);
 }
 
 }  // namespace kvnvfp4

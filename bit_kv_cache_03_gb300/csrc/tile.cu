@@ -106,7 +106,8 @@ constexpr int kTbDrain = kTbOFree + 1;              // every tcgen05 op of both 
 constexpr int kTNumBars = kTbDrain + 1;
 constexpr int kTOffPid = kTOffBars + kTNumBars * 8;            // [kTStages][2] page ids or -1
 constexpr int kTOffTmemSlot = kTOffPid + kTStages * 2 * 4;
-constexpr int kTSmemBytes = kTOffTmemSlot + 16;
+constexpr int kTOffLs = kTOffTmemSlot + 16;  // fp32 row sums of the warps that share a row
+constexpr int kTSmemBytes = kTOffLs + 2 * 128 * 4;
 static_assert(kTSmemBytes <= 227 * 1024, "shared memory budget");
 static_assert(kTOffXch % 16 == 0, "16-byte accesses of the exchange area");
 
@@ -139,6 +140,11 @@ struct TileParams {
   int32_t* status;
   int32_t Hq, Hkv, G, q_len, causal;
   float c2;                // sm_scale * log2(e)
+  // attention with per-key weights: bf16 rows instead of `out`, each row's (m, 1 / l) with l the
+  // fp32 sum of the unrounded P, and l per partial row
+  uint16_t* out16;         // [num_seqs * q_len][Hq][128]
+  float2* stats;           // [num_seqs][Hkv][G * q_len]
+  float* part_l;           // [num_partials][128]
 };
 
 struct TSeg {
@@ -498,7 +504,12 @@ __device__ __forceinline__ void t_scale_o32(uint32_t taddr, float alpha) {
   tmem_st32(taddr, o);
 }
 
-template <bool kDup>
+//
+// kAcc (attention with per-key weights): each thread also sums its P in fp32 before they are rounded
+// to f16. The output keeps the tensor core's sum of the rounded P (numerator and denominator then
+// round alike), but a key's weight is computed from its unrounded P, and against the rounded sum
+// every weight of a row would be off by up to 2^-12.
+template <bool kDup, bool kAcc>
 __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, int warp,
                           int lane) {
   constexpr int kNc = kDup ? 32 : 64;  // keys of each block that one warp takes
@@ -536,6 +547,7 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
     // largest visible key position of this row (-1: no key)
     const int limit = row_ok ? (p.causal ? sg.len - p.q_len + gr / p.G : sg.len - 1) : -1;
     float m = -INFINITY;
+    float ls = 0.f;  // kAcc: this thread's sum of the row's P
     // this warp's page of each block is skipped (its keys masked) when its id lies outside the
     // pool, as the producer skips it; the id is read from the block table one block ahead, so that
     // the block loop touches no shared-memory barrier but the S-full and P-full ones
@@ -608,12 +620,18 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
         // taken as 0)
         const float mc2 = m == -INFINITY ? 0.f : m * c2;
         uint32_t pk[kNc / 2];
+        float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < kNc; c += 2) {
           const float p0 = fast_exp2(fmaf(__uint_as_float(sv[c]), c2, -mc2));
           const float p1 = fast_exp2(fmaf(__uint_as_float(sv[c + 1]), c2, -mc2));
           pk[c >> 1] = pack_f16x2(p0, p1);
+          if (kAcc) {
+            l4[c & 2] += p0;
+            l4[(c & 2) + 1] += p1;
+          }
         }
+        if (kAcc) ls = fmaf(ls, alpha, (l4[0] + l4[1]) + (l4[2] + l4[3]));
         if constexpr (kDup) {
           tmem_st16(scol, pk);
           // zeros over the same keys of the other page (columns no warp of this quadrant reads)
@@ -680,7 +698,15 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
         }
         named_barrier_sync(nb_row, kRowThreads);
       }
+      float* lsum = reinterpret_cast<float*>(smem + kTOffLs);
+      if (kAcc) {  // [warps of a row][rows]; read below, rewritten a segment (and a barrier) later
+        lsum[kDup ? (2 * pg + h) * 64 + rr : h * 128 + rr] = ls;
+        named_barrier_sync(nb_row, kRowThreads);
+      }
       if (!kDup || q < 2) {
+        if (kAcc)
+          ls = kDup ? (lsum[rr] + lsum[64 + rr]) + (lsum[128 + rr] + lsum[192 + rr])
+                    : lsum[rr] + lsum[128 + rr];
         uint32_t o8[8];
         tmem_ld8(ocol + 128, o8);
         tmem_wait_ld_regs(o8);
@@ -711,6 +737,10 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
                 dst[e >> 2] = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+            } else if (kAcc) {
+              uint16_t* dst = p.out16 + (((int64_t)sg.seq * p.q_len + tok) * p.Hq + qh) * 128 + 32 * cc;
+              store_bf16x16(dst, reinterpret_cast<const float(&)[16]>(ov[0]), inv);
+              store_bf16x16(dst + 16, reinterpret_cast<const float(&)[16]>(ov[16]), inv);
             } else if (l > 0.f) {
               float4* dst = reinterpret_cast<float4*>(orow + 32 * cc);
 #pragma unroll
@@ -723,6 +753,10 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
         if (row_ok && split && h == 0) {
           part[kTRows * 128 + rr] = m;
           part[kTRows * 128 + kTRows + rr] = l;
+          if (kAcc) p.part_l[(int64_t)sg.part * kTRows + rr] = ls;
+        } else if (kAcc && row_ok && h == 0) {
+          p.stats[((int64_t)sg.seq * p.Hkv + sg.head) * rows_total + gr] =
+              make_float2(m, ls > 0.f ? 1.f / ls : 0.f);
         }
       }
       // the exchange area is read before the next segment's epilogue rewrites it
@@ -735,6 +769,7 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
   if (to && lane == 0) flag_status(p.status, KV_NVFP4_DEV_TIMEOUT);
 }
 
+template <bool kAcc>
 __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const TileParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -773,8 +808,8 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const TileParams p) 
   } else if (warp == kTWarpMma) {
     t_mma_qk(p, smem, tbase, lane);
   } else if (warp >= kTWarpSoft0 && warp < kTWarpDeq0) {
-    if (p.G * p.q_len <= kTRows / 2) t_softmax<true>(p, smem, tbase, warp, lane);
-    else t_softmax<false>(p, smem, tbase, warp, lane);
+    if (p.G * p.q_len <= kTRows / 2) t_softmax<true, kAcc>(p, smem, tbase, warp, lane);
+    else t_softmax<false, kAcc>(p, smem, tbase, warp, lane);
   } else if (warp < kTWarpPv) {
     t_dequant(p, smem, warp, lane);
   } else {
@@ -809,13 +844,18 @@ struct TMergeParams {
   float* out;
   int32_t Hq, G, q_len;
   float c2;
+  uint16_t* out16;         // kAcc: as in TileParams
+  float2* stats;
+  const float* part_l;
+  int32_t Hkv;
 };
 
 constexpr int kTMergeSlices = 8;
 constexpr int kTMergePerRound = 8;  // partials a slice requests at once (64 per CTA and round)
 
+template <bool kAcc>
 __global__ void __launch_bounds__(32 * kTMergeSlices, 2) tile_merge_kernel(const TMergeParams p) {
-  __shared__ float s_m[kTMergeSlices], s_l[kTMergeSlices];
+  __shared__ float s_m[kTMergeSlices], s_l[kTMergeSlices], s_w[kTMergeSlices];
   __shared__ float4 s_o[kTMergeSlices][32];
   asm volatile("griddepcontrol.launch_dependents;");
   const int gi = p.split[blockIdx.x];  // plan tables: written before the attention launch
@@ -828,12 +868,13 @@ __global__ void __launch_bounds__(32 * kTMergeSlices, 2) tile_merge_kernel(const
   const int n_seg = g1.x;
   const int slice = threadIdx.x >> 5, d4 = threadIdx.x & 31;
   const float* base = p.partials + (int64_t)g1.y * kTPartFloats;
+  const float* lbase = kAcc ? p.part_l + (int64_t)g1.y * kTRows + i : nullptr;
   // per round a slice requests its partials q = q0 + 8 u (u < 8) at once (one L2 round trip for a
   // group of up to 64 segments) and combines them with independent weights
-  float M = -INFINITY, L = 0.f;
+  float M = -INFINITY, L = 0.f, W = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int q0 = slice; q0 < n_seg; q0 += kTMergeSlices * kTMergePerRound) {
-    float mq[kTMergePerRound], lq[kTMergePerRound];
+    float mq[kTMergePerRound], lq[kTMergePerRound], wq[kTMergePerRound];
     float4 ov[kTMergePerRound];
 #pragma unroll
     for (int u = 0; u < kTMergePerRound; ++u) {
@@ -846,6 +887,7 @@ __global__ void __launch_bounds__(32 * kTMergeSlices, 2) tile_merge_kernel(const
         mq[u] = __ldcg(pq + kTRows * 128 + i);
         lq[u] = __ldcg(pq + kTRows * 128 + kTRows + i);
         ov[u] = __ldcg(reinterpret_cast<const float4*>(pq + i * 128) + d4);
+        if (kAcc) wq[u] = __ldcg(lbase + (int64_t)q * kTRows);
       }
     }
     float mn = M;
@@ -854,24 +896,26 @@ __global__ void __launch_bounds__(32 * kTMergeSlices, 2) tile_merge_kernel(const
     if (mn == -INFINITY) continue;  // no visible key for this row in any partial so far
     const float a = fast_exp2((M - mn) * p.c2);  // 0 while M is -inf
     L *= a;
+    if (kAcc) W *= a;
     O.x *= a; O.y *= a; O.z *= a; O.w *= a;
 #pragma unroll
     for (int u = 0; u < kTMergePerRound; ++u) {
       if (mq[u] == -INFINITY) continue;  // a segment with no visible key for this row
       const float f = fast_exp2((mq[u] - mn) * p.c2);
       L += f * lq[u];
+      if (kAcc) W += f * wq[u];
       O.x += f * ov[u].x; O.y += f * ov[u].y; O.z += f * ov[u].z; O.w += f * ov[u].w;
     }
     M = mn;
   }
   s_o[slice][d4] = O;
-  if (d4 == 0) { s_m[slice] = M; s_l[slice] = L; }
+  if (d4 == 0) { s_m[slice] = M; s_l[slice] = L; s_w[slice] = W; }
   __syncthreads();
   if (slice == 0) {
     float Mt = s_m[0];
 #pragma unroll
     for (int j = 1; j < kTMergeSlices; ++j) Mt = fmaxf(Mt, s_m[j]);
-    float Lt = 0.f;
+    float Lt = 0.f, Wt = 0.f;
     float4 Ot = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < kTMergeSlices; ++j) {
@@ -879,9 +923,19 @@ __global__ void __launch_bounds__(32 * kTMergeSlices, 2) tile_merge_kernel(const
       const float f = fast_exp2((s_m[j] - Mt) * p.c2);
       const float4 v = s_o[j][d4];
       Lt += f * s_l[j];
+      if (kAcc) Wt += f * s_w[j];
       Ot.x += f * v.x; Ot.y += f * v.y; Ot.z += f * v.z; Ot.w += f * v.w;
     }
-    if (Lt > 0.f) {
+    if (kAcc) {
+      const int tok = r / p.G, qh = head * p.G + r % p.G;
+      const float inv = Lt > 0.f ? 1.f / Lt : 0.f;
+      *reinterpret_cast<uint2*>(
+          p.out16 + (((int64_t)g0.x * p.q_len + tok) * p.Hq + qh) * 128 + 4 * d4) =
+          make_uint2(pack_bf16x2(Ot.x * inv, Ot.y * inv), pack_bf16x2(Ot.z * inv, Ot.w * inv));
+      if (d4 == 0)
+        p.stats[((int64_t)g0.x * p.Hkv + head) * (p.G * p.q_len) + r] =
+            make_float2(Mt, Wt > 0.f ? 1.f / Wt : 0.f);
+    } else if (Lt > 0.f) {
       const int tok = r / p.G, qh = head * p.G + r % p.G;
       float4* dst = reinterpret_cast<float4*>(
           p.out + (((int64_t)g0.x * p.q_len + tok) * p.Hq + qh) * 128 + 4 * d4);
@@ -902,16 +956,18 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
                         const void* groups, const void* segments, const int32_t* cta_seg,
                         const int32_t* split_groups, int32_t num_split, float* partials,
                         float* out, int32_t* status, int32_t Hq, int32_t Hkv, int32_t q_len,
-                        int32_t causal, int32_t grid, float sm_scale, cudaStream_t stream) {
+                        int32_t causal, int32_t grid, float sm_scale, uint16_t* out16,
+                        float2* stats, float* part_l, cudaStream_t stream) {
   // the attribute belongs to each device: set once per device
   static bool attr_done[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
   if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(tile_kernel,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kTSmemBytes);
-    if (e != cudaSuccess) return e;
+    for (const void* kf : {(const void*)tile_kernel<false>, (const void*)tile_kernel<true>}) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(kf, cudaFuncAttributeMaxDynamicSharedMemorySize, kTSmemBytes);
+      if (e != cudaSuccess) return e;
+    }
     if (dev >= 0 && dev < 64) attr_done[dev] = true;
   }
   if (Hkv < 1) return cudaErrorInvalidValue;
@@ -924,6 +980,7 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
   p.partials = partials; p.out = out; p.status = status;
   p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.q_len = q_len; p.causal = causal;
   p.c2 = sm_scale * 1.4426950408889634f;
+  p.out16 = out16; p.stats = stats; p.part_l = part_l;
   if (grid <= 0) return cudaSuccess;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -936,7 +993,8 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t le = cudaLaunchKernelEx(&cfg, tile_kernel, p);
+    const cudaError_t le = out16 ? cudaLaunchKernelEx(&cfg, tile_kernel<true>, p)
+                                 : cudaLaunchKernelEx(&cfg, tile_kernel<false>, p);
     if (le != cudaSuccess) return le;
   }
   cudaError_t e = cudaGetLastError();
@@ -944,6 +1002,7 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
   TMergeParams mp;
   mp.groups = p.groups; mp.split = split_groups; mp.partials = partials; mp.out = out;
   mp.Hq = Hq; mp.G = p.G; mp.q_len = q_len; mp.c2 = p.c2;
+  mp.out16 = out16; mp.stats = stats; mp.part_l = part_l; mp.Hkv = Hkv;
   const int rows_total = p.G * q_len;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)num_split, (unsigned)(rows_total < kTRows ? rows_total : kTRows));
@@ -952,7 +1011,8 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tile_merge_kernel, mp);
+  return out16 ? cudaLaunchKernelEx(&cfg, tile_merge_kernel<true>, mp)
+               : cudaLaunchKernelEx(&cfg, tile_merge_kernel<false>, mp);
 }
 
 }  // namespace kvnvfp4

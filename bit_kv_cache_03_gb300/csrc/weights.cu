@@ -1,0 +1,434 @@
+// The weight pass of kv_nvfp4_decode_attn_weights: what every query row of the call gave to each
+// key, summed per key. The attention kernel before it (decode.cu or tile.cu) leaves each row's
+// softmax statistics (m, 1 / l); with them a key's weight needs no further reduction over keys:
+//   w_out[s][h][t] = w_in[s][h][t] + sum over the rows r of (s, h) that see t of
+//                    exp2((q_r . k_t - m_r) c2) / l_r,     c2 = sm_scale log2(e).
+//
+// The scores are computed again from the K half of the cache (72 of a token's 144 bytes per KV
+// head). The product is taken transposed, keys as the M dimension: a thread owns one key (its
+// tensor-memory lane) and sums over the query rows in its own registers, in row order, so there is
+// no reduction across threads and no atomic, and the result does not depend on the launch shape.
+//
+// A CTA takes `blocks_per_cta` consecutive 128-key blocks (two pages) of one (sequence, KV head)
+// and walks all row tiles of 64 rows over each: Q.K^T by tcgen05.mma kind::mxf4nvf4, M = 128 keys,
+// N = the tile's rows (a multiple of 16 up to 64), two K = 64 instructions per tile, into one of
+// two S buffers. Roles (256 threads): warp 0 copies K pages (ring of kStages blocks), warp 1
+// issues the MMAs and owns tensor memory, warps 2, 3 lay out Q tiles (codes in the tensor core's
+// tile order, scales, statistics; ring of two, or a single tile loaded once when all rows fit one),
+// warps 4..7 sum. Two such CTAs share an SM. Every wait is bounded in time, as in the attention
+// kernels.
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "nvfp4_device.cuh"
+
+namespace kvnvfp4 {
+
+namespace {
+
+constexpr int kStages = 4;
+constexpr int kRowTile = 64;                 // query rows of a tile
+constexpr int kStScales = 8192;              // within a stage: K codes of two pages, then scales
+constexpr int kStageBytes = 8192 + 2 * 1024;
+constexpr int kQTileBytes = kRowTile * 64;
+// a Q slot: codes, scale factors [2 k-halves][32 x 16 B], -m [64], 1 / l [64]
+constexpr int kQSf = kQTileBytes, kQNegM = kQSf + 1024, kQInv = kQNegM + kRowTile * 4;
+constexpr int kQSlotBytes = kQInv + kRowTile * 4;
+
+constexpr int kOffStage = 0;
+constexpr int kOffSfk = kOffStage + kStages * kStageBytes;  // [kStages][2 k-halves][32 x 16 B]
+constexpr int kOffQ = kOffSfk + kStages * 1024;             // [2] Q slots
+constexpr int kOffBars = kOffQ + 2 * kQSlotBytes;
+constexpr int kBarKFull = 0, kBarKEmpty = kBarKFull + kStages, kBarQFull = kBarKEmpty + kStages;
+constexpr int kBarQEmpty = kBarQFull + 2, kBarSFull = kBarQEmpty + 2, kBarSEmpty = kBarSFull + 2;
+constexpr int kBarDrain = kBarSEmpty + 2, kNumBars = kBarDrain + 1;
+constexpr int kOffTmemSlot = kOffBars + kNumBars * 8;
+constexpr int kSmemBytes = kOffTmemSlot + 16;
+static_assert(kQSlotBytes % 16 == 0 && kOffBars % 8 == 0, "alignment");
+
+// tensor memory: S [2][64], K scales [2][2 k-halves][4], Q scales [2][2 k-halves][4]
+constexpr uint32_t kColS = 0, kColSfa = 128, kColSfb = 144, kTmemCols = 256;
+
+constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpQ0 = 2, kQWarps = 2, kWarpSum0 = 4;
+constexpr int kSumWarps = 4;
+constexpr int kThreads = 32 * (kWarpSum0 + kSumWarps);
+
+struct WeightParams {
+  const uint8_t* q_codes;
+  const uint8_t* q_scales;
+  const uint8_t* pool;
+  const int32_t* block_table;
+  const int4* groups;      // 2 x int4 per group, .w of the first = the sequence's length
+  const float2* stats;     // [num_seqs][Hkv][rows]: m, 1 / l
+  const float* w_in;       // [num_seqs][Hkv][w_stride], or null for zeros
+  float* w_out;
+  int64_t w_stride;
+  int32_t max_pages, num_pages;
+  int32_t groups_per_seq;
+  int32_t Hq, Hkv, G, q_len, rows, causal;
+  int32_t chunks, blocks_per_cta;  // CTAs per (sequence, KV head), blocks of each
+  int32_t* status;
+  float c2;
+};
+
+// What one CTA works on.
+struct Span {
+  int seq, head, len, b0, b1, tiles;
+  __device__ Span(const WeightParams& p) {
+    head = blockIdx.x % p.Hkv;
+    const int rest = blockIdx.x / p.Hkv;
+    seq = rest / p.chunks;
+    len = p.groups[2 * ((int64_t)seq * p.groups_per_seq)].w;
+    b0 = (rest % p.chunks) * p.blocks_per_cta;
+    b1 = min(b0 + p.blocks_per_cta, (len + 127) >> 7);
+    tiles = (p.rows + kRowTile - 1) / kRowTile;
+  }
+  // the first row tile with a row that sees the block's first key
+  __device__ int first_tile(const WeightParams& p, int b) const {
+    const int64_t t = (int64_t)b * 128 - (len - p.q_len);
+    return p.causal && t > 0 ? (int)(t * p.G / kRowTile) : 0;
+  }
+};
+
+__device__ __forceinline__ void produce_keys(const WeightParams& p, const Span& sp, uint32_t sbase,
+                                             int lane) {
+  const uint32_t bars = sbase + kOffBars;
+  const bool lone = (sp.head | 1) >= p.Hkv;  // the last head of an odd count has no partner
+  const uint32_t ksb = lone ? 512u : 1024u;
+  const int32_t* bt = p.block_table + (int64_t)sp.seq * p.max_pages;
+  const int pages = (sp.len + kPage - 1) / kPage;
+  uint32_t k = 0;
+  bool to = false;
+  for (int b = sp.b0; b < sp.b1; b += 16) {
+    const int page = 2 * b + lane;
+    const int32_t mine = page < pages ? bt[page] : -1;
+    for (int j = 0; j < 16 && b + j < sp.b1; ++j, ++k) {
+      const int32_t pid[2] = {__shfl_sync(0xffffffffu, mine, 2 * j),
+                              __shfl_sync(0xffffffffu, mine, 2 * j + 1)};
+      if (lane == 0) {
+        const uint32_t st = k % kStages, full = bars + 8 * (kBarKFull + st);
+        if (k >= kStages)
+          wait_bar_sleep(bars + 8 * (kBarKEmpty + st), ((k / kStages) - 1) & 1, to);
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (pid[q] >= 0 && pid[q] < p.num_pages) bytes += 4096u + ksb;
+        if (bytes == 0) {
+          mbar_arrive(full);
+        } else {
+          mbar_arrive_expect_tx(full, bytes);
+          const uint32_t dst = sbase + kOffStage + st * kStageBytes;
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            if (pid[q] < 0 || pid[q] >= p.num_pages) continue;
+            const uint8_t* src = p.pool + (int64_t)pid[q] * p.Hkv * 9216;
+            bulk_g2s(dst + q * 4096, src + sp.head * 4096, 4096u, full);
+            bulk_g2s(dst + kStScales + q * 1024, src + p.Hkv * 4096 + (sp.head >> 1) * 1024, ksb,
+                     full);
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+  if (lane == 0) {
+    // no copy into this CTA's shared memory may still be in flight at exit
+    for (uint32_t st = 0; st < kStages && st < k; ++st) {
+      const uint32_t last = k - 1 - ((k - 1 - st) % kStages);
+      wait_bar_sleep(bars + 8 * (kBarKFull + st), (last / kStages) & 1, to);
+    }
+    if (to) flag_status(p.status, KV_NVFP4_DEV_TIMEOUT);
+  }
+}
+
+// One row tile into a Q slot: thread i of 64 takes row i of the tile.
+__device__ __forceinline__ void load_q_tile(const WeightParams& p, const Span& sp, uint8_t* slot,
+                                            int tile, int i) {
+  const int r = tile * kRowTile + i;
+  uint4 c[4];
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch) c[ch] = make_uint4(0u, 0u, 0u, 0u);
+  uint2 sc = make_uint2(0u, 0u);
+  // a row past the last, or one that saw no key at all, adds nothing: exp2(-inf) * 0
+  float negm = -INFINITY, inv = 0.f;
+  if (r < p.rows) {
+    const int64_t qrow = ((int64_t)sp.seq * p.q_len + r / p.G) * p.Hq + sp.head * p.G + r % p.G;
+    const uint4* src = reinterpret_cast<const uint4*>(p.q_codes + qrow * kCodeBytes);
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) c[ch] = src[ch];
+    sc = *reinterpret_cast<const uint2*>(p.q_scales + qrow * kScaleBytes);
+    const float2 st = p.stats[((int64_t)sp.seq * p.Hkv + sp.head) * p.rows + r];
+    if (st.y > 0.f) {
+      negm = -st.x;
+      inv = st.y;
+    }
+  }
+#pragma unroll
+  for (int ch = 0; ch < 4; ++ch)
+    *reinterpret_cast<uint4*>(slot + (i >> 3) * 512 + ch * 128 + (i & 7) * 16) = c[ch];
+  // scale-factor rows: row i holds the 4-byte groups of tile rows i and 32 + i (and none of the
+  // rows 64 + i, 96 + i that a wider tile would have)
+#pragma unroll
+  for (int kh = 0; kh < 2; ++kh) {
+    uint32_t* d = reinterpret_cast<uint32_t*>(slot + kQSf + kh * 512 + (i & 31) * 16);
+    d[i >> 5] = kh ? sc.y : sc.x;
+    d[2 + (i >> 5)] = 0u;
+  }
+  reinterpret_cast<float*>(slot + kQNegM)[i] = negm;
+  reinterpret_cast<float*>(slot + kQInv)[i] = inv;
+}
+
+__device__ __forceinline__ void load_queries(const WeightParams& p, const Span& sp, uint8_t* smem,
+                                             int warp, int lane) {
+  const uint32_t bars = smem_u32(smem) + kOffBars;
+  const int i = (warp - kWarpQ0) * 32 + lane;
+  uint32_t k = 0;
+  bool to = false;
+  for (int b = sp.b0; b < sp.b1; ++b) {
+    for (int tile = sp.first_tile(p, b); tile < sp.tiles; ++tile, ++k) {
+      if (sp.tiles == 1 && k > 0) return;  // the one tile stays
+      const uint32_t sl = k & 1u;
+      if (k >= 2) wait_bar_sleep(bars + 8 * (kBarQEmpty + sl), ((k >> 1) - 1) & 1, to);
+      load_q_tile(p, sp, smem + kOffQ + sl * kQSlotBytes, tile, i);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (kBarQFull + sl));
+    }
+  }
+  if (to && lane == 0) flag_status(p.status, KV_NVFP4_DEV_TIMEOUT);
+}
+
+__device__ __forceinline__ void issue_products(const WeightParams& p, const Span& sp,
+                                               uint32_t sbase, uint32_t tbase, int lane) {
+  const uint32_t bars = sbase + kOffBars;
+  const bool lone = (sp.head | 1) >= p.Hkv;
+  const bool one = sp.tiles == 1;
+  const uint32_t n = one ? (uint32_t)((p.rows + 15) & ~15) : (uint32_t)kRowTile;
+  // A, B = E2M1 K-major, scale type UE4M3, M = 128
+  const uint32_t idesc = (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+  uint32_t k = 0, step = 0;
+  bool to = false;
+  for (int b = sp.b0; b < sp.b1; ++b, ++k) {
+    const uint32_t st = k % kStages;
+    const uint32_t stage = sbase + kOffStage + st * kStageBytes;
+    const uint32_t sfk = sbase + kOffSfk + st * 1024;
+    wait_bar_sleep(bars + 8 * (kBarKFull + st), (k / kStages) & 1, to);
+    // the head's K scales of both pages into the scale-factor copy's rows: row r = page 0's keys r
+    // and r + 32, then page 1's. The slot's previous reader completed before the stage was refilled
+#pragma unroll
+    for (int kh = 0; kh < 2; ++kh) {
+      uint2 v[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)  // a skipped page leaves stale scales: its keys are not counted
+        v[q] = lone ? lds64(stage + kStScales + q * 1024 + kh * 256 + lane * 8)
+                    : lds64(stage + kStScales + q * 1024 + kh * 512 + lane * 16 + (sp.head & 1) * 8);
+      sts128(sfk + kh * 512 + lane * 16, v[0].x, v[0].y, v[1].x, v[1].y);
+    }
+    fence_async_smem();
+    __syncwarp();
+    for (int tile = sp.first_tile(p, b); tile < sp.tiles; ++tile, ++step) {
+      const uint32_t buf = step & 1u, sl = one ? 0u : buf;
+      // S buffer and scale-factor columns `buf` are free once step - 2 has been read
+      if (step >= 2) wait_bar_sleep(bars + 8 * (kBarSEmpty + buf), ((step >> 1) - 1) & 1, to);
+      if (!one || step == 0)
+        wait_bar_sleep(bars + 8 * (kBarQFull + sl), one ? 0u : (step >> 1) & 1, to);
+      if (to) break;
+      if (lane == 0) {
+        tc_fence_after();
+        const uint32_t q = sbase + kOffQ + sl * kQSlotBytes;
+#pragma unroll
+        for (int kh = 0; kh < 2; ++kh) {
+          tmem_cp_32x128b_x4(tbase + kColSfa + buf * 8 + kh * 4, smem_desc(sfk + kh * 512, 16, 128));
+          tmem_cp_32x128b_x4(tbase + kColSfb + buf * 8 + kh * 4,
+                             smem_desc(q + kQSf + kh * 512, 16, 128));
+        }
+#pragma unroll
+        for (int kh = 0; kh < 2; ++kh)
+          mma_nvf4_ss(tbase + kColS + buf * kRowTile, smem_desc(stage + kh * 256, 128, 512),
+                      smem_desc(q + kh * 256, 128, 512), idesc, tbase + kColSfa + buf * 8 + kh * 4,
+                      tbase + kColSfb + buf * 8 + kh * 4, (uint32_t)kh);
+        mma_commit(bars + 8 * (kBarSFull + buf));
+        if (!one) mma_commit(bars + 8 * (kBarQEmpty + sl));
+      }
+      __syncwarp();
+    }
+    if (to) break;
+    if (lane == 0) mma_commit(bars + 8 * (kBarKEmpty + st));  // K codes and scales consumed
+    __syncwarp();
+  }
+  if (to && lane == 0) flag_status(p.status, KV_NVFP4_DEV_TIMEOUT);
+}
+
+// kMasked: only rows from r0 on see this thread's key (r0 counted within the tile).
+template <bool kMasked>
+__device__ __forceinline__ void add_rows16(const uint32_t (&s)[16], const float* negm,
+                                           const float* inv, float c2, int r0, float (&acc)[4]) {
+#pragma unroll
+  for (int c = 0; c < 16; c += 4) {
+    const float4 m4 = *reinterpret_cast<const float4*>(negm + c);
+    const float4 i4 = *reinterpret_cast<const float4*>(inv + c);
+    const float nm[4] = {m4.x, m4.y, m4.z, m4.w}, iv[4] = {i4.x, i4.y, i4.z, i4.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = fast_exp2((__uint_as_float(s[c + e]) + nm[e]) * c2);
+      if (!kMasked || c + e >= r0) acc[e] = fmaf(x, iv[e], acc[e]);
+    }
+  }
+}
+
+__device__ __forceinline__ void sum_weights(const WeightParams& p, const Span& sp, uint8_t* smem,
+                                            uint32_t tbase, int warp, int lane) {
+  const uint32_t bars = smem_u32(smem) + kOffBars;
+  const int q = warp & 3, key = 32 * q + lane;
+  const bool one = sp.tiles == 1;
+  const int cols = one ? (p.rows + 15) & ~15 : kRowTile;
+  const int32_t* bt = p.block_table + (int64_t)sp.seq * p.max_pages;
+  const int64_t wrow = ((int64_t)sp.seq * p.Hkv + sp.head) * p.w_stride;
+  const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+  uint32_t step = 0;
+  bool to = false;
+  for (int b = sp.b0; b < sp.b1; ++b) {
+    const int t = b * 128 + key;
+    const bool real = t < sp.len;
+    const int32_t pid = real ? __ldg(bt + t / kPage) : -1;
+    const bool valid = pid >= 0 && pid < p.num_pages;  // a bad page's keys got no weight
+    const float before = real && p.w_in != nullptr ? p.w_in[wrow + t] : 0.f;
+    // the first row that sees this key
+    const int64_t past = (int64_t)t - (sp.len - p.q_len);
+    const int first = p.causal && past > 0 ? (int)(past * p.G) : 0;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int tile = sp.first_tile(p, b); tile < sp.tiles; ++tile, ++step) {
+      const uint32_t buf = step & 1u;
+      const uint8_t* slot = smem + kOffQ + (one ? 0u : buf) * kQSlotBytes;
+      const float* negm = reinterpret_cast<const float*>(slot + kQNegM);
+      const float* inv = reinterpret_cast<const float*>(slot + kQInv);
+      // the tile's statistics were written before its MMAs were issued, by other threads
+      if (!one || step == 0)
+        wait_bar_sleep(bars + 8 * (kBarQFull + (one ? 0u : buf)), one ? 0u : (step >> 1) & 1, to);
+      wait_bar_sleep(bars + 8 * (kBarSFull + buf), (step >> 1) & 1, to);
+      tc_fence_after();
+      __syncwarp();
+      const int r0 = first - tile * kRowTile;
+      const bool masked = __any_sync(0xffffffffu, r0 > 0);
+      for (int c = 0; c < cols; c += 16) {
+        uint32_t s[16];
+        tmem_ld16(tbase + lane_base + kColS + buf * kRowTile + c, s);
+        tmem_wait_ld_regs16(s);
+        if (masked) add_rows16<true>(s, negm + c, inv + c, p.c2, r0 - c, acc);
+        else add_rows16<false>(s, negm + c, inv + c, p.c2, 0, acc);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bars + 8 * (kBarSEmpty + buf));
+        if (!one) mbar_arrive(bars + 8 * (kBarQEmpty + buf));
+      }
+    }
+    if (real) {
+      const float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      p.w_out[wrow + t] = valid ? before + sum : before;
+    }
+  }
+  if (to && lane == 0) flag_status(p.status, KV_NVFP4_DEV_TIMEOUT);
+}
+
+__global__ void __launch_bounds__(kThreads, 2) weight_kernel(const WeightParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t sbase = smem_u32(smem), bars = sbase + kOffBars;
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bars + 8 * (kBarKFull + s), 1);
+      mbar_init(bars + 8 * (kBarKEmpty + s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bars + 8 * (kBarQFull + b), kQWarps);
+      mbar_init(bars + 8 * (kBarQEmpty + b), 1 + kSumWarps);
+      mbar_init(bars + 8 * (kBarSFull + b), 1);
+      mbar_init(bars + 8 * (kBarSEmpty + b), kSumWarps);
+    }
+    mbar_init(bars + 8 * kBarDrain, 1);
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) tmem_alloc(sbase + kOffTmemSlot, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // a programmatic dependent of the attention kernel or its merge, which write the statistics
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(smem + kOffTmemSlot);
+  const Span sp(p);
+  if (warp == kWarpProducer) {
+    produce_keys(p, sp, sbase, lane);
+  } else if (warp == kWarpMma) {
+    issue_products(p, sp, sbase, tbase, lane);
+  } else if (warp < kWarpSum0) {
+    load_queries(p, sp, smem, warp, lane);
+  } else {
+    sum_weights(p, sp, smem, tbase, warp, lane);
+  }
+  if (warp == kWarpMma) {
+    // tensor memory is freed only once no tcgen05 op of this CTA is in flight
+    if (lane == 0) mma_commit(bars + 8 * kBarDrain);
+    __syncwarp();
+    bool to = false;
+    wait_bar_sleep(bars + 8 * kBarDrain, 0, to);
+    if (to && lane == 0) flag_status(p.status, KV_NVFP4_DEV_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kWarpMma) tmem_dealloc(tbase, kTmemCols);
+}
+
+}  // namespace
+
+cudaError_t launch_weights(const uint8_t* q_codes, const uint8_t* q_scales, const uint8_t* pool,
+                           const int32_t* block_table, int32_t max_pages, int32_t num_pages,
+                           const void* groups, int32_t groups_per_seq, int32_t num_seqs,
+                           int32_t max_seq_len, int64_t total_tokens, const float2* stats,
+                           const float* w_in, float* w_out, int64_t w_stride, int32_t Hq,
+                           int32_t Hkv, int32_t q_len, int32_t causal, float sm_scale,
+                           int32_t num_sms, int32_t* status, cudaStream_t stream) {
+  static bool attr_done[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
+  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        weight_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_done[dev] = true;
+  }
+  WeightParams p;
+  p.q_codes = q_codes; p.q_scales = q_scales; p.pool = pool; p.block_table = block_table;
+  p.groups = static_cast<const int4*>(groups); p.stats = stats;
+  p.w_in = w_in; p.w_out = w_out; p.w_stride = w_stride;
+  p.max_pages = max_pages; p.num_pages = num_pages; p.groups_per_seq = groups_per_seq;
+  p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.q_len = q_len; p.rows = p.G * q_len;
+  p.causal = causal; p.status = status;
+  p.c2 = sm_scale * 1.4426950408889634f;
+  // about four CTAs for each of the two places on every SM, so that the last ones to finish cost
+  // little, and at most 64 blocks each
+  const int64_t blocks = (total_tokens / 128 + num_seqs) * Hkv;
+  const int64_t per = blocks / ((int64_t)num_sms * 8);
+  p.blocks_per_cta = (int32_t)(per < 1 ? 1 : per > 64 ? 64 : per);
+  const int64_t most = ((int64_t)max_seq_len + 127) / 128;
+  p.chunks = (int32_t)((most + p.blocks_per_cta - 1) / p.blocks_per_cta);
+  const int64_t grid = (int64_t)p.chunks * Hkv * num_seqs;
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weight_kernel, p);
+}
+
+}  // namespace kvnvfp4

@@ -174,6 +174,24 @@ kv_nvfp4_status kv_nvfp4_append(const kv_nvfp4_layout *layout, const void *q, co
                                 uint8_t *pool, uint8_t *q_codes, uint8_t *q_scales,
                                 int32_t *d_status, void *stream);
 
+/* ---- Append at a slot other than the position -----------------------------------------------
+ * No counterpart in the pages: kv_nvfp4_append for a sequence whose cache was compacted
+ * (kv_nvfp4_evict_compact), where a token's place in the cache is no longer its position.
+ *   d_slots:        DEVICE int32 [T], the cache slot of each token: its K/V rows go to page
+ *                   block_table[seq * max_pages + slot / 64], slot slot % 64
+ *   d_positions:    DEVICE int32 [T], the angle-table row of RoPE only (>= 0)
+ * Everything else is kv_nvfp4_append's; with d_slots equal to d_positions the result is the same
+ * bit for bit. A slot outside [0, max_pages * 64) or a negative position sets
+ * KV_NVFP4_DEV_BAD_POS and skips the token. One kernel launch. */
+kv_nvfp4_status kv_nvfp4_append_slots(const kv_nvfp4_layout *layout, const void *q, const void *k,
+                                      const void *v, const int32_t *d_seq_ids,
+                                      const int32_t *d_slots, const int32_t *d_positions,
+                                      int32_t T, const float *d_rope_table, int32_t rope_max_pos,
+                                      const int32_t *d_block_table, int32_t num_seqs,
+                                      int32_t max_pages, int32_t num_pages, uint8_t *pool,
+                                      uint8_t *q_codes, uint8_t *q_scales, int32_t *d_status,
+                                      void *stream);
+
 /* ---- Page-table / split-K setup ------------------------------------------------------------
  * Sizes and builds the work list of one attention call from HOST sequence lengths (after the
  * append, i.e. including the q_len new tokens). chunk_tokens (a positive multiple of 64) is the
@@ -235,6 +253,86 @@ kv_nvfp4_status kv_nvfp4_decode_attn(const kv_nvfp4_layout *layout,
                                      float sm_scale, const uint8_t *pool, int32_t num_pages,
                                      const int32_t *d_block_table, int32_t max_pages, float *out,
                                      int32_t *d_status, void *stream);
+
+/* ---- Attention that accounts for each key's weight --------------------------------------------
+ * No counterpart in the pages: kv_nvfp4_decode_attn for a cache that is to be evicted by
+ * accumulated attention weight. Beside the output it adds, per sequence, KV head and key, the
+ * softmax probabilities that the call's query rows gave the key:
+ *   weights_out[s][h][t] = weights_in[s][h][t] + sum_r p[r][t],     0 <= t < seq_len_s
+ * over the (num_q_heads / num_kv_heads) * q_len rows r of KV head h, p as in the output's softmax
+ * (0 where the plan's causal mask hides t from r). Entries t >= seq_len_s are left as they were.
+ *   plan, d_workspace, q_codes, q_scales, sm_scale, pool, num_pages, d_block_table, max_pages:
+ *              as for kv_nvfp4_decode_attn (any plan that it takes)
+ *   d_weights_workspace, ww_bytes: DEVICE, 16-byte aligned, at least
+ *              kv_nvfp4_weights_workspace_bytes(layout, plan) bytes; belongs to the call like
+ *              d_workspace (calls that overlap on it race)
+ *   out:       DEVICE bf16 [num_seqs * q_len][num_q_heads][128], 16-byte aligned: the fp32 result
+ *              of kv_nvfp4_decode_attn rounded once to bf16. A row all of whose pages are bad
+ *              gets zeros and adds no weight.
+ *   weights_in, weights_out: DEVICE fp32 [num_seqs][num_kv_heads][weights_stride],
+ *              weights_stride >= the plan's longest sequence. weights_in null counts as zeros; it
+ *              may be weights_out itself, and must not overlap it in any other way.
+ * Probabilities and sums are fp32; the rows of a key are added in a fixed order, so equal inputs
+ * give equal weights. A bad page's keys keep their weights_in. Up to three kernel launches: the
+ * attention kernel, the merge of its split groups, the weight pass. EINVAL for a plan that is not
+ * this layout's, a null or misaligned buffer, a plan longer than max_pages * 64 or weights_stride;
+ * ENOSPACE for a second workspace that is too small. */
+kv_nvfp4_status kv_nvfp4_weights_workspace_bytes(const kv_nvfp4_layout *layout,
+                                                 const kv_nvfp4_plan_info *plan, size_t *bytes);
+kv_nvfp4_status kv_nvfp4_decode_attn_weights(
+    const kv_nvfp4_layout *layout, const kv_nvfp4_plan_info *plan, void *d_workspace,
+    void *d_weights_workspace, size_t ww_bytes, const uint8_t *q_codes, const uint8_t *q_scales,
+    float sm_scale, const uint8_t *pool, int32_t num_pages, const int32_t *d_block_table,
+    int32_t max_pages, void *out, const float *weights_in, float *weights_out,
+    int64_t weights_stride, int32_t *d_status, void *stream);
+
+/* ---- Eviction by accumulated weight ------------------------------------------------------------
+ * No counterpart in the pages. kv_nvfp4_evict_select chooses the slots of each sequence to keep;
+ * kv_nvfp4_evict_compact moves them to the front of the sequence's cache, after which the pages
+ * behind ceil(kept / 64) are free, kv_nvfp4_plan takes the kept count as the sequence's length,
+ * and kv_nvfp4_append_slots appends behind it. K rows keep the RoPE angle of their own position.
+ *
+ * Select: per sequence and KV head (per_head != 0), or per sequence with one set for all its heads
+ * (per_head == 0), the kept = min(seq_len, keep) slots that come first when ordered by
+ *   1. slots below `sink` and slots >= seq_len - recent, ahead of all others;
+ *   2. the larger weight (per_head == 0: the heads' weights added in fp32, head 0 first); -0 equals
+ *      0, NaN counts below every other value;
+ *   3. the lower slot.
+ *   weights:   DEVICE fp32 [num_seqs][num_kv_heads][weights_stride]
+ *   d_seq_lens, d_keep: DEVICE int32 [num_seqs]
+ *   d_index:   DEVICE int32 [num_seqs][num_kv_heads, or 1][index_stride]: the kept slots in
+ *              ascending order, entries from kept on left as they were
+ * A sequence with a negative length or keep, a length above weights_stride or kept above
+ * index_stride sets KV_NVFP4_DEV_BAD_POS and is skipped. One kernel launch.
+ *
+ * Compact: per sequence s and KV head h, slot j of the new cache takes the K and V row (codes and
+ * scales) of slot index[s][h][j] of the old one, for j < kept = min(seq_len, keep); the index (of
+ * head h, or the sequence's one set when per_head == 0) must ascend strictly within [0, seq_len),
+ * as evict_select's does. All other slots keep their bytes.
+ *   d_block_table: DEVICE int32 [num_seqs][max_pages], the old cache
+ *   d_dst_block_table: DEVICE int32 [num_seqs][dst_max_pages], the new one, whose first
+ *              ceil(kept / 64) pages per sequence belong to no other table row; or null (and
+ *              dst_max_pages 0): in place, in the old cache's pages. Pages shared by several rows
+ *              of d_block_table (a common prefix) must not be compacted in place.
+ *   weights:   DEVICE fp32 as above, moved in place like the rows, with 0 for kept <= t < seq_len
+ *              (ready for new tokens in those slots); or null
+ * A sequence with a negative length or keep, kept above index_stride or dst_max_pages * 64, or a
+ * length above max_pages * 64 or (with weights) weights_stride sets KV_NVFP4_DEV_BAD_POS and is
+ * skipped; so are a row whose index lies outside [0, seq_len) (BAD_POS) and one whose old or new
+ * page lies outside the pool (BAD_PAGE). One kernel launch. num_seqs = 0 does nothing. */
+kv_nvfp4_status kv_nvfp4_evict_select(const kv_nvfp4_layout *layout, const float *weights,
+                                      int64_t weights_stride, const int32_t *d_seq_lens,
+                                      const int32_t *d_keep, int32_t num_seqs, int32_t per_head,
+                                      int32_t sink, int32_t recent, int32_t *d_index,
+                                      int64_t index_stride, int32_t *d_status, void *stream);
+kv_nvfp4_status kv_nvfp4_evict_compact(const kv_nvfp4_layout *layout, const int32_t *d_index,
+                                       int64_t index_stride, int32_t per_head,
+                                       const int32_t *d_seq_lens, const int32_t *d_keep,
+                                       int32_t num_seqs, const int32_t *d_block_table,
+                                       int32_t max_pages, int32_t num_pages, uint8_t *pool,
+                                       const int32_t *d_dst_block_table, int32_t dst_max_pages,
+                                       float *weights, int64_t weights_stride, int32_t *d_status,
+                                       void *stream);
 
 /* ---- Fused decode step [NVFP4: the decode path quantises the current K/V as it runs] -----------
  * One launch doing what kv_nvfp4_append (of the step's new tokens, with Q) followed by
