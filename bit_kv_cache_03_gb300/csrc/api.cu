@@ -60,13 +60,14 @@ cudaError_t launch_weights(const uint8_t* q_codes, const uint8_t* q_scales, cons
 cudaError_t launch_evict_select(const float* weights, int64_t w_stride, const int32_t* seq_lens,
                                 const int32_t* keep, int32_t num_seqs, int32_t per_head,
                                 int32_t sink, int32_t recent, int32_t* index, int64_t index_stride,
-                                int32_t Hkv, int32_t* status, cudaStream_t stream);
+                                int32_t Hkv, int32_t num_sms, int32_t* status,
+                                cudaStream_t stream);
 cudaError_t launch_evict_compact(const int32_t* index, int64_t index_stride, int32_t per_head,
                                  const int32_t* seq_lens, const int32_t* keep, int32_t num_seqs,
                                  const int32_t* block_table, int32_t max_pages, int32_t num_pages,
                                  uint8_t* pool, const int32_t* dst_table, int32_t dst_max_pages,
-                                 float* weights, int64_t w_stride, int32_t Hkv, int32_t* status,
-                                 cudaStream_t stream);
+                                 float* weights, int64_t w_stride, int32_t Hkv, int32_t num_sms,
+                                 int32_t* status, cudaStream_t stream);
 cudaError_t launch_page_copy(bool spill, const uint8_t* src, uint8_t* dst, const int32_t* ids,
                              int32_t n, int32_t num_pages, uint32_t page_bytes, int sms,
                              int32_t* status, cudaStream_t stream);
@@ -809,7 +810,7 @@ kv_nvfp4_status kv_nvfp4_evict_select(const kv_nvfp4_layout* L, const float* wei
     return KV_NVFP4_EINVAL;
   return cuda_status(kvnvfp4::launch_evict_select(
       weights, weights_stride, d_seq_lens, d_keep, num_seqs, per_head, sink, recent, d_index,
-      index_stride, L->num_kv_heads, d_status, (cudaStream_t)stream));
+      index_stride, L->num_kv_heads, num_sms_current_device(), d_status, (cudaStream_t)stream));
 }
 
 kv_nvfp4_status kv_nvfp4_evict_compact(const kv_nvfp4_layout* L, const int32_t* d_index,
@@ -832,8 +833,8 @@ kv_nvfp4_status kv_nvfp4_evict_compact(const kv_nvfp4_layout* L, const int32_t* 
   return cuda_status(kvnvfp4::launch_evict_compact(
       d_index, index_stride, per_head, d_seq_lens, d_keep, num_seqs, d_block_table, max_pages,
       num_pages, pool, in_place ? d_block_table : d_dst_block_table,
-      in_place ? max_pages : dst_max_pages, weights, weights_stride, L->num_kv_heads, d_status,
-      (cudaStream_t)stream));
+      in_place ? max_pages : dst_max_pages, weights, weights_stride, L->num_kv_heads,
+      num_sms_current_device(), d_status, (cudaStream_t)stream));
 }
 
 kv_nvfp4_status kv_nvfp4_decode_step(const kv_nvfp4_layout* L, const kv_nvfp4_plan_info* plan,
