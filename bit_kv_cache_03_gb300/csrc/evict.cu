@@ -554,12 +554,12 @@ struct CompactParams {
 // 16-byte pieces in sectors of 32 that hold a neighbour's piece as well, its scales two words in two
 // more sectors, so a sparse choice reads about twice its bytes. At 4 x 4 sets, 16384 kept of 131072,
 // one CTA per part took 272 us.
-constexpr int kMoveThreads = 512;
+constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 8;                       // rows in flight per thread
 constexpr int kMoveMaxCluster = 8;
 constexpr int kMoveTile = kMoveThreads / 4 * kMoveRows;  // rows of a CTA per wave, codes and scales
 
-__global__ void __launch_bounds__(kMoveThreads, 2) compact_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 3) compact_kernel(const CompactParams p) {
   const uint32_t C = cluster_size(), rank = cluster_rank();
   const int parts = p.weights != nullptr ? 3 : 2;
   const int64_t unit = blockIdx.x / C;
@@ -618,51 +618,51 @@ __global__ void __launch_bounds__(kMoveThreads, 2) compact_kernel(const CompactP
                      : p.Hkv * 8704 + head * 512 + slot * 8 + 4 * (piece & 1);
   };
   const int64_t wave = (int64_t)C * kMoveTile;
-  for (int64_t j0 = 0; j0 < kept; j0 += wave) {
-    const int64_t first = j0 + (int64_t)rank * kMoveTile + (tid >> 2);
-    int32_t t[kMoveRows], to[kMoveRows], from[kMoveRows];
+  constexpr int kApart = kMoveThreads / 4;  // rows between a thread's rows
+  int64_t first = (int64_t)rank * kMoveTile + (tid >> 2);
+  int32_t t[kMoveRows], bad = 0;
+#pragma unroll
+  for (int u = 0; u < kMoveRows; ++u) t[u] = first + u * kApart < kept ? index[first + u * kApart] : -1;
+  for (int64_t j0 = 0; j0 < kept; j0 += wave, first += wave) {
+    int32_t from[kMoveRows], to[kMoveRows];
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) {
+      const bool real = first + u * kApart < kept, ok = t[u] >= 0 && t[u] < len;
+      if (real && !ok) bad |= KV_NVFP4_DEV_BAD_POS;
+      from[u] = ok ? src_table[t[u] / kPage] : -1;
+      to[u] = real && ok ? dst_table[(first + u * kApart) / kPage] : -1;
+    }
     uint4 c[kMoveRows];
     uint32_t sc[kMoveRows];
 #pragma unroll
     for (int u = 0; u < kMoveRows; ++u) {
-      const int64_t j = first + u * (kMoveThreads / 4);
-      t[u] = j < kept ? index[j] : -1;
-      to[u] = j < kept ? dst_table[j / kPage] : 0;
+      const bool real = first + u * kApart < kept && t[u] >= 0 && t[u] < len;
+      const bool ok = from[u] >= 0 && from[u] < p.num_pages && to[u] >= 0 && to[u] < p.num_pages;
+      if (real && !ok) bad |= KV_NVFP4_DEV_BAD_PAGE;
+      // a row that is already there stays; it and a skipped one read slot 0 of page 0 for nothing
+      const bool move = ok && (t[u] != first + u * kApart || from[u] != to[u]);
+      const uint8_t* src = p.pool + (move ? from[u] * block : 0);
+      const int slot = move ? t[u] % kPage : 0;
+      c[u] = *reinterpret_cast<const uint4*>(src + code_at(slot));
+      sc[u] = *reinterpret_cast<const uint32_t*>(src + scale_at(slot));
+      if (!move) to[u] = -1;
     }
 #pragma unroll
     for (int u = 0; u < kMoveRows; ++u)
-      from[u] = t[u] >= 0 && t[u] < len ? src_table[t[u] / kPage] : -1;
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      const int64_t j = first + u * (kMoveThreads / 4);
-      if (j >= kept) {
-        to[u] = -1;
-      } else if (t[u] < 0 || t[u] >= len) {
-        flag_status(p.status, KV_NVFP4_DEV_BAD_POS);
-        to[u] = -1;
-      } else if (from[u] < 0 || from[u] >= p.num_pages || to[u] < 0 || to[u] >= p.num_pages) {
-        flag_status(p.status, KV_NVFP4_DEV_BAD_PAGE);
-        to[u] = -1;
-      } else if (t[u] == j && from[u] == to[u]) {
-        to[u] = -1;  // stays where it is
-      } else {
-        const uint8_t* src = p.pool + from[u] * block;
-        c[u] = *reinterpret_cast<const uint4*>(src + code_at(t[u] % kPage));
-        if (piece < 2) sc[u] = *reinterpret_cast<const uint32_t*>(src + scale_at(t[u] % kPage));
-      }
-    }
+      t[u] = first + wave + u * kApart < kept ? index[first + wave + u * kApart] : -1;
     // the wave is read whole before any of its rows is written
     cluster_arrive();
     cluster_wait();
 #pragma unroll
     for (int u = 0; u < kMoveRows; ++u) {
       if (to[u] < 0) continue;
-      const int slot = (int)((first + u * (kMoveThreads / 4)) % kPage);
+      const int slot = (int)((first + u * kApart) % kPage);
       uint8_t* dst = p.pool + to[u] * block;
       *reinterpret_cast<uint4*>(dst + code_at(slot)) = c[u];
       if (piece < 2) *reinterpret_cast<uint32_t*>(dst + scale_at(slot)) = sc[u];
     }
   }
+  if (bad != 0) flag_status(p.status, bad);
 }
 
 }  // namespace
@@ -730,7 +730,7 @@ cudaError_t launch_evict_compact(const int32_t* index, int64_t index_stride, int
   // no more CTAs than run at once
   const int64_t units = (int64_t)num_seqs * Hkv * (weights != nullptr ? 3 : 2);
   int64_t C = 1;
-  while (C < kMoveMaxCluster && C * kMoveTile < index_stride && units * C * 2 <= 2 * (int64_t)num_sms)
+  while (C < kMoveMaxCluster && C * kMoveTile < index_stride && units * C * 2 <= 3 * (int64_t)num_sms)
     C *= 2;
   if (units * C > 0x7FFFFFFF) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1];
