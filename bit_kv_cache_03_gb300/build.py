@@ -13,7 +13,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(BUILD, "libkvnvfp4.so")
 SOURCES = ["api.cu", "append.cu", "decode.cu", "tile.cu", "decode_noalloc.cu", "spill.cu",
            "compare.cu", "host_step.cu", "weights.cu", "evict.cu"]
-HEADERS = ["nvfp4_device.cuh"]
+HEADERS = ["nvfp4_device.cuh", "accounts.cuh"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 

@@ -29,7 +29,14 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
                           const uint16_t* v_new, const float* rope, int32_t rope_max_pos,
                           int32_t rot_dim, uint8_t* pool_w, uint8_t* q_codes_out,
                           uint8_t* q_scales_out, bool late_tables, uint16_t* out16, float2* stats,
-                          cudaStream_t stream);
+                          float* scores, cudaStream_t stream);
+cudaError_t launch_merge_weights(const void* groups, const int32_t* split_groups,
+                                 int32_t num_split, const float* partials, uint16_t* out16,
+                                 const float2* stats, const float* scores, const float* w_in,
+                                 float* w_out, int64_t w_stride, int32_t num_seqs,
+                                 int32_t max_seq_len, int64_t total_tokens,
+                                 int32_t num_sms, int32_t Hq, int32_t Hkv, int32_t q_len,
+                                 float sm_scale, cudaStream_t stream);
 int cmp_chunk_bytes(int fmt);
 cudaError_t launch_cmp_append(int fmt, const uint16_t* q, const uint16_t* k, const uint16_t* v,
                               const int32_t* seq_ids, const int32_t* positions, int64_t T,
@@ -49,7 +56,15 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
                         const int32_t* split_groups, int32_t num_split, float* partials,
                         float* out, int32_t* status, int32_t Hq, int32_t Hkv, int32_t q_len,
                         int32_t causal, int32_t grid, float sm_scale, uint16_t* out16,
-                        float2* stats, float* part_l, cudaStream_t stream);
+                        float2* stats, float* part_l, float* scores, cudaStream_t stream);
+cudaError_t launch_tile_merge_weights(const void* groups, const int32_t* split_groups,
+                                      int32_t num_split, const float* partials,
+                                      const float* part_l, uint16_t* out16, float2* stats,
+                                      const float* scores, const float* w_in, float* w_out,
+                                      int64_t w_stride, int32_t num_seqs, int32_t max_seq_len, int64_t total_tokens,
+                                 int32_t num_sms,
+                                      int32_t Hq, int32_t Hkv, int32_t q_len, float sm_scale,
+                                      cudaStream_t stream);
 cudaError_t launch_weights(const uint8_t* q_codes, const uint8_t* q_scales, const uint8_t* pool,
                            const int32_t* block_table, int32_t max_pages, int32_t num_pages,
                            const void* groups, int32_t groups_per_seq, int32_t num_seqs,
@@ -288,11 +303,14 @@ kv_nvfp4_status plan_build(const kv_nvfp4_layout* L, const int32_t* h_seq_lens, 
   pb->split.clear();
   for (int64_t gi = 0; gi < n_groups; ++gi)
     if (seg_count[(size_t)gi] > 1) pb->split.push_back((int32_t)gi);
+  int64_t page0 = 0;  // pages of the groups before; 0 in every group when they pass 31 bits
   for (int64_t gi = 0; gi < n_groups; ++gi) {
     const int64_t rg = gi % n_rg, pr = (gi / n_rg) % n_pairs, s = gi / (n_rg * n_pairs);
     int32_t* g = &pb->groups[(size_t)gi * 8];
     g[0] = (int32_t)s; g[1] = (int32_t)pr; g[2] = (int32_t)rg; g[3] = h_seq_lens[s];
-    g[4] = seg_count[(size_t)gi]; g[5] = first_part[(size_t)gi]; g[6] = gpages[(size_t)gi]; g[7] = 0;
+    g[4] = seg_count[(size_t)gi]; g[5] = first_part[(size_t)gi]; g[6] = gpages[(size_t)gi];
+    g[7] = total_pages <= 0x7FFFFFFF ? (int32_t)page0 : 0;
+    page0 += gpages[(size_t)gi];
   }
   kv_nvfp4_plan_info* info = &pb->info;
   std::memset(info, 0, sizeof(*info));
@@ -474,7 +492,7 @@ static kv_nvfp4_status decode_step_impl(const kv_nvfp4_layout* L, const kv_nvfp4
       L->num_q_heads, L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
       (const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, d_rope_table, rope_max_pos,
       L->rot_dim, pool, q_codes_out, q_scales_out, late_tables, nullptr, nullptr,
-      (cudaStream_t)stream);
+      nullptr, (cudaStream_t)stream);
   return cuda_status(e);
 }
 
@@ -513,15 +531,22 @@ static bool plan_matches(const kv_nvfp4_layout* L, const kv_nvfp4_plan_info* pla
   const int64_t rows = (int64_t)(L->num_q_heads / L->num_kv_heads) * plan->q_len;
   const bool tile = tile_mode(L, plan->q_len);
   const int64_t tile_rows = tile ? kTileRows : kRowsPerItem;
+  // the stored scores of few rows are found by the groups' page0, which has 31 bits
+  if (rows <= kRowsPerItem && plan->total_pages > 0x7FFFFFFF) return false;
   return plan->num_row_groups == (rows + tile_rows - 1) / tile_rows &&
          plan->num_groups ==
              (int64_t)plan->num_seqs * plan->num_row_groups * (tile ? L->num_kv_heads : 1);
 }
 
-// The second workspace of kv_nvfp4_decode_attn_weights: each row's softmax statistics, and on the
-// tile kernel the fp32 row sums of the split groups' partials.
+// The second workspace of kv_nvfp4_decode_attn_weights: each row's softmax statistics, on the tile
+// kernel the fp32 row sums of the split groups' partials, and the scores where they are stored.
+//
+// With at most 8 rows per KV head the attention kernel stores its scores for the weights (8 bytes
+// of traffic per row and key), with more the weight pass computes them again from K (72 bytes per
+// key whatever the rows). 4 x 131072 tokens, 6 rows per head: 124 us with the weight pass.
 struct WeightsWorkspace {
-  uint64_t off_stats, off_part_l, bytes;
+  uint64_t off_stats, off_part_l, off_scores, bytes;
+  bool scores;
 };
 static WeightsWorkspace weights_workspace(const kv_nvfp4_layout* L, const kv_nvfp4_plan_info* plan) {
   WeightsWorkspace w;
@@ -529,8 +554,13 @@ static WeightsWorkspace weights_workspace(const kv_nvfp4_layout* L, const kv_nvf
   w.off_stats = 0;
   w.off_part_l = align_up(8 * rows, 256);
   w.bytes = w.off_part_l;
-  if (tile_mode(L, plan->q_len))
-    w.bytes += align_up((uint64_t)plan->num_partials * kTileRows * 4, 256);
+  const bool tile = tile_mode(L, plan->q_len);
+  if (tile) w.bytes += align_up((uint64_t)plan->num_partials * kTileRows * 4, 256);
+  const uint64_t head_rows = (uint64_t)plan->q_len * (L->num_q_heads / L->num_kv_heads);
+  w.scores = head_rows <= kRowsPerItem;
+  w.off_scores = w.bytes;
+  if (w.scores)
+    w.bytes += (uint64_t)plan->total_pages * (tile ? 1 : L->num_kv_heads) * head_rows * 256;
   return w;
 }
 
@@ -723,7 +753,7 @@ kv_nvfp4_status kv_nvfp4_decode_attn(const kv_nvfp4_layout* L, const kv_nvfp4_pl
                              (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
                              (float*)(ws + plan->off_partials), out, d_status, L->num_q_heads,
                              L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
-                             nullptr, nullptr, nullptr, (cudaStream_t)stream);
+                             nullptr, nullptr, nullptr, nullptr, (cudaStream_t)stream);
   } else {
     e = kvnvfp4::launch_decode(
         q_codes, q_scales, pool, d_block_table, max_pages, num_pages, ws + plan->off_groups,
@@ -732,7 +762,7 @@ kv_nvfp4_status kv_nvfp4_decode_attn(const kv_nvfp4_layout* L, const kv_nvfp4_pl
         (float*)(ws + plan->off_partials), out, d_status,
         L->num_q_heads, L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
         nullptr, nullptr, nullptr, nullptr, 0, 0, nullptr, nullptr, nullptr, false, nullptr,
-        nullptr, (cudaStream_t)stream);
+        nullptr, nullptr, (cudaStream_t)stream);
   }
   return cuda_status(e);
 }
@@ -769,6 +799,7 @@ kv_nvfp4_status kv_nvfp4_decode_attn_weights(
   char* ws = (char*)d_workspace;
   char* ww = (char*)d_weights_workspace;
   float2* stats = (float2*)(ww + w.off_stats);
+  float* scores = w.scores ? (float*)(ww + w.off_scores) : nullptr;
   const bool tile = tile_mode(L, plan->q_len);
   cudaError_t e;
   if (tile) {
@@ -778,8 +809,15 @@ kv_nvfp4_status kv_nvfp4_decode_attn_weights(
                              (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
                              (float*)(ws + plan->off_partials), nullptr, d_status, L->num_q_heads,
                              L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
-                             (uint16_t*)out, stats, (float*)(ww + w.off_part_l),
+                             (uint16_t*)out, stats, (float*)(ww + w.off_part_l), scores,
                              (cudaStream_t)stream);
+    if (e == cudaSuccess && scores != nullptr)
+      e = kvnvfp4::launch_tile_merge_weights(
+          ws + plan->off_groups, (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
+          (const float*)(ws + plan->off_partials), (const float*)(ww + w.off_part_l),
+          (uint16_t*)out, stats, scores, weights_in, weights_out, weights_stride, plan->num_seqs,
+          plan->max_seq_len, plan->total_kv_tokens, num_sms, L->num_q_heads, L->num_kv_heads, plan->q_len, sm_scale,
+          (cudaStream_t)stream);
   } else {
     e = kvnvfp4::launch_decode(
         q_codes, q_scales, pool, d_block_table, max_pages, num_pages, ws + plan->off_groups,
@@ -787,9 +825,15 @@ kv_nvfp4_status kv_nvfp4_decode_attn_weights(
         (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
         (float*)(ws + plan->off_partials), nullptr, d_status, L->num_q_heads, L->num_kv_heads,
         plan->q_len, plan->causal, plan->grid, sm_scale, nullptr, nullptr, nullptr, nullptr, 0, 0,
-        nullptr, nullptr, nullptr, false, (uint16_t*)out, stats, (cudaStream_t)stream);
+        nullptr, nullptr, nullptr, false, (uint16_t*)out, stats, scores, (cudaStream_t)stream);
+    if (e == cudaSuccess && scores != nullptr)
+      e = kvnvfp4::launch_merge_weights(
+          ws + plan->off_groups, (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
+          (const float*)(ws + plan->off_partials), (uint16_t*)out, stats, scores, weights_in,
+          weights_out, weights_stride, plan->num_seqs, plan->max_seq_len, plan->total_kv_tokens, num_sms, L->num_q_heads,
+          L->num_kv_heads, plan->q_len, sm_scale, (cudaStream_t)stream);
   }
-  if (e != cudaSuccess) return cuda_status(e);
+  if (e != cudaSuccess || scores != nullptr) return cuda_status(e);
   return cuda_status(kvnvfp4::launch_weights(
       q_codes, q_scales, pool, d_block_table, max_pages, num_pages, ws + plan->off_groups,
       plan->num_groups / plan->num_seqs, plan->num_seqs, plan->max_seq_len, plan->total_kv_tokens,

@@ -44,6 +44,7 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "accounts.cuh"
 #include "nvfp4_device.cuh"
 
 namespace kvnvfp4 {
@@ -122,7 +123,7 @@ struct DecodeParams {
   const int32_t* block_table;
   int32_t max_pages;
   int32_t num_pages;
-  const int4* groups;      // 2 x int4 per group: {seq, 0, rg, len}, {n_seg, first_part, pages, 0}
+  const int4* groups;      // 2 x int4 per group: {seq, 0, rg, len}, {n_seg, first_part, pages, page0}
   const int4* segments;    // {group, page_lo, page_hi, part_slot or -1}
   const int32_t* cta_seg;  // [grid + 1]
   float* partials;         // [num_partials][Hkv][kPartHeadFloats]
@@ -145,10 +146,11 @@ struct DecodeParams {
   // attention with per-key weights: bf16 rows instead of `out`, and each row's (m, 1 / l)
   uint16_t* out16;         // [num_seqs * q_len][Hq][128]
   float2* stats;           // [num_seqs][Hkv][G * q_len]
+  float* scores;           // [pages of all groups][Hkv][G * q_len][64 keys]
 };
 
 struct SegInfo {
-  int seq, rg, len, n_seg, first_part, lo, hi, part, group;
+  int seq, rg, len, n_seg, first_part, lo, hi, part, group, page0;
 };
 
 __device__ __forceinline__ SegInfo load_seg(const DecodeParams& p, int s) {
@@ -158,7 +160,7 @@ __device__ __forceinline__ SegInfo load_seg(const DecodeParams& p, int s) {
   SegInfo r;
   r.group = seg.x; r.lo = seg.y; r.hi = seg.z; r.part = seg.w;
   r.seq = g0.x; r.rg = g0.z; r.len = g0.w;
-  r.n_seg = g1.x; r.first_part = g1.y;
+  r.n_seg = g1.x; r.first_part = g1.y; r.page0 = g1.w;
   return r;
 }
 
@@ -390,8 +392,11 @@ __device__ __forceinline__ void s_issue(AttnCtx& c, uint32_t kk, uint32_t (&sr)[
 // update, P = exp2((s - m) c2) <= 1 in f16. Returns whether a max grew (then alpha_a and
 // alpha_b are the factors for rows 2t and 2t + 1 of the accumulator). kv_lim: keys of the page
 // below it are real (0 when the page was skipped).
-template <int NR>
+// ACC: the scores of the page's R real rows also go to `scores` (this head's [R][64] block), -inf
+// where the row does not see the key.
+template <int NR, bool ACC>
 __device__ __forceinline__ bool s_softmax(AttnCtx& c, uint32_t kk, uint32_t kst, int page, int len,
+                                          float* scores, int R,
                                           const RowVis& rv, uint32_t (&sr)[8], float (&m)[kRows],
                                           float (&lp)[kRows], uint32_t pt, int t, float c2,
                                           float& alpha_a, float& alpha_b, int& kv_lim) {
@@ -413,6 +418,13 @@ __device__ __forceinline__ bool s_softmax(AttnCtx& c, uint32_t kk, uint32_t kst,
       for (int i = 0; i < NR; ++i)
         if (kp <= __shfl_sync(0xffffffffu, rv.mylim, i)) vmask |= 1u << i;
     }
+  }
+  if (ACC) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+      if (i < R)
+        scores[i * kPage + c.key0 + c.lane] =
+            ((vmask >> i) & 1u) ? __uint_as_float(sr[i]) : -INFINITY;
   }
   float pm[NR];
 #pragma unroll
@@ -846,8 +858,11 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
       float alpha_a = 1.f, alpha_b = 1.f;
       int kv_lim = 0;
       s_issue(c, k, sr);
-      const bool grow = s_softmax<NR>(c, k, ks, sg.lo + j, sg.len, rv, sr, m, lp, ps, t, c2,
-                                      alpha_a, alpha_b, kv_lim);
+      float* scores = nullptr;  // this page's and head's block
+      if (ACC)
+        scores = p.scores + (((int64_t)sg.page0 + sg.lo + j) * p.Hkv + c.head) * rows_total * kPage;
+      const bool grow = s_softmax<NR, ACC>(c, k, ks, sg.lo + j, sg.len, scores, rows_total, rv, sr,
+                                           m, lp, ps, t, c2, alpha_a, alpha_b, kv_lim);
       __syncwarp();
       if (grow) {  // entries 0, 2: row 2t; entries 1, 3: row 2t + 1
 #pragma unroll
@@ -1051,8 +1066,7 @@ struct MergeParams {
   float* out;
   int32_t Hq, Hkv, G, q_len;
   float c2;
-  uint16_t* out16;         // ACC: bf16 rows and (m, 1 / l) per row, as in DecodeParams
-  float2* stats;
+  uint16_t* out16;         // ACC: bf16 rows, as in DecodeParams
 };
 
 constexpr int kMergeSlices = 8;
@@ -1061,15 +1075,14 @@ constexpr int kMergePerRound = 8;  // partials a slice requests at once (64 per 
 // LATE_TABLES: the plan tables were written by a kernel earlier in the same step (not by a copy
 // before the attention launch), so they are read only after the wait as well.
 template <bool LATE_TABLES, bool ACC>
-__global__ void __launch_bounds__(32 * kMergeSlices, 2) merge_kernel(const MergeParams p) {
+__device__ __forceinline__ void merge_row(const MergeParams& p, int split_index, int row) {
   __shared__ float s_m[kMergeSlices], s_l[kMergeSlices];
   __shared__ float4 s_o[kMergeSlices][32];
-  asm volatile("griddepcontrol.launch_dependents;");  // the next kernel may begin its launch
   // launched as a programmatic dependent of the attention kernel: its partials are visible only
   // after this wait (which returns when that grid has completed and flushed)
   if (LATE_TABLES) asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int gi = p.split[blockIdx.x];  // plan tables: written before the attention launch
-  const int h = blockIdx.y / kRows, i = blockIdx.y % kRows;
+  const int gi = p.split[split_index];  // plan tables: written before the attention launch
+  const int h = row / kRows, i = row % kRows;
   const int4 g0 = p.groups[2 * gi], g1 = p.groups[2 * gi + 1];
   const int r = g0.z * kRows + i;
   if (!LATE_TABLES) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1138,8 +1151,6 @@ __global__ void __launch_bounds__(32 * kMergeSlices, 2) merge_kernel(const Merge
       *reinterpret_cast<uint2*>(
           p.out16 + (((int64_t)g0.x * p.q_len + tok) * p.Hq + qh) * 128 + 4 * d4) =
           make_uint2(pack_bf16x2(Ot.x * inv, Ot.y * inv), pack_bf16x2(Ot.z * inv, Ot.w * inv));
-      if (d4 == 0)
-        p.stats[((int64_t)g0.x * p.Hkv + h) * (p.G * p.q_len) + r] = make_float2(Mt, inv);
     } else if (Lt > 0.f) {
       const int tok = r / p.G, qh = h * p.G + r % p.G;
       float4* dst = reinterpret_cast<float4*>(
@@ -1148,6 +1159,34 @@ __global__ void __launch_bounds__(32 * kMergeSlices, 2) merge_kernel(const Merge
       *dst = make_float4(Ot.x * inv, Ot.y * inv, Ot.z * inv, Ot.w * inv);
     }
   }
+}
+
+template <bool LATE_TABLES>
+__global__ void __launch_bounds__(32 * kMergeSlices, 2) merge_kernel(const MergeParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");  // the next kernel may begin its launch
+  merge_row<LATE_TABLES, false>(p, blockIdx.x, blockIdx.y);
+}
+
+// The second launch of an attention call with per-key weights: the first `merges` CTAs merge the
+// split groups' rows (as merge_kernel), the others turn the stored scores into weights. The merge
+// and the weights need only what the attention kernel wrote, so they run side by side.
+static_assert(32 * kMergeSlices == kAccThreads, "one block size for both kinds of CTA");
+__global__ void __launch_bounds__(kAccThreads, 4) merge_weights_kernel(const MergeParams p,
+                                                                       const AccountParams a,
+                                                                       int32_t merges) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  if ((int)blockIdx.x < merges) {
+    merge_row<false, true>(p, blockIdx.x / (p.Hkv * kRows), blockIdx.x % (p.Hkv * kRows));
+    return;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t stride = (int64_t)p.Hkv * kPartHeadFloats;
+  auto part = [&](int q, int head) { return p.partials + q * stride + head * kPartHeadFloats; };
+  account_chunk(
+      a, p.groups, (int)blockIdx.x - merges, p.Hkv, p.Hkv, p.c2,
+      [](int seq, int) { return (int64_t)seq; },
+      [&](int q, int head, int r) { return part(q, head) + kRows * 128 + r; },
+      [&](int q, int head, int r) { return part(q, head) + kRows * 128 + kRows + r; });
 }
 
 }  // namespace
@@ -1159,9 +1198,6 @@ cudaError_t launch_split_merge(const void* groups, const int32_t* split_groups,
                                int32_t G, int32_t q_len, float c2, int32_t num_split,
                                bool late_tables, cudaStream_t stream);
 
-static cudaError_t launch_merge(const MergeParams& mp, int32_t num_split, bool late_tables,
-                                cudaStream_t stream);
-
 cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const uint8_t* pool,
                           const int32_t* block_table, int32_t max_pages, int32_t num_pages,
                           const void* groups, const void* segments, const int32_t* cta_seg,
@@ -1172,7 +1208,7 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
                           const uint16_t* v_new, const float* rope, int32_t rope_max_pos,
                           int32_t rot_dim, uint8_t* pool_w, uint8_t* q_codes_out,
                           uint8_t* q_scales_out, bool late_tables, uint16_t* out16, float2* stats,
-                          cudaStream_t stream) {
+                          float* scores, cudaStream_t stream) {
   // the attribute belongs to each instantiation and each device: set once per device
   static bool attr_done[64] = {};
   int dev = 0;
@@ -1203,7 +1239,7 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
   p.rope_max_pos = rope_max_pos; p.rot_dim = rot_dim; p.pool_w = pool_w;
   p.q_codes_out = q_codes_out; p.q_scales_out = q_scales_out;
   p.early_tables = late_tables ? 0 : 1;
-  p.out16 = out16; p.stats = stats;
+  p.out16 = out16; p.stats = stats; p.scores = scores;
   const bool fused = q_new != nullptr;
   if (grid <= 0) return cudaSuccess;
   // programmatic dependent launch: the kernel is set up while the previous kernel on the stream
@@ -1231,12 +1267,29 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
     if (le != cudaSuccess) return le;
   }
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || num_split <= 0) return e;
+  if (e != cudaSuccess || num_split <= 0 || out16 != nullptr) return e;
+  return launch_split_merge(p.groups, split_groups, partials, out, Hq, Hkv, p.G, q_len, p.c2,
+                            num_split, late_tables, stream);
+}
+
+// The launch after launch_decode with out16: the merge of the split groups and the weights.
+cudaError_t launch_merge_weights(const void* groups, const int32_t* split_groups,
+                                 int32_t num_split, const float* partials, uint16_t* out16,
+                                 const float2* stats, const float* scores, const float* w_in,
+                                 float* w_out, int64_t w_stride, int32_t num_seqs,
+                                 int32_t max_seq_len, int64_t total_tokens,
+                                 int32_t num_sms, int32_t Hq, int32_t Hkv, int32_t q_len,
+                                 float sm_scale, cudaStream_t stream) {
   MergeParams mp;
-  mp.groups = p.groups; mp.split = split_groups; mp.partials = partials; mp.out = out;
-  mp.Hq = Hq; mp.Hkv = Hkv; mp.G = p.G; mp.q_len = q_len; mp.c2 = p.c2;
-  mp.out16 = out16; mp.stats = stats;
-  return launch_merge(mp, num_split, late_tables, stream);
+  mp.groups = static_cast<const int4*>(groups); mp.split = split_groups; mp.partials = partials;
+  mp.out = nullptr; mp.Hq = Hq; mp.Hkv = Hkv; mp.G = Hq / Hkv; mp.q_len = q_len;
+  mp.c2 = sm_scale * 1.4426950408889634f;
+  mp.out16 = out16;
+  const AccountParams a = account_params(scores, stats, w_in, w_out, w_stride, mp.G * q_len,
+                                         num_seqs, Hkv, max_seq_len, total_tokens, num_sms);
+  const int32_t merges = num_split * Hkv * kRows;
+  return launch_with_accounts(merge_weights_kernel, mp, a, merges,
+                              merges + (int64_t)num_seqs * Hkv * a.parts, stream);
 }
 
 // The split-K merge launch (also used by the comparator decode): one CTA per (split group, KV
@@ -1250,14 +1303,9 @@ cudaError_t launch_split_merge(const void* groups, const int32_t* split_groups,
   MergeParams mp;
   mp.groups = static_cast<const int4*>(groups); mp.split = split_groups; mp.partials = partials;
   mp.out = out; mp.Hq = Hq; mp.Hkv = Hkv; mp.G = G; mp.q_len = q_len; mp.c2 = c2;
-  mp.out16 = nullptr; mp.stats = nullptr;
-  return launch_merge(mp, num_split, late_tables, stream);
-}
-
-static cudaError_t launch_merge(const MergeParams& mp, int32_t num_split, bool late_tables,
-                                cudaStream_t stream) {
+  mp.out16 = nullptr;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)num_split, (unsigned)(mp.Hkv * kRows));
+  cfg.gridDim = dim3((unsigned)num_split, (unsigned)(Hkv * kRows));
   cfg.blockDim = dim3(32 * kMergeSlices);
   cfg.dynamicSmemBytes = 0;
   cfg.stream = stream;
@@ -1266,9 +1314,8 @@ static cudaError_t launch_merge(const MergeParams& mp, int32_t num_split, bool l
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (mp.out16 != nullptr) return cudaLaunchKernelEx(&cfg, merge_kernel<false, true>, mp);
-  return late_tables ? cudaLaunchKernelEx(&cfg, merge_kernel<true, false>, mp)
-                     : cudaLaunchKernelEx(&cfg, merge_kernel<false, false>, mp);
+  return late_tables ? cudaLaunchKernelEx(&cfg, merge_kernel<true>, mp)
+                     : cudaLaunchKernelEx(&cfg, merge_kernel<false>, mp);
 }
 
 }  // namespace kvnvfp4

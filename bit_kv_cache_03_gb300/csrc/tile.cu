@@ -56,6 +56,7 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "accounts.cuh"
 #include "nvfp4_device.cuh"
 
 namespace kvnvfp4 {
@@ -132,7 +133,7 @@ struct TileParams {
   const int32_t* block_table;
   int32_t max_pages;
   int32_t num_pages;
-  const int4* groups;      // 2 x int4 per group: {seq, kv head, rg, len}, {n_seg, first_part, pages, 0}
+  const int4* groups;      // 2 x int4 per group: {seq, kv head, rg, len}, {n_seg, first_part, pages, page0}
   const int4* segments;    // {group, page_lo, page_hi, part_slot or -1}
   const int32_t* cta_seg;  // [grid + 1]
   float* partials;         // [num_partials][kTPartFloats]
@@ -145,10 +146,11 @@ struct TileParams {
   uint16_t* out16;         // [num_seqs * q_len][Hq][128]
   float2* stats;           // [num_seqs][Hkv][G * q_len]
   float* part_l;           // [num_partials][128]
+  float* scores;           // [pages of all groups][G * q_len][64 keys], or null (more than 8 rows)
 };
 
 struct TSeg {
-  int seq, head, rg, len, n_seg, first_part, lo, hi, part;
+  int seq, head, rg, len, n_seg, first_part, lo, hi, part, page0;
 };
 
 __device__ __forceinline__ TSeg t_load_seg(const TileParams& p, int s) {
@@ -158,7 +160,7 @@ __device__ __forceinline__ TSeg t_load_seg(const TileParams& p, int s) {
   TSeg r;
   r.lo = seg.y; r.hi = seg.z; r.part = seg.w;
   r.seq = g0.x; r.head = g0.y; r.rg = g0.z; r.len = g0.w;
-  r.n_seg = g1.x; r.first_part = g1.y;
+  r.n_seg = g1.x; r.first_part = g1.y; r.page0 = g1.w;
   return r;
 }
 
@@ -579,6 +581,15 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
 #pragma unroll
           for (int c = 0; c < kNc; ++c) sv[c] = c < nv ? sv[c] : __float_as_uint(-INFINITY);
         }
+        if (kAcc && kDup && p.scores != nullptr && row_ok && rr < 32 && page < sg.hi) {
+          // this row's 32 scores (lanes of real rows only: at most 8)
+          float4* dst = reinterpret_cast<float4*>(
+              p.scores + (((int64_t)sg.page0 + page) * rows_total + gr) * kPage + kofs);
+#pragma unroll
+          for (int c = 0; c < kNc; c += 4)
+            dst[c >> 2] = make_float4(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]),
+                                      __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
+        }
         // this warp's max of the row: eight chains of three-input maxima, then a tree
         float mx[8];
 #pragma unroll
@@ -854,12 +865,10 @@ constexpr int kTMergeSlices = 8;
 constexpr int kTMergePerRound = 8;  // partials a slice requests at once (64 per CTA and round)
 
 template <bool kAcc>
-__global__ void __launch_bounds__(32 * kTMergeSlices, 2) tile_merge_kernel(const TMergeParams p) {
+__device__ __forceinline__ void tile_merge_row(const TMergeParams& p, int split_index, int i) {
   __shared__ float s_m[kTMergeSlices], s_l[kTMergeSlices], s_w[kTMergeSlices];
   __shared__ float4 s_o[kTMergeSlices][32];
-  asm volatile("griddepcontrol.launch_dependents;");
-  const int gi = p.split[blockIdx.x];  // plan tables: written before the attention launch
-  const int i = blockIdx.y;
+  const int gi = p.split[split_index];  // plan tables: written before the attention launch
   const int4 g0 = p.groups[2 * gi], g1 = p.groups[2 * gi + 1];
   const int r = g0.z * kTRows + i, head = g0.y;
   // the partials are visible only after the attention grid has completed and flushed
@@ -945,6 +954,31 @@ __global__ void __launch_bounds__(32 * kTMergeSlices, 2) tile_merge_kernel(const
   }
 }
 
+template <bool kAcc>
+__global__ void __launch_bounds__(32 * kTMergeSlices, 2) tile_merge_kernel(const TMergeParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  tile_merge_row<kAcc>(p, blockIdx.x, blockIdx.y);
+}
+
+// The second launch of an attention call with per-key weights and at most 8 rows per KV head: the
+// first `merges` CTAs merge the split groups' rows, the others turn the stored scores into weights.
+static_assert(32 * kTMergeSlices == kAccThreads, "one block size for both kinds of CTA");
+__global__ void __launch_bounds__(kAccThreads, 4) tile_merge_weights_kernel(const TMergeParams p,
+                                                                            const AccountParams a,
+                                                                            int32_t merges) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  if ((int)blockIdx.x < merges) {
+    tile_merge_row<true>(p, blockIdx.x / a.R, blockIdx.x % a.R);
+    return;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  account_chunk(
+      a, p.groups, (int)blockIdx.x - merges, p.Hkv, 1, p.c2,
+      [&](int seq, int head) { return (int64_t)seq * p.Hkv + head; },
+      [&](int q, int, int r) { return p.partials + (int64_t)q * kTPartFloats + kTRows * 128 + r; },
+      [&](int q, int, int r) { return p.part_l + (int64_t)q * kTRows + r; });
+}
+
 }  // namespace
 
 int tile_smem_bytes() { return kTSmemBytes; }
@@ -957,7 +991,7 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
                         const int32_t* split_groups, int32_t num_split, float* partials,
                         float* out, int32_t* status, int32_t Hq, int32_t Hkv, int32_t q_len,
                         int32_t causal, int32_t grid, float sm_scale, uint16_t* out16,
-                        float2* stats, float* part_l, cudaStream_t stream) {
+                        float2* stats, float* part_l, float* scores, cudaStream_t stream) {
   // the attribute belongs to each device: set once per device
   static bool attr_done[64] = {};
   int dev = 0;
@@ -980,7 +1014,7 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
   p.partials = partials; p.out = out; p.status = status;
   p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.q_len = q_len; p.causal = causal;
   p.c2 = sm_scale * 1.4426950408889634f;
-  p.out16 = out16; p.stats = stats; p.part_l = part_l;
+  p.out16 = out16; p.stats = stats; p.part_l = part_l; p.scores = scores;
   if (grid <= 0) return cudaSuccess;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -998,7 +1032,7 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
     if (le != cudaSuccess) return le;
   }
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || num_split <= 0) return e;
+  if (e != cudaSuccess || num_split <= 0 || scores != nullptr) return e;
   TMergeParams mp;
   mp.groups = p.groups; mp.split = split_groups; mp.partials = partials; mp.out = out;
   mp.Hq = Hq; mp.G = p.G; mp.q_len = q_len; mp.c2 = p.c2;
@@ -1013,6 +1047,27 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
   cfg.numAttrs = 1;
   return out16 ? cudaLaunchKernelEx(&cfg, tile_merge_kernel<true>, mp)
                : cudaLaunchKernelEx(&cfg, tile_merge_kernel<false>, mp);
+}
+
+// The launch after launch_tile with scores: the merge of the split groups and the weights.
+cudaError_t launch_tile_merge_weights(const void* groups, const int32_t* split_groups,
+                                      int32_t num_split, const float* partials,
+                                      const float* part_l, uint16_t* out16, float2* stats,
+                                      const float* scores, const float* w_in, float* w_out,
+                                      int64_t w_stride, int32_t num_seqs, int32_t max_seq_len, int64_t total_tokens,
+                                 int32_t num_sms,
+                                      int32_t Hq, int32_t Hkv, int32_t q_len, float sm_scale,
+                                      cudaStream_t stream) {
+  TMergeParams mp;
+  mp.groups = static_cast<const int4*>(groups); mp.split = split_groups; mp.partials = partials;
+  mp.out = nullptr; mp.Hq = Hq; mp.G = Hq / Hkv; mp.q_len = q_len;
+  mp.c2 = sm_scale * 1.4426950408889634f;
+  mp.out16 = out16; mp.stats = stats; mp.part_l = part_l; mp.Hkv = Hkv;
+  const AccountParams a = account_params(scores, stats, w_in, w_out, w_stride, mp.G * q_len,
+                                         num_seqs, Hkv, max_seq_len, total_tokens, num_sms);
+  const int32_t merges = num_split * a.R;
+  return launch_with_accounts(tile_merge_weights_kernel, mp, a, merges,
+                              merges + (int64_t)num_seqs * Hkv * a.parts, stream);
 }
 
 }  // namespace kvnvfp4

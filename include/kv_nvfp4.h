@@ -208,8 +208,9 @@ kv_nvfp4_status kv_nvfp4_plan_workspace_bytes(const kv_nvfp4_layout *layout,
 /* Host-only variant of kv_nvfp4_plan for a given CTA count: writes the image of the workspace
  * tables (groups, segments, per-CTA segment ranges, split-group list; everything before
  * info->off_partials) into HOST memory h_workspace and fills *info. No CUDA call. Layout of the
- * image: groups are 8 int32 {seq, pair, row_tile, seq_len, n_segments, first_partial, pages, 0}
- * (pair = 0 for 8-row tiles, which cover every KV head);
+ * image: groups are 8 int32 {seq, pair, row_tile, seq_len, n_segments, first_partial, pages, page0}
+ * (pair = 0 for 8-row tiles, which cover every KV head; page0: pages of the groups before, or 0 in
+ * every group when info->total_pages passes 31 bits);
  * segments are 4 int32 {group, page_lo, page_hi, partial or -1}; CTA b owns segments
  * [cta[b], cta[b+1]); the split list holds info->num_split_groups group indices in order. */
 kv_nvfp4_status kv_nvfp4_plan_host(const kv_nvfp4_layout *layout, const int32_t *h_seq_lens,
