@@ -10,12 +10,12 @@
 // no reduction across threads and no atomic, and the result does not depend on the launch shape.
 //
 // A CTA takes `blocks_per_cta` consecutive 128-key blocks (two pages) of one (sequence, KV head)
-// and walks all row tiles of 64 rows over each: Q.K^T by tcgen05.mma kind::mxf4nvf4, M = 128 keys,
-// N = the tile's rows (a multiple of 16 up to 64), two K = 64 instructions per tile, into one of
+// and walks all row tiles of 48 rows over each: Q.K^T by tcgen05.mma kind::mxf4nvf4, M = 128 keys,
+// N = the tile's rows (a multiple of 16 up to 48), two K = 64 instructions per tile, into one of
 // two S buffers. Roles (256 threads): warp 0 copies K pages (ring of kStages blocks), warp 1
 // issues the MMAs and owns tensor memory, warps 2, 3 lay out Q tiles (codes in the tensor core's
 // tile order, scales, statistics; ring of two, or a single tile loaded once when all rows fit one),
-// warps 4..7 sum. Two such CTAs share an SM. Every wait is bounded in time, as in the attention
+// warps 4..7 sum. Four such CTAs share an SM, so that sixteen warps keep its exponential units busy. Every wait is bounded in time, as in the attention
 // kernels.
 
 #include <cstdint>
@@ -28,11 +28,11 @@ namespace kvnvfp4 {
 namespace {
 
 constexpr int kStages = 4;
-constexpr int kRowTile = 64;                 // query rows of a tile
+constexpr int kRowTile = 48;                 // query rows of a tile
 constexpr int kStScales = 8192;              // within a stage: K codes of two pages, then scales
 constexpr int kStageBytes = 8192 + 2 * 1024;
 constexpr int kQTileBytes = kRowTile * 64;
-// a Q slot: codes, scale factors [2 k-halves][32 x 16 B], -m [64], 1 / l [64]
+// a Q slot: codes, scale factors [2 k-halves][32 x 16 B], -m c2 [48], 1 / l [48]
 constexpr int kQSf = kQTileBytes, kQNegM = kQSf + 1024, kQInv = kQNegM + kRowTile * 4;
 constexpr int kQSlotBytes = kQInv + kRowTile * 4;
 
@@ -45,12 +45,15 @@ constexpr int kBarQEmpty = kBarQFull + 2, kBarSFull = kBarQEmpty + 2, kBarSEmpty
 constexpr int kBarDrain = kBarSEmpty + 2, kNumBars = kBarDrain + 1;
 constexpr int kOffTmemSlot = kOffBars + kNumBars * 8;
 constexpr int kSmemBytes = kOffTmemSlot + 16;
-static_assert(kQSlotBytes % 16 == 0 && kOffBars % 8 == 0, "alignment");
+static_assert(kQTileBytes % 16 == 0 && kQSlotBytes % 16 == 0 && kOffBars % 8 == 0, "alignment");
 
-// tensor memory: S [2][64], K scales [2][2 k-halves][4], Q scales [2][2 k-halves][4]
-constexpr uint32_t kColS = 0, kColSfa = 128, kColSfb = 144, kTmemCols = 256;
+// tensor memory: S [2][48], K scales [2][2 k-halves][4], Q scales [2][2 k-halves][4]: 128 columns, so
+// that four CTAs share the 512 of an SM
+constexpr uint32_t kColS = 0, kColSfa = 96, kColSfb = 112, kTmemCols = 128;
+constexpr int kCtasPerSm = 4;
+static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of four CTAs");
 
-constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpQ0 = 2, kQWarps = 2, kWarpSum0 = 4;
+constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpQ0 = 2, kWarpSum0 = 4;
 constexpr int kSumWarps = 4;
 constexpr int kThreads = 32 * (kWarpSum0 + kSumWarps);
 
@@ -142,61 +145,88 @@ __device__ __forceinline__ void produce_keys(const WeightParams& p, const Span& 
   }
 }
 
-// One row tile into a Q slot: thread i of 64 takes row i of the tile.
-__device__ __forceinline__ void load_q_tile(const WeightParams& p, const Span& sp, uint8_t* slot,
-                                            int tile, int i) {
-  const int r = tile * kRowTile + i;
-  uint4 c[4];
+// The rows lane and lane + 32 of a row tile (48 rows: the upper half of the lanes has one).
+struct QRows {
+  uint4 c[2][4];
+  uint2 sc[2];
+  float2 st[2];
+};
+
+__device__ __forceinline__ void fetch_q_tile(const WeightParams& p, const Span& sp, int tile,
+                                             int lane, QRows& q) {
 #pragma unroll
-  for (int ch = 0; ch < 4; ++ch) c[ch] = make_uint4(0u, 0u, 0u, 0u);
-  uint2 sc = make_uint2(0u, 0u);
-  // a row past the last, or one that saw no key at all, adds nothing: exp2(-inf) * 0
-  float negm = -INFINITY, inv = 0.f;
-  if (r < p.rows) {
+  for (int u = 0; u < 2; ++u) {
+    const int i = lane + 32 * u, r = tile * kRowTile + i;
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) q.c[u][ch] = make_uint4(0u, 0u, 0u, 0u);
+    q.sc[u] = make_uint2(0u, 0u);
+    q.st[u] = make_float2(0.f, 0.f);
+    if (i >= kRowTile || r >= p.rows) continue;
     const int64_t qrow = ((int64_t)sp.seq * p.q_len + r / p.G) * p.Hq + sp.head * p.G + r % p.G;
     const uint4* src = reinterpret_cast<const uint4*>(p.q_codes + qrow * kCodeBytes);
 #pragma unroll
-    for (int ch = 0; ch < 4; ++ch) c[ch] = src[ch];
-    sc = *reinterpret_cast<const uint2*>(p.q_scales + qrow * kScaleBytes);
-    const float2 st = p.stats[((int64_t)sp.seq * p.Hkv + sp.head) * p.rows + r];
-    if (st.y > 0.f) {
-      negm = -st.x;
-      inv = st.y;
-    }
+    for (int ch = 0; ch < 4; ++ch) q.c[u][ch] = src[ch];
+    q.sc[u] = *reinterpret_cast<const uint2*>(p.q_scales + qrow * kScaleBytes);
+    q.st[u] = p.stats[((int64_t)sp.seq * p.Hkv + sp.head) * p.rows + r];
   }
-#pragma unroll
-  for (int ch = 0; ch < 4; ++ch)
-    *reinterpret_cast<uint4*>(slot + (i >> 3) * 512 + ch * 128 + (i & 7) * 16) = c[ch];
-  // scale-factor rows: row i holds the 4-byte groups of tile rows i and 32 + i (and none of the
-  // rows 64 + i, 96 + i that a wider tile would have)
-#pragma unroll
-  for (int kh = 0; kh < 2; ++kh) {
-    uint32_t* d = reinterpret_cast<uint32_t*>(slot + kQSf + kh * 512 + (i & 31) * 16);
-    d[i >> 5] = kh ? sc.y : sc.x;
-    d[2 + (i >> 5)] = 0u;
-  }
-  reinterpret_cast<float*>(slot + kQNegM)[i] = negm;
-  reinterpret_cast<float*>(slot + kQInv)[i] = inv;
 }
 
+__device__ __forceinline__ void store_q_tile(const WeightParams& p, uint8_t* slot, int lane,
+                                             const QRows& q) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int i = lane + 32 * u;
+    if (i >= kRowTile) continue;
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch)
+      *reinterpret_cast<uint4*>(slot + (i >> 3) * 512 + ch * 128 + (i & 7) * 16) = q.c[u][ch];
+    // a row past the last, or one that saw no key at all, adds nothing: exp2(-inf) * 0
+    const bool live = q.st[u].y > 0.f;
+    reinterpret_cast<float*>(slot + kQNegM)[i] = live ? -(q.st[u].x * p.c2) : -INFINITY;
+    reinterpret_cast<float*>(slot + kQInv)[i] = live ? q.st[u].y : 0.f;
+  }
+  // scale-factor rows: row `lane` holds the 4-byte groups of tile rows lane and 32 + lane (and zeros
+  // for the rows from 48 on that a wider tile would have)
+#pragma unroll
+  for (int kh = 0; kh < 2; ++kh)
+    *reinterpret_cast<uint4*>(slot + kQSf + kh * 512 + lane * 16) =
+        make_uint4(kh ? q.sc[0].y : q.sc[0].x, kh ? q.sc[1].y : q.sc[1].x, 0u, 0u);
+}
+
+// The two Q warps take alternate steps, each with a slot of its own, and fetch their next tile
+// before they wait for the slot: a fetch takes about as long as the sums of two steps.
 __device__ __forceinline__ void load_queries(const WeightParams& p, const Span& sp, uint8_t* smem,
                                              int warp, int lane) {
   const uint32_t bars = smem_u32(smem) + kOffBars;
-  const int i = (warp - kWarpQ0) * 32 + lane;
-  uint32_t k = 0;
+  const uint32_t sl = (uint32_t)(warp - kWarpQ0);
+  uint8_t* slot = smem + kOffQ + sl * kQSlotBytes;
+  int b = sp.b0, tile = b < sp.b1 ? sp.first_tile(p, b) : 0;
+  auto next = [&]() {
+    if (++tile == sp.tiles && ++b < sp.b1) tile = sp.first_tile(p, b);
+  };
+  if (sp.tiles == 1 && sl == 1) return;  // the one tile stays in slot 0
+  if (sl == 1 && b < sp.b1) next();
+  QRows q;
+  if (b < sp.b1) fetch_q_tile(p, sp, tile, lane, q);
+  uint32_t use = 0;
   bool to = false;
-  for (int b = sp.b0; b < sp.b1; ++b) {
-    for (int tile = sp.first_tile(p, b); tile < sp.tiles; ++tile, ++k) {
-      if (sp.tiles == 1 && k > 0) return;  // the one tile stays
-      const uint32_t sl = k & 1u;
-      if (k >= 2) wait_bar_sleep(bars + 8 * (kBarQEmpty + sl), ((k >> 1) - 1) & 1, to);
-      load_q_tile(p, sp, smem + kOffQ + sl * kQSlotBytes, tile, i);
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (kBarQFull + sl));
-    }
+  while (b < sp.b1) {
+    if (use > 0) wait_bar_sleep(bars + 8 * (kBarQEmpty + sl), (use - 1) & 1, to);
+    store_q_tile(p, slot, lane, q);
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * (kBarQFull + sl));
+    if (sp.tiles == 1) return;
+    ++use;
+    next();
+    if (b < sp.b1) next();
+    if (b < sp.b1) fetch_q_tile(p, sp, tile, lane, q);
   }
   if (to && lane == 0) flag_status(p.status, KV_NVFP4_DEV_TIMEOUT);
+}
+
+__device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes) {
+  return d + (uint64_t)(bytes >> 4);  // start-address field: addresses stay below 2^18
 }
 
 __device__ __forceinline__ void issue_products(const WeightParams& p, const Span& sp,
@@ -207,12 +237,15 @@ __device__ __forceinline__ void issue_products(const WeightParams& p, const Span
   const uint32_t n = one ? (uint32_t)((p.rows + 15) & ~15) : (uint32_t)kRowTile;
   // A, B = E2M1 K-major, scale type UE4M3, M = 128
   const uint32_t idesc = (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((128u >> 4) << 24);
+  const uint64_t dk = smem_desc(sbase + kOffStage, 128, 512);
+  const uint64_t dq = smem_desc(sbase + kOffQ, 128, 512);
+  const uint64_t dsfk = smem_desc(sbase + kOffSfk, 16, 128);
+  const uint64_t dsfq = smem_desc(sbase + kOffQ + kQSf, 16, 128);
   uint32_t k = 0, step = 0;
   bool to = false;
   for (int b = sp.b0; b < sp.b1; ++b, ++k) {
     const uint32_t st = k % kStages;
     const uint32_t stage = sbase + kOffStage + st * kStageBytes;
-    const uint32_t sfk = sbase + kOffSfk + st * 1024;
     wait_bar_sleep(bars + 8 * (kBarKFull + st), (k / kStages) & 1, to);
     // the head's K scales of both pages into the scale-factor copy's rows: row r = page 0's keys r
     // and r + 32, then page 1's. The slot's previous reader completed before the stage was refilled
@@ -223,56 +256,85 @@ __device__ __forceinline__ void issue_products(const WeightParams& p, const Span
       for (int q = 0; q < 2; ++q)  // a skipped page leaves stale scales: its keys are not counted
         v[q] = lone ? lds64(stage + kStScales + q * 1024 + kh * 256 + lane * 8)
                     : lds64(stage + kStScales + q * 1024 + kh * 512 + lane * 16 + (sp.head & 1) * 8);
-      sts128(sfk + kh * 512 + lane * 16, v[0].x, v[0].y, v[1].x, v[1].y);
+      sts128(sbase + kOffSfk + st * 1024 + kh * 512 + lane * 16, v[0].x, v[0].y, v[1].x, v[1].y);
     }
     fence_async_smem();
     __syncwarp();
+    const uint32_t sfa = tbase + kColSfa + (k & 1u) * 8;
+    bool fresh = true;  // the block's scales are not in tensor memory yet
     for (int tile = sp.first_tile(p, b); tile < sp.tiles; ++tile, ++step) {
       const uint32_t buf = step & 1u, sl = one ? 0u : buf;
-      // S buffer and scale-factor columns `buf` are free once step - 2 has been read
+      // S buffer `buf` and the Q scales beside it are free once step - 2 has been read; so are the
+      // K scales of block k - 2, whose last step was step - 2 or earlier
       if (step >= 2) wait_bar_sleep(bars + 8 * (kBarSEmpty + buf), ((step >> 1) - 1) & 1, to);
       if (!one || step == 0)
         wait_bar_sleep(bars + 8 * (kBarQFull + sl), one ? 0u : (step >> 1) & 1, to);
       if (to) break;
       if (lane == 0) {
         tc_fence_after();
-        const uint32_t q = sbase + kOffQ + sl * kQSlotBytes;
-#pragma unroll
-        for (int kh = 0; kh < 2; ++kh) {
-          tmem_cp_32x128b_x4(tbase + kColSfa + buf * 8 + kh * 4, smem_desc(sfk + kh * 512, 16, 128));
-          tmem_cp_32x128b_x4(tbase + kColSfb + buf * 8 + kh * 4,
-                             smem_desc(q + kQSf + kh * 512, 16, 128));
+        const uint32_t sfb = tbase + kColSfb + sl * 8, d = tbase + kColS + buf * kRowTile;
+        const uint64_t kd = desc_add(dk, st * kStageBytes), qd = desc_add(dq, sl * kQSlotBytes);
+        if (fresh) {
+          tmem_cp_32x128b_x4(sfa, desc_add(dsfk, st * 1024));
+          tmem_cp_32x128b_x4(sfa + 4, desc_add(dsfk, st * 1024 + 512));
         }
-#pragma unroll
-        for (int kh = 0; kh < 2; ++kh)
-          mma_nvf4_ss(tbase + kColS + buf * kRowTile, smem_desc(stage + kh * 256, 128, 512),
-                      smem_desc(q + kh * 256, 128, 512), idesc, tbase + kColSfa + buf * 8 + kh * 4,
-                      tbase + kColSfb + buf * 8 + kh * 4, (uint32_t)kh);
+        if (!one || step == 0) {
+          tmem_cp_32x128b_x4(sfb, desc_add(dsfq, sl * kQSlotBytes));
+          tmem_cp_32x128b_x4(sfb + 4, desc_add(dsfq, sl * kQSlotBytes + 512));
+        }
+        mma_nvf4_ss(d, kd, qd, idesc, sfa, sfb, 0u);
+        mma_nvf4_ss(d, desc_add(kd, 256), desc_add(qd, 256), idesc, sfa + 4, sfb + 4, 1u);
         mma_commit(bars + 8 * (kBarSFull + buf));
         if (!one) mma_commit(bars + 8 * (kBarQEmpty + sl));
+        if (tile + 1 == sp.tiles) mma_commit(bars + 8 * (kBarKEmpty + st));  // K consumed
       }
+      fresh = false;
       __syncwarp();
     }
     if (to) break;
-    if (lane == 0) mma_commit(bars + 8 * (kBarKEmpty + st));  // K codes and scales consumed
-    __syncwarp();
   }
   if (to && lane == 0) flag_status(p.status, KV_NVFP4_DEV_TIMEOUT);
 }
 
-// kMasked: only rows from r0 on see this thread's key (r0 counted within the tile).
+// Pairs of fp32 in one 64-bit register, computed by one instruction; each half rounds on its own.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void halves_of(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Adds 16 rows' exp2(s c2 - m c2) / l. The product m c2 is rounded once per row, as in the tile
+// kernel's P, whose sum l divides by: the two roundings cancel. kMasked: only rows from r0 on see
+// this thread's key.
 template <bool kMasked>
 __device__ __forceinline__ void add_rows16(const uint32_t (&s)[16], const float* negm,
-                                           const float* inv, float c2, int r0, float (&acc)[4]) {
+                                           const float* inv, uint64_t c2, int r0,
+                                           uint64_t (&acc)[2]) {
 #pragma unroll
   for (int c = 0; c < 16; c += 4) {
-    const float4 m4 = *reinterpret_cast<const float4*>(negm + c);
-    const float4 i4 = *reinterpret_cast<const float4*>(inv + c);
-    const float nm[4] = {m4.x, m4.y, m4.z, m4.w}, iv[4] = {i4.x, i4.y, i4.z, i4.w};
+    const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(negm + c);
+    const ulonglong2 iv = *reinterpret_cast<const ulonglong2*>(inv + c);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x = fast_exp2((__uint_as_float(s[c + e]) + nm[e]) * c2);
-      if (!kMasked || c + e >= r0) acc[e] = fmaf(x, iv[e], acc[e]);
+    for (int e = 0; e < 4; e += 2) {
+      float x, y;
+      halves_of(fma2(pair_of(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])), c2,
+                     e ? m.y : m.x),
+                x, y);
+      x = fast_exp2(x);
+      y = fast_exp2(y);
+      if (kMasked) {
+        x = c + e >= r0 ? x : 0.f;
+        y = c + e + 1 >= r0 ? y : 0.f;
+      }
+      acc[e / 2] = fma2(pair_of(x, y), e ? iv.y : iv.x, acc[e / 2]);
     }
   }
 }
@@ -286,6 +348,7 @@ __device__ __forceinline__ void sum_weights(const WeightParams& p, const Span& s
   const int32_t* bt = p.block_table + (int64_t)sp.seq * p.max_pages;
   const int64_t wrow = ((int64_t)sp.seq * p.Hkv + sp.head) * p.w_stride;
   const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+  const uint64_t c2 = pair_of(p.c2, p.c2);
   uint32_t step = 0;
   bool to = false;
   for (int b = sp.b0; b < sp.b1; ++b) {
@@ -297,7 +360,7 @@ __device__ __forceinline__ void sum_weights(const WeightParams& p, const Span& s
     // the first row that sees this key
     const int64_t past = (int64_t)t - (sp.len - p.q_len);
     const int first = p.causal && past > 0 ? (int)(past * p.G) : 0;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    uint64_t acc[2] = {0ull, 0ull};
     for (int tile = sp.first_tile(p, b); tile < sp.tiles; ++tile, ++step) {
       const uint32_t buf = step & 1u;
       const uint8_t* slot = smem + kOffQ + (one ? 0u : buf) * kQSlotBytes;
@@ -311,12 +374,25 @@ __device__ __forceinline__ void sum_weights(const WeightParams& p, const Span& s
       __syncwarp();
       const int r0 = first - tile * kRowTile;
       const bool masked = __any_sync(0xffffffffu, r0 > 0);
-      for (int c = 0; c < cols; c += 16) {
-        uint32_t s[16];
-        tmem_ld16(tbase + lane_base + kColS + buf * kRowTile + c, s);
-        tmem_wait_ld_regs16(s);
-        if (masked) add_rows16<true>(s, negm + c, inv + c, p.c2, r0 - c, acc);
-        else add_rows16<false>(s, negm + c, inv + c, p.c2, 0, acc);
+      // the tile's columns 16 at a time, the next 16 on their way while these are summed
+      const uint32_t col = tbase + lane_base + kColS + buf * kRowTile;
+      auto add = [&](uint32_t (&s)[16], int c) {
+        if (masked) add_rows16<true>(s, negm + c, inv + c, c2, r0 - c, acc);
+        else add_rows16<false>(s, negm + c, inv + c, c2, 0, acc);
+      };
+      uint32_t s0[16], s1[16];
+      tmem_ld16(col, s0);
+      tmem_wait_ld_regs16(s0);
+      if (cols > 16) tmem_ld16(col + 16, s1);
+      add(s0, 0);
+      if (cols > 16) {
+        tmem_wait_ld_regs16(s1);
+        if (cols > 32) tmem_ld16(col + 32, s0);
+        add(s1, 16);
+        if (cols > 32) {
+          tmem_wait_ld_regs16(s0);
+          add(s0, 32);
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -326,14 +402,17 @@ __device__ __forceinline__ void sum_weights(const WeightParams& p, const Span& s
       }
     }
     if (real) {
-      const float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      float a[4];
+      halves_of(acc[0], a[0], a[1]);
+      halves_of(acc[1], a[2], a[3]);
+      const float sum = (a[0] + a[1]) + (a[2] + a[3]);
       p.w_out[wrow + t] = valid ? before + sum : before;
     }
   }
   if (to && lane == 0) flag_status(p.status, KV_NVFP4_DEV_TIMEOUT);
 }
 
-__global__ void __launch_bounds__(kThreads, 2) weight_kernel(const WeightParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) weight_kernel(const WeightParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(smem), bars = sbase + kOffBars;
@@ -344,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 2) weight_kernel(const WeightParams 
       mbar_init(bars + 8 * (kBarKEmpty + s), 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(bars + 8 * (kBarQFull + b), kQWarps);
+      mbar_init(bars + 8 * (kBarQFull + b), 1);
       mbar_init(bars + 8 * (kBarQEmpty + b), 1 + kSumWarps);
       mbar_init(bars + 8 * (kBarSFull + b), 1);
       mbar_init(bars + 8 * (kBarSEmpty + b), kSumWarps);
@@ -409,11 +488,11 @@ cudaError_t launch_weights(const uint8_t* q_codes, const uint8_t* q_scales, cons
   p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.q_len = q_len; p.rows = p.G * q_len;
   p.causal = causal; p.status = status;
   p.c2 = sm_scale * 1.4426950408889634f;
-  // about four CTAs for each of the two places on every SM, so that the last ones to finish cost
-  // little, and at most 64 blocks each
+  // about one round of CTAs: each starts its pipeline once
   const int64_t blocks = (total_tokens / 128 + num_seqs) * Hkv;
-  const int64_t per = blocks / ((int64_t)num_sms * 8);
-  p.blocks_per_cta = (int32_t)(per < 1 ? 1 : per > 64 ? 64 : per);
+  const int64_t places = (int64_t)num_sms * kCtasPerSm;
+  const int64_t per = (blocks + places - 1) / places;
+  p.blocks_per_cta = (int32_t)(per < 1 ? 1 : per > 256 ? 256 : per);
   const int64_t most = ((int64_t)max_seq_len + 127) / 128;
   p.chunks = (int32_t)((most + p.blocks_per_cta - 1) / p.blocks_per_cta);
   const int64_t grid = (int64_t)p.chunks * Hkv * num_seqs;
