@@ -57,7 +57,7 @@ __device__ __forceinline__ float set_weight(const float* w, int64_t stride, int 
 // whole histograms are C x 8 KB for every CTA, which took 5 to 8 us). Once the chosen bin holds at
 // most 2048 keys, which is after the first pass for weights that are not mostly equal, the CTAs
 // exchange those keys instead, and each finds the threshold among them on its own, seven bits at a
-// time.
+// time until one key is left.
 // With the exchanged keys go the counts of keys above the bin, so every CTA also knows how many
 // slots the CTAs before it list: three meetings of the cluster in all. The warps then list their
 // parts of the slice in order, by ballots.
@@ -431,17 +431,20 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
         const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += y;
       }
-      uint32_t before = sum - mine, digit = (uint32_t)(127 - 4 * lane);
+      uint32_t before = sum - mine, digit = (uint32_t)(127 - 4 * lane), share = v.w;
       const bool here = before < left && left <= sum;
       if (before + v.w < left) {
         before += v.w;
         --digit;
+        share = v.z;
         if (before + v.z < left) {
           before += v.z;
           --digit;
+          share = v.y;
           if (before + v.y < left) {
             before += v.y;
             --digit;
+            share = v.x;
           }
         }
       }
@@ -449,6 +452,16 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
       prefix |= __shfl_sync(0xffffffffu, digit, src) << shift;
       left -= __shfl_sync(0xffffffffu, before, src);
       done = shift;
+      if (done > 0 && __shfl_sync(0xffffffffu, share, src) == 1u) {
+        // one key is left: it is the edge (as a rule the case after one round or two)
+        const uint32_t rest = 0xFFFFFFFFu >> (32 - done);
+#pragma unroll
+        for (int u = 0; u < kSelRounds; ++u)
+          if (real[u] && x[u] - prefix <= rest) sh.digit = x[u];
+        __syncthreads();
+        prefix = sh.digit;
+        break;
+      }
       // the other bins: every warp read them before the barrier above
       if (tid < 128) sh.bins7[(round + 1) & 1][tid] = 0;
       __syncthreads();
