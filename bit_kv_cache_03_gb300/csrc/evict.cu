@@ -560,19 +560,21 @@ struct CompactParams {
 // One cluster per (sequence, KV head, part): part 0 the K rows, 1 the V rows, 2 the weights. The
 // cluster takes its rows in waves: in a wave every thread loads what it moves into registers (a
 // 16-byte code piece, and for half of the threads four scales, of kMoveRows rows), the cluster
-// meets, and the wave is stored. The next wave's reads start right behind the stores: they lie
-// beyond the stored rows.
+// meets, and the wave is stored. The next wave's reads, which lie behind the wave's rows, are on
+// their way meanwhile.
 //
 // Bounds: 296 bytes per kept row and KV head, but the rows lie apart: a K row's codes are four
-// 16-byte pieces in sectors of 32 that hold a neighbour's piece as well, its scales two words in two
-// more sectors, so a sparse choice reads about twice its bytes. At 4 x 4 sets, 16384 kept of 131072,
-// one CTA per part took 272 us.
+// 16-byte pieces in sectors that hold a neighbour's piece as well, its scales two words in two more,
+// and DRAM gives 64 bytes at a time. 4 x 4 sets, 16384 kept of 131072: 78 MB of rows move, 184 MB
+// cross the memory bus, in 43 us (4.3 TB/s). One CTA per part took 272 us, waves without reads
+// ahead 45 us, eight rows per thread at two CTAs per SM 59 us, two rows at six 55 us.
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 8;                       // rows in flight per thread
+constexpr int kMoveRows = 4;                                // rows in flight per thread
 constexpr int kMoveMaxCluster = 8;
+constexpr int kMoveCtasPerSm = 3;
 constexpr int kMoveTile = kMoveThreads / 4 * kMoveRows;  // rows of a CTA per wave, codes and scales
 
-__global__ void __launch_bounds__(kMoveThreads, 3) compact_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) compact_kernel(const CompactParams p) {
   const uint32_t C = cluster_size(), rank = cluster_rank();
   const int parts = p.weights != nullptr ? 3 : 2;
   const int64_t unit = blockIdx.x / C;
@@ -632,48 +634,75 @@ __global__ void __launch_bounds__(kMoveThreads, 3) compact_kernel(const CompactP
   };
   const int64_t wave = (int64_t)C * kMoveTile;
   constexpr int kApart = kMoveThreads / 4;  // rows between a thread's rows
-  int64_t first = (int64_t)rank * kMoveTile + (tid >> 2);
-  int32_t t[kMoveRows], bad = 0;
-#pragma unroll
-  for (int u = 0; u < kMoveRows; ++u) t[u] = first + u * kApart < kept ? index[first + u * kApart] : -1;
-  for (int64_t j0 = 0; j0 < kept; j0 += wave, first += wave) {
-    int32_t from[kMoveRows], to[kMoveRows];
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      const bool real = first + u * kApart < kept, ok = t[u] >= 0 && t[u] < len;
-      if (real && !ok) bad |= KV_NVFP4_DEV_BAD_POS;
-      from[u] = ok ? src_table[t[u] / kPage] : -1;
-      to[u] = real && ok ? dst_table[(first + u * kApart) / kPage] : -1;
-    }
+  const int64_t first = (int64_t)rank * kMoveTile + (tid >> 2);
+  int32_t bad = 0;
+  struct Rows {
     uint4 c[kMoveRows];
     uint32_t sc[kMoveRows];
+    int32_t to[kMoveRows];
+  };
+  int32_t t[kMoveRows], from[kMoveRows];  // of the wave that is loaded next
+  auto find = [&](int64_t j) {             // its old slots and pages
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) t[u] = j + u * kApart < kept ? index[j + u * kApart] : -1;
 #pragma unroll
     for (int u = 0; u < kMoveRows; ++u) {
-      const bool real = first + u * kApart < kept && t[u] >= 0 && t[u] < len;
-      const bool ok = from[u] >= 0 && from[u] < p.num_pages && to[u] >= 0 && to[u] < p.num_pages;
-      if (real && !ok) bad |= KV_NVFP4_DEV_BAD_PAGE;
+      const bool real = j + u * kApart < kept, ok = t[u] >= 0 && t[u] < len;
+      if (real && !ok) bad |= KV_NVFP4_DEV_BAD_POS;
+      if (!ok) t[u] = -1;
+      from[u] = ok ? src_table[t[u] / kPage] : -1;
+    }
+  };
+  auto load = [&](int64_t j, Rows& r) {
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) r.to[u] = t[u] >= 0 ? dst_table[(j + u * kApart) / kPage] : -1;
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) {
+      const bool ok = from[u] >= 0 && from[u] < p.num_pages && r.to[u] >= 0 && r.to[u] < p.num_pages;
+      if (t[u] >= 0 && !ok) bad |= KV_NVFP4_DEV_BAD_PAGE;
       // a row that is already there stays; it and a skipped one read slot 0 of page 0 for nothing
-      const bool move = ok && (t[u] != first + u * kApart || from[u] != to[u]);
+      const bool move = ok && (t[u] != j + u * kApart || from[u] != r.to[u]);
       const uint8_t* src = p.pool + (move ? from[u] * block : 0);
       const int slot = move ? t[u] % kPage : 0;
-      c[u] = *reinterpret_cast<const uint4*>(src + code_at(slot));
-      sc[u] = *reinterpret_cast<const uint32_t*>(src + scale_at(slot));
-      if (!move) to[u] = -1;
+      r.c[u] = *reinterpret_cast<const uint4*>(src + code_at(slot));
+      r.sc[u] = *reinterpret_cast<const uint32_t*>(src + scale_at(slot));
+      if (!move) r.to[u] = -1;
     }
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u)
-      t[u] = first + wave + u * kApart < kept ? index[first + wave + u * kApart] : -1;
-    // the wave is read whole before any of its rows is written
-    cluster_arrive();
-    cluster_wait();
+  };
+  auto store = [&](int64_t j, const Rows& r) {
 #pragma unroll
     for (int u = 0; u < kMoveRows; ++u) {
-      if (to[u] < 0) continue;
-      const int slot = (int)((first + u * kApart) % kPage);
-      uint8_t* dst = p.pool + to[u] * block;
-      *reinterpret_cast<uint4*>(dst + code_at(slot)) = c[u];
-      if (piece < 2) *reinterpret_cast<uint32_t*>(dst + scale_at(slot)) = sc[u];
+      if (r.to[u] < 0) continue;
+      const int slot = (int)((j + u * kApart) % kPage);
+      uint8_t* dst = p.pool + r.to[u] * block;
+      *reinterpret_cast<uint4*>(dst + code_at(slot)) = r.c[u];
+      if (piece < 2) *reinterpret_cast<uint32_t*>(dst + scale_at(slot)) = r.sc[u];
     }
+  };
+  Rows a, b;
+  if (kept > 0) {
+    find(first);
+    load(first, a);
+    find(first + wave);
+  }
+  for (int64_t j0 = 0; j0 < kept; j0 += 2 * wave) {
+    // the wave is read whole before any of its rows is written; the next one's reads (of slots
+    // behind the wave) start while the cluster meets
+    cluster_arrive();
+    if (j0 + wave < kept) {
+      load(first + j0 + wave, b);
+      find(first + j0 + 2 * wave);
+    }
+    cluster_wait();
+    store(first + j0, a);
+    if (j0 + wave >= kept) break;
+    cluster_arrive();
+    if (j0 + 2 * wave < kept) {
+      load(first + j0 + 2 * wave, a);
+      find(first + j0 + 3 * wave);
+    }
+    cluster_wait();
+    store(first + j0 + wave, b);
   }
   if (bad != 0) flag_status(p.status, bad);
 }
@@ -743,7 +772,7 @@ cudaError_t launch_evict_compact(const int32_t* index, int64_t index_stride, int
   // no more CTAs than run at once
   const int64_t units = (int64_t)num_seqs * Hkv * (weights != nullptr ? 3 : 2);
   int64_t C = 1;
-  while (C < kMoveMaxCluster && C * kMoveTile < index_stride && units * C * 2 <= 3 * (int64_t)num_sms)
+  while (C < kMoveMaxCluster && C * kMoveTile < index_stride && units * C * 2 <= kMoveCtasPerSm * (int64_t)num_sms)
     C *= 2;
   if (units * C > 0x7FFFFFFF) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1];
