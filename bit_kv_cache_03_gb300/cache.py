@@ -87,6 +87,8 @@ class PagedNVFP4Cache:
         """attend() with a bf16 `out`, adding every key's attention weight to `weights` (or writing
         weights_in plus them). On the plan of the last plan()."""
         self._check_accounts(weights, weights_in)
+        if weights_in is not None and weights_in.shape != weights.shape:
+            raise ValueError("weights_in must have the shape of weights")
         if out.dtype != torch.bfloat16 or not out.is_contiguous():
             raise ValueError("out must be a contiguous bfloat16 tensor")
         if sm_scale is None:
@@ -108,6 +110,10 @@ class PagedNVFP4Cache:
         [num_seqs, num_kv_heads, n] (every KV head keeps its own tokens) or [num_seqs, 1, n] (one
         set for all), n at least the largest kept count; receives the kept slots, ascending."""
         self._check_accounts(weights)
+        for x in (seq_lens, keep):
+            if x.dtype != torch.int32 or not x.is_contiguous() or x.numel() != self.num_seqs or \
+                    x.device != weights.device:
+                raise ValueError("seq_lens and keep must be device int32 [num_seqs]")
         if index.dtype != torch.int32 or not index.is_contiguous() or index.dim() != 3 or \
                 index.shape[0] != self.num_seqs or index.shape[1] not in (1, self.layout.num_kv_heads):
             raise ValueError("index must be a contiguous int32 [num_seqs, num_kv_heads or 1, n]")
@@ -120,9 +126,10 @@ class PagedNVFP4Cache:
 
     def _check_accounts(self, *tensors):
         for w in tensors:
-            if w is not None and (w.dtype != torch.float32 or not w.is_contiguous() or w.dim() != 3 or
+            if w is not None and (not w.is_cuda or w.dtype != torch.float32 or not w.is_contiguous() or w.dim() != 3 or
                                   tuple(w.shape[:2]) != (self.num_seqs, self.layout.num_kv_heads)):
-                raise ValueError("weights must be contiguous float32 [num_seqs, num_kv_heads, slots]")
+                raise ValueError("weights must be a contiguous device float32 "
+                                 "[num_seqs, num_kv_heads, slots]")
 
     # -- append of the step's new tokens + attention, one launch ------------------------------
     def decode_step(self, q, k, v, out, q_codes=None, q_scales=None, sm_scale=None, stream=None):

@@ -71,10 +71,13 @@ __device__ __forceinline__ void account_chunk(const AccountParams& p, const int4
   const int part = unit % p.parts, pair = unit / p.parts;
   const int head = pair % Hkv, seq = pair / Hkv;
   const int64_t group = group_of(seq, head);
-  const int4 g0 = groups[2 * group], g1 = groups[2 * group + 1];
+  const int4 g0 = groups[2 * group], g1 = groups[2 * group + 1];  // written before the attention
   const int len = g0.w;
   const int first = part * p.per_cta * kAccPages;  // page
+  // A sequence shorter than the longest has CTAs without pages. They end here, before the wait for
+  // the attention kernel (the others, of which there is at least one, carry it to the next kernel).
   if ((int64_t)first * kPage >= len) return;  // uniform over the CTA
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int pages = min(p.per_cta * kAccPages, (len + kPage - 1) / kPage - first);
   const int key = 4 * (tid & 15);
   const float* src = p.scores + (((int64_t)g1.w + first + (tid >> 4)) * heads_per_group +

@@ -121,6 +121,7 @@ kv_nvfp4_status cuda_status(cudaError_t e) {
   return KV_NVFP4_ECUDA;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int num_sms_current_device() {
@@ -791,6 +792,8 @@ kv_nvfp4_status kv_nvfp4_decode_attn_weights(
   const void* ptrs[] = {d_workspace, d_weights_workspace, q_codes, q_scales, pool, out};
   for (const void* p : ptrs)
     if (!aligned16(p)) return KV_NVFP4_EINVAL;
+  if (!aligned4(weights_in) || !aligned4(weights_out) || !aligned4(d_block_table))
+    return KV_NVFP4_EINVAL;
   const WeightsWorkspace w = weights_workspace(L, plan);
   if (ww_bytes < w.bytes) return KV_NVFP4_ENOSPACE;
   const int num_sms = num_sms_current_device();
@@ -852,6 +855,8 @@ kv_nvfp4_status kv_nvfp4_evict_select(const kv_nvfp4_layout* L, const float* wei
   if (!weights || !d_seq_lens || !d_keep || !d_index || weights_stride <= 0 || index_stride <= 0 ||
       sink < 0 || recent < 0)
     return KV_NVFP4_EINVAL;
+  if (!aligned4(weights) || !aligned4(d_seq_lens) || !aligned4(d_keep) || !aligned4(d_index))
+    return KV_NVFP4_EINVAL;
   return cuda_status(kvnvfp4::launch_evict_select(
       weights, weights_stride, d_seq_lens, d_keep, num_seqs, per_head, sink, recent, d_index,
       index_stride, L->num_kv_heads, num_sms_current_device(), d_status, (cudaStream_t)stream));
@@ -873,6 +878,9 @@ kv_nvfp4_status kv_nvfp4_evict_compact(const kv_nvfp4_layout* L, const int32_t* 
   if (d_dst_block_table != nullptr ? dst_max_pages <= 0 : dst_max_pages != 0)
     return KV_NVFP4_EINVAL;
   if (weights != nullptr && weights_stride <= 0) return KV_NVFP4_EINVAL;
+  const void* words[] = {d_index, d_seq_lens, d_keep, d_block_table, d_dst_block_table, weights};
+  for (const void* p : words)
+    if (!aligned4(p)) return KV_NVFP4_EINVAL;
   const bool in_place = d_dst_block_table == nullptr;
   return cuda_status(kvnvfp4::launch_evict_compact(
       d_index, index_stride, per_head, d_seq_lens, d_keep, num_seqs, d_block_table, max_pages,

@@ -1179,7 +1179,6 @@ __global__ void __launch_bounds__(kAccThreads, 4) merge_weights_kernel(const Mer
     merge_row<false, true>(p, blockIdx.x / (p.Hkv * kRows), blockIdx.x % (p.Hkv * kRows));
     return;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t stride = (int64_t)p.Hkv * kPartHeadFloats;
   auto part = [&](int q, int head) { return p.partials + q * stride + head * kPartHeadFloats; };
   account_chunk(

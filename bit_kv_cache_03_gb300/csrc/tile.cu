@@ -971,7 +971,6 @@ __global__ void __launch_bounds__(kAccThreads, 4) tile_merge_weights_kernel(cons
     tile_merge_row<true>(p, blockIdx.x / a.R, blockIdx.x % a.R);
     return;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   account_chunk(
       a, p.groups, (int)blockIdx.x - merges, p.Hkv, 1, p.c2,
       [&](int seq, int head) { return (int64_t)seq * p.Hkv + head; },

@@ -417,6 +417,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weight_kernel(const Weig
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(smem), bars = sbase + kOffBars;
   asm volatile("griddepcontrol.launch_dependents;");
+  // a sequence shorter than the longest has CTAs without blocks; the plan's tables were written
+  // before the attention kernel started, so that they can be read ahead of the wait
+  const Span sp(p);
+  if (sp.b0 >= sp.b1) return;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bars + 8 * (kBarKFull + s), 1);
@@ -438,7 +442,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weight_kernel(const Weig
   // a programmatic dependent of the attention kernel or its merge, which write the statistics
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(smem + kOffTmemSlot);
-  const Span sp(p);
   if (warp == kWarpProducer) {
     produce_keys(p, sp, sbase, lane);
   } else if (warp == kWarpMma) {

@@ -49,7 +49,7 @@ A = 1 << 20  # a 16-byte aligned address that is never read
     dict(workspace=0), dict(weights_workspace=0), dict(q_codes=0), dict(q_scales=0), dict(pool=0),
     dict(block_table=0), dict(out=0), dict(weights_out=0), dict(num_pages=0), dict(max_pages=0),
     dict(max_pages=1), dict(weights_stride=99), dict(out=A + 8), dict(pool=A + 1),
-    dict(weights_workspace=A + 4),
+    dict(weights_workspace=A + 4), dict(weights_out=A + 2), dict(weights_in=A + 1),
 ])
 def test_attend_weights_refuses(kv, change):
     L, info = _plan(kv, 24, 4, [100], 1)
@@ -72,6 +72,7 @@ def test_attend_weights_refuses_a_small_workspace(kv):
 @pytest.mark.parametrize("change", [
     dict(weights=0), dict(seq_lens=0), dict(keep=0), dict(index=0), dict(weights_stride=0),
     dict(index_stride=0), dict(sink=-1), dict(recent=-1), dict(num_seqs=-1),
+    dict(weights=A + 2), dict(index=A + 1), dict(keep=A + 3),
 ])
 def test_select_refuses(kv, change):
     a = dict(layout=kv.make_layout(24, 4), weights=A, weights_stride=64, seq_lens=A, keep=A,
@@ -86,6 +87,7 @@ def test_select_refuses(kv, change):
     dict(index=0), dict(seq_lens=0), dict(keep=0), dict(block_table=0), dict(pool=0),
     dict(pool=A + 8), dict(index_stride=0), dict(max_pages=0), dict(num_pages=0),
     dict(num_seqs=-1), dict(dst_max_pages=2), dict(dst_block_table=A), dict(weights=A),
+    dict(index=A + 2), dict(weights=A + 2, weights_stride=64),
 ])
 def test_compact_refuses(kv, change):
     a = dict(layout=kv.make_layout(24, 4), index=A, index_stride=8, per_head=True, seq_lens=A,

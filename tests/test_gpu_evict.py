@@ -92,6 +92,8 @@ def kv():
     ([0, 300], 50, True, 128, 24, 4),                       # a prompt of its own; 300 rows
     ([130, 1], 200, False, 192, 8, 2),
     ([0], 300, True, 128, 3, 1),                            # causal over several key blocks
+    ([5, 900, 3, 60, 0, 1, 2, 700, 9, 64, 30, 7], 1, True, 64, 8, 2),  # many, mostly short
+    ([5, 900, 3, 60, 0, 1, 2, 700, 9], 9, True, 128, 8, 2),
 ])
 def test_attend_weights(lens, q_len, causal, chunk, Hq, Hkv):
     w = synth.Workload("weights", lens, q_len=q_len, causal=causal, seed=sum(lens) + q_len,
@@ -104,6 +106,18 @@ def test_attend_weights(lens, q_len, causal, chunk, Hq, Hkv):
     a.run()  # equal inputs give equal bits, on a used workspace too
     torch.cuda.synchronize()
     assert torch.equal(first.nan_to_num(), a.weights.nan_to_num()) and torch.equal(out, a.out)
+
+
+@pytest.mark.parametrize("lens,q_len,Hq,Hkv", [([500, 20], 1, 24, 4), ([300, 40], 1, 32, 8),
+                                             ([300, 40], 8, 24, 4)])
+def test_attend_weights_onto_aligned_accounts(lens, q_len, Hq, Hkv):
+    w = synth.Workload("aligned", lens, q_len=q_len, seed=7, q_heads=Hq, kv_heads=Hkv,
+                       chunk_tokens=128)
+    a = Attend(w, 128)
+    a.held = a.held[..., :a.c.max_pages * 64].contiguous()
+    a.weights = torch.full_like(a.held, float("nan"))
+    a.run()
+    a.check(a.held.cpu().numpy().astype(np.float64))
 
 
 def test_attend_weights_without_and_onto_the_accounts():
@@ -231,6 +245,66 @@ def test_select_of_hard_values(kind):
         if kind == "special" and not per_head:
             w[:, 1] = 0  # no inf - inf: the sum is the first head's
         _check_select(w, [2999, 1200], [1300, 7], per_head, 2, 9)
+
+
+@pytest.mark.parametrize("H,per_head", [(1, True), (3, False)])
+def test_select_of_more_slots_than_a_cluster_holds(H, per_head):
+    # 16 CTAs hold 48K keys each: the rest is read again in every pass
+    rng = np.random.default_rng(H)
+    w = np.exp(2.5 * rng.standard_normal((1, H, 900001))).astype(np.float32)
+    w[:, :, ::11] = 0.5
+    for keep in (70000, 899990):
+        _check_select(w, [900001], [keep], per_head, 5, 100)
+
+
+@pytest.mark.parametrize("sets", [40, 700])
+def test_select_of_many_sets(sets):
+    rng = np.random.default_rng(sets)
+    lens = [int(x) for x in rng.integers(1, 3000, sets)]
+    w = rng.random((sets, 2, 3000), dtype=np.float32)
+    _check_select(w, lens, [n // 3 + 1 for n in lens], True, 1, 7)
+
+
+def test_select_and_compact_in_a_graph():
+    # captured once, replayed on new weights and lengths
+    k = kv()
+    rng = np.random.default_rng(0)
+    H, L = 2, k.make_layout(2, 2)
+    lens, keep = [700, 300], [256, 100]
+    pool, table, dst, index, weights = _compact_case(lens, keep, H, True, 5)
+    dev = lambda x: torch.from_numpy(x.copy()).cuda()  # noqa: E731
+    p, t, i, w = dev(pool), dev(table), dev(index), dev(weights)
+    n, m = dev(np.array(lens, np.int32)), dev(np.array(keep, np.int32))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def both():
+        k.kv_nvfp4_evict_select(L, w, w.shape[2], n, m, 2, True, 2, 8, i, i.shape[2], status)
+        k.kv_nvfp4_evict_compact(L, i, i.shape[2], True, n, m, 2, t, t.shape[1], pool.shape[0], p,
+                                 None, 0, w, w.shape[2], status)
+
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()  # attributes are set outside the capture
+        with torch.cuda.graph(graph, stream=side):
+            both()
+    torch.cuda.synchronize()
+    for lens in ([700, 300], [650, 101], [3, 290]):
+        new = rng.random(weights.shape, dtype=np.float32)
+        w.copy_(torch.from_numpy(new))
+        p.copy_(torch.from_numpy(pool))
+        n.copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        ix = np.full(index.shape, -1, np.int32)
+        for s in range(2):
+            for h in range(H):
+                x = evictref.select(new[s, h], lens[s], keep[s], 2, 8)
+                ix[s, h, :len(x)] = x
+                assert np.array_equal(i[s, h, :len(x)].cpu().numpy(), x)
+        want, ww = evictref.compact(pool, table, table, H, ix, lens, keep, new)
+        assert np.array_equal(p.cpu().numpy(), want) and np.array_equal(w.cpu().numpy(), ww)
+    assert int(status.item()) == 0
 
 
 def test_select_flags_bad_sequences_and_leaves_them():
@@ -401,6 +475,33 @@ def test_append_slots_flags():
         c.append(x, x, i32(0, 0, 0, 0), i32(*pos), slots=i32(*slots))
         torch.cuda.synchronize()
         assert int(c.status.item()) == bit
+
+
+def test_the_cache_checks_its_arguments():
+    k = kv()
+    c = k.PagedNVFP4Cache(4, np.arange(4, dtype=np.int32).reshape(2, 2), 100, 4, 2)
+    w = c.weight_accounts()
+    assert tuple(w.shape) == (2, 2, 128) and not w.any()
+    i32 = torch.tensor([5, 5], dtype=torch.int32, device="cuda")
+    index = torch.zeros(2, 2, 5, dtype=torch.int32, device="cuda")
+    c.plan([10, 10], 1)
+    out = torch.zeros(2, 4, 128, dtype=torch.bfloat16, device="cuda")
+    qc, qs = c.quantized_q_buffers(2)
+    for bad in (w.half(), w[:, :1], w.cpu(), w.transpose(0, 1)[:, :1]):
+        with pytest.raises(ValueError):
+            c.attend_weights(qc, qs, out, bad)
+        with pytest.raises(ValueError):
+            c.evict(bad, i32, i32, index)
+    for bad in (out.float(), out.transpose(0, 1)):
+        with pytest.raises(ValueError):
+            c.attend_weights(qc, qs, bad, w)
+    with pytest.raises(ValueError):
+        c.attend_weights(qc, qs, out, w, weights_in=w[..., :64].contiguous())
+    for lens, keep, ix in ((i32.long(), i32, index), (i32, i32[:1], index), (i32.cpu(), i32, index),
+                           (i32, i32, index.long()), (i32, i32, index[0]),
+                           (i32, i32, torch.zeros(2, 3, 5, dtype=torch.int32, device="cuda"))):
+        with pytest.raises(ValueError):
+            c.evict(w, lens, keep, ix)
 
 
 # ---- together ----------------------------------------------------------------------------------
