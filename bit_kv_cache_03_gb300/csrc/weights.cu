@@ -9,14 +9,15 @@
 // tensor-memory lane) and sums over the query rows in its own registers, in row order, so there is
 // no reduction across threads and no atomic, and the result does not depend on the launch shape.
 //
-// A CTA takes `blocks_per_cta` consecutive 128-key blocks (two pages) of one (sequence, KV head)
-// and walks all row tiles of 48 rows over each: Q.K^T by tcgen05.mma kind::mxf4nvf4, M = 128 keys,
-// N = the tile's rows (a multiple of 16 up to 48), two K = 64 instructions per tile, into one of
-// two S buffers. Roles (256 threads): warp 0 copies K pages (ring of kStages blocks), warp 1
-// issues the MMAs and owns tensor memory, warps 2, 3 lay out Q tiles (codes in the tensor core's
-// tile order, scales, statistics; ring of two, or a single tile loaded once when all rows fit one),
-// warps 4..7 sum. Four such CTAs share an SM, so that sixteen warps keep its exponential units busy. Every wait is bounded in time, as in the attention
-// kernels.
+// A CTA takes `blocks_per_cta` consecutive 128-key blocks (two pages) of one (sequence, KV head), two
+// at a time, and walks all row tiles of 48 rows over the pair: Q.K^T by tcgen05.mma
+// kind::mxf4nvf4, M = 128 keys, N = the tile's rows (a multiple of 16 up to 48), two K = 64
+// instructions per tile and block. A thread sums two keys, one of each block, so that the tile's
+// statistics are read once for both and two independent chains run. Roles (256 threads): warp 0
+// copies K pages (ring of kStages blocks), warp 1 issues the MMAs and owns tensor memory, warps 2, 3
+// lay out Q tiles (codes in the tensor core's tile order, scales, statistics; ring of two, or a
+// single tile loaded once when all rows fit one), warps 4..7 sum. Two such CTAs share an SM. Every
+// wait is bounded in time, as in the attention kernels.
 
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -27,7 +28,8 @@ namespace kvnvfp4 {
 
 namespace {
 
-constexpr int kStages = 4;
+constexpr int kStages = 8;
+constexpr int kPair = 2;                     // key blocks of a step
 constexpr int kRowTile = 48;                 // query rows of a tile
 constexpr int kStScales = 8192;              // within a stage: K codes of two pages, then scales
 constexpr int kStageBytes = 8192 + 2 * 1024;
@@ -47,11 +49,10 @@ constexpr int kOffTmemSlot = kOffBars + kNumBars * 8;
 constexpr int kSmemBytes = kOffTmemSlot + 16;
 static_assert(kQTileBytes % 16 == 0 && kQSlotBytes % 16 == 0 && kOffBars % 8 == 0, "alignment");
 
-// tensor memory: S [2][48], K scales [2][2 k-halves][4], Q scales [2][2 k-halves][4]: 128 columns, so
-// that four CTAs share the 512 of an SM
-constexpr uint32_t kColS = 0, kColSfa = 96, kColSfb = 112, kTmemCols = 128;
-constexpr int kCtasPerSm = 4;
-static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of four CTAs");
+// tensor memory: S [2][kPair][48], K scales [2][kPair][2 k-halves][4], Q scales [2][2 k-halves][4]
+constexpr uint32_t kColS = 0, kColSfa = 192, kColSfb = 224, kTmemCols = 256;
+constexpr int kCtasPerSm = 2;
+static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of two CTAs");
 
 constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpQ0 = 2, kWarpSum0 = 4;
 constexpr int kSumWarps = 4;
@@ -202,7 +203,7 @@ __device__ __forceinline__ void load_queries(const WeightParams& p, const Span& 
   uint8_t* slot = smem + kOffQ + sl * kQSlotBytes;
   int b = sp.b0, tile = b < sp.b1 ? sp.first_tile(p, b) : 0;
   auto next = [&]() {
-    if (++tile == sp.tiles && ++b < sp.b1) tile = sp.first_tile(p, b);
+    if (++tile == sp.tiles && (b += kPair) < sp.b1) tile = sp.first_tile(p, b);
   };
   if (sp.tiles == 1 && sl == 1) return;  // the one tile stays in slot 0
   if (sl == 1 && b < sp.b1) next();
@@ -243,50 +244,59 @@ __device__ __forceinline__ void issue_products(const WeightParams& p, const Span
   const uint64_t dsfq = smem_desc(sbase + kOffQ + kQSf, 16, 128);
   uint32_t k = 0, step = 0;
   bool to = false;
-  for (int b = sp.b0; b < sp.b1; ++b, ++k) {
-    const uint32_t st = k % kStages;
-    const uint32_t stage = sbase + kOffStage + st * kStageBytes;
-    wait_bar_sleep(bars + 8 * (kBarKFull + st), (k / kStages) & 1, to);
-    // the head's K scales of both pages into the scale-factor copy's rows: row r = page 0's keys r
-    // and r + 32, then page 1's. The slot's previous reader completed before the stage was refilled
+  for (int b = sp.b0; b < sp.b1; b += kPair, k += kPair) {
+    const int blocks = min(kPair, sp.b1 - b);
+    for (int i = 0; i < blocks; ++i) {
+      const uint32_t st = (k + i) % kStages;
+      const uint32_t stage = sbase + kOffStage + st * kStageBytes;
+      wait_bar_sleep(bars + 8 * (kBarKFull + st), ((k + i) / kStages) & 1, to);
+      // the head's K scales of both pages into the scale-factor copy's rows: row r = page 0's keys r
+      // and r + 32, then page 1's. The slot's previous reader completed before the stage was refilled
 #pragma unroll
-    for (int kh = 0; kh < 2; ++kh) {
-      uint2 v[2];
+      for (int kh = 0; kh < 2; ++kh) {
+        uint2 v[2];
 #pragma unroll
-      for (int q = 0; q < 2; ++q)  // a skipped page leaves stale scales: its keys are not counted
-        v[q] = lone ? lds64(stage + kStScales + q * 1024 + kh * 256 + lane * 8)
-                    : lds64(stage + kStScales + q * 1024 + kh * 512 + lane * 16 + (sp.head & 1) * 8);
-      sts128(sbase + kOffSfk + st * 1024 + kh * 512 + lane * 16, v[0].x, v[0].y, v[1].x, v[1].y);
+        for (int q = 0; q < 2; ++q)  // a skipped page leaves stale scales: its keys are not counted
+          v[q] = lone
+                     ? lds64(stage + kStScales + q * 1024 + kh * 256 + lane * 8)
+                     : lds64(stage + kStScales + q * 1024 + kh * 512 + lane * 16 + (sp.head & 1) * 8);
+        sts128(sbase + kOffSfk + st * 1024 + kh * 512 + lane * 16, v[0].x, v[0].y, v[1].x, v[1].y);
+      }
     }
     fence_async_smem();
     __syncwarp();
-    const uint32_t sfa = tbase + kColSfa + (k & 1u) * 8;
-    bool fresh = true;  // the block's scales are not in tensor memory yet
+    bool fresh = true;  // the pair's scales are not in tensor memory yet
     for (int tile = sp.first_tile(p, b); tile < sp.tiles; ++tile, ++step) {
       const uint32_t buf = step & 1u, sl = one ? 0u : buf;
       // S buffer `buf` and the Q scales beside it are free once step - 2 has been read; so are the
-      // K scales of block k - 2, whose last step was step - 2 or earlier
+      // K scales of the pair before the last, whose last step was step - 2 or earlier
       if (step >= 2) wait_bar_sleep(bars + 8 * (kBarSEmpty + buf), ((step >> 1) - 1) & 1, to);
       if (!one || step == 0)
         wait_bar_sleep(bars + 8 * (kBarQFull + sl), one ? 0u : (step >> 1) & 1, to);
       if (to) break;
       if (lane == 0) {
         tc_fence_after();
-        const uint32_t sfb = tbase + kColSfb + sl * 8, d = tbase + kColS + buf * kRowTile;
-        const uint64_t kd = desc_add(dk, st * kStageBytes), qd = desc_add(dq, sl * kQSlotBytes);
-        if (fresh) {
-          tmem_cp_32x128b_x4(sfa, desc_add(dsfk, st * 1024));
-          tmem_cp_32x128b_x4(sfa + 4, desc_add(dsfk, st * 1024 + 512));
-        }
+        const uint32_t sfb = tbase + kColSfb + sl * 8;
+        const uint64_t qd = desc_add(dq, sl * kQSlotBytes);
         if (!one || step == 0) {
           tmem_cp_32x128b_x4(sfb, desc_add(dsfq, sl * kQSlotBytes));
           tmem_cp_32x128b_x4(sfb + 4, desc_add(dsfq, sl * kQSlotBytes + 512));
         }
-        mma_nvf4_ss(d, kd, qd, idesc, sfa, sfb, 0u);
-        mma_nvf4_ss(d, desc_add(kd, 256), desc_add(qd, 256), idesc, sfa + 4, sfb + 4, 1u);
+        for (int i = 0; i < blocks; ++i) {
+          const uint32_t st = (k + i) % kStages;
+          const uint32_t sfa = tbase + kColSfa + ((k & 2u) + i) * 8;
+          const uint32_t d = tbase + kColS + (2 * buf + i) * kRowTile;
+          const uint64_t kd = desc_add(dk, st * kStageBytes);
+          if (fresh) {
+            tmem_cp_32x128b_x4(sfa, desc_add(dsfk, st * 1024));
+            tmem_cp_32x128b_x4(sfa + 4, desc_add(dsfk, st * 1024 + 512));
+          }
+          mma_nvf4_ss(d, kd, qd, idesc, sfa, sfb, 0u);
+          mma_nvf4_ss(d, desc_add(kd, 256), desc_add(qd, 256), idesc, sfa + 4, sfb + 4, 1u);
+        }
+        // the only commit: the summing warps, which wait for it, release the Q slot and the K stages
+        // (a tcgen05 instruction costs this warp 100 to 200 cycles, and it is the one that never waits)
         mma_commit(bars + 8 * (kBarSFull + buf));
-        if (!one) mma_commit(bars + 8 * (kBarQEmpty + sl));
-        if (tile + 1 == sp.tiles) mma_commit(bars + 8 * (kBarKEmpty + st));  // K consumed
       }
       fresh = false;
       __syncwarp();
@@ -311,31 +321,33 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// Adds 16 rows' exp2(s c2 - m c2) / l. The product m c2 is rounded once per row, as in the tile
-// kernel's P, whose sum l divides by: the two roundings cancel. kMasked: only rows from r0 on see
-// this thread's key.
+// Adds 16 rows' exp2(s c2 - m c2) / l for each of the thread's two keys. The product m c2 is rounded
+// once per row, as in the tile kernel's P, whose sum l divides by: the two roundings cancel.
+// kMasked: only rows from r0 on see a key.
 template <bool kMasked>
-__device__ __forceinline__ void add_rows16(const uint32_t (&s)[16], const float* negm,
-                                           const float* inv, uint64_t c2, int r0,
-                                           uint64_t (&acc)[2]) {
+__device__ __forceinline__ void add_rows16(const uint32_t (&s)[kPair][16], const float* negm,
+                                           const float* inv, uint64_t c2, const int (&r0)[kPair],
+                                           int c0, uint64_t (&acc)[kPair][2]) {
 #pragma unroll
   for (int c = 0; c < 16; c += 4) {
     const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(negm + c);
     const ulonglong2 iv = *reinterpret_cast<const ulonglong2*>(inv + c);
 #pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-      float x, y;
-      halves_of(fma2(pair_of(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1])), c2,
-                     e ? m.y : m.x),
-                x, y);
-      x = fast_exp2(x);
-      y = fast_exp2(y);
-      if (kMasked) {
-        x = c + e >= r0 ? x : 0.f;
-        y = c + e + 1 >= r0 ? y : 0.f;
+    for (int i = 0; i < kPair; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        float x, y;
+        halves_of(fma2(pair_of(__uint_as_float(s[i][c + e]), __uint_as_float(s[i][c + e + 1])), c2,
+                       e ? m.y : m.x),
+                  x, y);
+        x = fast_exp2(x);
+        y = fast_exp2(y);
+        if (kMasked) {
+          x = c0 + c + e >= r0[i] ? x : 0.f;
+          y = c0 + c + e + 1 >= r0[i] ? y : 0.f;
+        }
+        acc[i][e / 2] = fma2(pair_of(x, y), e ? iv.y : iv.x, acc[i][e / 2]);
       }
-      acc[e / 2] = fma2(pair_of(x, y), e ? iv.y : iv.x, acc[e / 2]);
-    }
   }
 }
 
@@ -347,20 +359,28 @@ __device__ __forceinline__ void sum_weights(const WeightParams& p, const Span& s
   const int cols = one ? (p.rows + 15) & ~15 : kRowTile;
   const int32_t* bt = p.block_table + (int64_t)sp.seq * p.max_pages;
   const int64_t wrow = ((int64_t)sp.seq * p.Hkv + sp.head) * p.w_stride;
-  const uint32_t lane_base = (uint32_t)(32 * q) << 16;
+  const uint32_t scol = tbase + ((uint32_t)(32 * q) << 16) + kColS;
   const uint64_t c2 = pair_of(p.c2, p.c2);
+  const int L0 = sp.len - p.q_len;
   uint32_t step = 0;
   bool to = false;
-  for (int b = sp.b0; b < sp.b1; ++b) {
-    const int t = b * 128 + key;
-    const bool real = t < sp.len;
-    const int32_t pid = real ? __ldg(bt + t / kPage) : -1;
-    const bool valid = pid >= 0 && pid < p.num_pages;  // a bad page's keys got no weight
-    const float before = real && p.w_in != nullptr ? p.w_in[wrow + t] : 0.f;
-    // the first row that sees this key
-    const int64_t past = (int64_t)t - (sp.len - p.q_len);
-    const int first = p.causal && past > 0 ? (int)(past * p.G) : 0;
-    uint64_t acc[2] = {0ull, 0ull};
+  for (int b = sp.b0; b < sp.b1; b += kPair) {
+    int first[kPair];
+    bool real[kPair], valid[kPair];
+    float before[kPair];
+#pragma unroll
+    for (int i = 0; i < kPair; ++i) {
+      const int t = (b + i) * 128 + key;
+      real[i] = b + i < sp.b1 && t < sp.len;
+      const int32_t pid = real[i] ? __ldg(bt + t / kPage) : -1;
+      valid[i] = pid >= 0 && pid < p.num_pages;  // a bad page's keys got no weight
+      before[i] = real[i] && p.w_in != nullptr ? p.w_in[wrow + t] : 0.f;
+      first[i] = p.causal && t > L0 ? (t - L0) * p.G : 0;  // the first row that sees the key
+    }
+    // the first row that sees the pair's last key: a tile from there on is seen whole
+    const int last = (b + kPair) * 128 - 1;
+    const int whole = p.causal && last > L0 ? (last - L0) * p.G : 0;
+    uint64_t acc[kPair][2] = {};
     for (int tile = sp.first_tile(p, b); tile < sp.tiles; ++tile, ++step) {
       const uint32_t buf = step & 1u;
       const uint8_t* slot = smem + kOffQ + (one ? 0u : buf) * kQSlotBytes;
@@ -372,25 +392,35 @@ __device__ __forceinline__ void sum_weights(const WeightParams& p, const Span& s
       wait_bar_sleep(bars + 8 * (kBarSFull + buf), (step >> 1) & 1, to);
       tc_fence_after();
       __syncwarp();
-      const int r0 = first - tile * kRowTile;
-      const bool masked = __any_sync(0xffffffffu, r0 > 0);
-      // the tile's columns 16 at a time, the next 16 on their way while these are summed
-      const uint32_t col = tbase + lane_base + kColS + buf * kRowTile;
-      auto add = [&](uint32_t (&s)[16], int c) {
-        if (masked) add_rows16<true>(s, negm + c, inv + c, c2, r0 - c, acc);
-        else add_rows16<false>(s, negm + c, inv + c, c2, 0, acc);
+      const bool masked = whole > tile * kRowTile;
+      int r0[kPair];
+#pragma unroll
+      for (int i = 0; i < kPair; ++i) r0[i] = first[i] - tile * kRowTile;
+      const uint32_t col = scol + buf * (kPair * kRowTile);
+      auto load = [&](uint32_t (&s)[kPair][16], int c) {
+        tmem_ld16(col + c, s[0]);
+        tmem_ld16(col + kRowTile + c, s[1]);
       };
-      uint32_t s0[16], s1[16];
-      tmem_ld16(col, s0);
-      tmem_wait_ld_regs16(s0);
-      if (cols > 16) tmem_ld16(col + 16, s1);
+      auto add = [&](uint32_t (&s)[kPair][16], int c) {
+        if (masked) add_rows16<true>(s, negm + c, inv + c, c2, r0, c, acc);
+        else add_rows16<false>(s, negm + c, inv + c, c2, r0, c, acc);
+      };
+      auto wait = [&](uint32_t (&s)[kPair][16]) {
+        tmem_wait_ld_regs16(s[0]);
+        tmem_wait_ld_regs16(s[1]);
+      };
+      // the tile's columns 16 at a time, the next 16 on their way while these are summed
+      uint32_t s0[kPair][16], s1[kPair][16];
+      load(s0, 0);
+      wait(s0);
+      if (cols > 16) load(s1, 16);
       add(s0, 0);
       if (cols > 16) {
-        tmem_wait_ld_regs16(s1);
-        if (cols > 32) tmem_ld16(col + 32, s0);
+        wait(s1);
+        if (cols > 32) load(s0, 32);
         add(s1, 16);
         if (cols > 32) {
-          tmem_wait_ld_regs16(s0);
+          wait(s0);
           add(s0, 32);
         }
       }
@@ -399,15 +429,20 @@ __device__ __forceinline__ void sum_weights(const WeightParams& p, const Span& s
       if (lane == 0) {
         mbar_arrive(bars + 8 * (kBarSEmpty + buf));
         if (!one) mbar_arrive(bars + 8 * (kBarQEmpty + buf));
+        if (tile + 1 == sp.tiles)  // the pair's products are complete, its K consumed
+          for (int i = 0; i < min(kPair, sp.b1 - b); ++i)
+            mbar_arrive(bars + 8 * (kBarKEmpty + (uint32_t)(b - sp.b0 + i) % kStages));
       }
     }
-    if (real) {
-      float a[4];
-      halves_of(acc[0], a[0], a[1]);
-      halves_of(acc[1], a[2], a[3]);
-      const float sum = (a[0] + a[1]) + (a[2] + a[3]);
-      p.w_out[wrow + t] = valid ? before + sum : before;
-    }
+#pragma unroll
+    for (int i = 0; i < kPair; ++i)
+      if (real[i]) {
+        float a[4];
+        halves_of(acc[i][0], a[0], a[1]);
+        halves_of(acc[i][1], a[2], a[3]);
+        p.w_out[wrow + (b + i) * 128 + key] =
+            valid[i] ? before[i] + ((a[0] + a[1]) + (a[2] + a[3])) : before[i];
+      }
   }
   if (to && lane == 0) flag_status(p.status, KV_NVFP4_DEV_TIMEOUT);
 }
@@ -424,11 +459,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) weight_kernel(const Weig
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bars + 8 * (kBarKFull + s), 1);
-      mbar_init(bars + 8 * (kBarKEmpty + s), 1);
+      mbar_init(bars + 8 * (kBarKEmpty + s), kSumWarps);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bars + 8 * (kBarQFull + b), 1);
-      mbar_init(bars + 8 * (kBarQEmpty + b), 1 + kSumWarps);
+      mbar_init(bars + 8 * (kBarQEmpty + b), kSumWarps);
       mbar_init(bars + 8 * (kBarSFull + b), 1);
       mbar_init(bars + 8 * (kBarSEmpty + b), kSumWarps);
     }
@@ -496,6 +531,7 @@ cudaError_t launch_weights(const uint8_t* q_codes, const uint8_t* q_scales, cons
   const int64_t places = (int64_t)num_sms * kCtasPerSm;
   const int64_t per = (blocks + places - 1) / places;
   p.blocks_per_cta = (int32_t)(per < 1 ? 1 : per > 256 ? 256 : per);
+  if (p.blocks_per_cta > 1) p.blocks_per_cta = (p.blocks_per_cta + 1) & ~1;  // whole pairs
   const int64_t most = ((int64_t)max_seq_len + 127) / 128;
   p.chunks = (int32_t)((most + p.blocks_per_cta - 1) / p.blocks_per_cta);
   const int64_t grid = (int64_t)p.chunks * Hkv * num_seqs;
