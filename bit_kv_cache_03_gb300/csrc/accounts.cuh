@@ -7,8 +7,11 @@
 // needs no merge before it: it runs in the same launch as the merge of the outputs.
 //
 // For 6 rows the scores are 24 bytes per key and KV head, written once and read once, against 72
-// bytes of K to read again and a second Q.K^T; most of them stay in the L2 between the kernels (the
-// pages of the cache are marked first for eviction).
+// bytes of K to read again and a second Q.K^T (the call of 4 x 131072 tokens: 73.5 us, and 124 us
+// with the weight pass in its first form); most of them stay in the L2 between the kernels (the pages
+// of the cache are marked first for eviction). What is left beside the attention kernel, about 12 us,
+// is the latency of a launch, of the statistics and of three rounds of loads; the scores' stores cost
+// the attention kernel nothing that could be measured.
 #pragma once
 
 #include "nvfp4_device.cuh"
@@ -18,6 +21,9 @@ namespace kvnvfp4 {
 constexpr int kAccThreads = 256;
 constexpr int kAccPages = kAccThreads / 16;  // pages of a CTA: 16 threads per page, 4 keys each
 constexpr int kAccRows = 8;
+// Four (64 registers: the loads in flight spilled) took a decode call of 4 x 131072 tokens 78.0 us,
+// three 73.5, two 74.5; twice as many, shorter CTAs 76.3
+constexpr int kAccCtasPerSm = 3;
 
 struct AccountParams {
   const float* scores;     // [pages of all groups][heads per group][R][64]
@@ -137,9 +143,10 @@ inline AccountParams account_params(const float* scores, const float2* stats, co
   AccountParams a;
   a.scores = scores; a.stats = stats; a.w_in = w_in; a.w_out = w_out; a.w_stride = w_stride;
   a.R = R;
-  // four CTAs share an SM: about one round of CTAs, each putting the statistics together once
+  // about one round of CTAs, each putting the statistics together once
   const int64_t rounds = (total_tokens / (kAccPages * kPage) + num_seqs) * Hkv;
-  const int64_t per = (rounds + 4 * num_sms - 1) / (4 * num_sms);
+  const int64_t places = (int64_t)kAccCtasPerSm * num_sms;
+  const int64_t per = (rounds + places - 1) / places;
   a.per_cta = (int32_t)(per < 1 ? 1 : per > 64 ? 64 : per);
   const int64_t span = (int64_t)a.per_cta * kAccPages * kPage;
   a.parts = (int32_t)((max_seq_len + span - 1) / span);

@@ -1171,7 +1171,7 @@ __global__ void __launch_bounds__(32 * kMergeSlices, 2) merge_kernel(const Merge
 // split groups' rows (as merge_kernel), the others turn the stored scores into weights. The merge
 // and the weights need only what the attention kernel wrote, so they run side by side.
 static_assert(32 * kMergeSlices == kAccThreads, "one block size for both kinds of CTA");
-__global__ void __launch_bounds__(kAccThreads, 4) merge_weights_kernel(const MergeParams p,
+__global__ void __launch_bounds__(kAccThreads, kAccCtasPerSm) merge_weights_kernel(const MergeParams p,
                                                                        const AccountParams a,
                                                                        int32_t merges) {
   asm volatile("griddepcontrol.launch_dependents;");

@@ -963,7 +963,7 @@ __global__ void __launch_bounds__(32 * kTMergeSlices, 2) tile_merge_kernel(const
 // The second launch of an attention call with per-key weights and at most 8 rows per KV head: the
 // first `merges` CTAs merge the split groups' rows, the others turn the stored scores into weights.
 static_assert(32 * kTMergeSlices == kAccThreads, "one block size for both kinds of CTA");
-__global__ void __launch_bounds__(kAccThreads, 4) tile_merge_weights_kernel(const TMergeParams p,
+__global__ void __launch_bounds__(kAccThreads, kAccCtasPerSm) tile_merge_weights_kernel(const TMergeParams p,
                                                                             const AccountParams a,
                                                                             int32_t merges) {
   asm volatile("griddepcontrol.launch_dependents;");
