@@ -29,7 +29,7 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
                           const uint16_t* v_new, const float* rope, int32_t rope_max_pos,
                           int32_t rot_dim, uint8_t* pool_w, uint8_t* q_codes_out,
                           uint8_t* q_scales_out, bool late_tables, uint16_t* out16, float2* stats,
-                          float* scores, cudaStream_t stream);
+                          float* scores, float* part_l, cudaStream_t stream);
 cudaError_t launch_merge_weights(const void* groups, const int32_t* split_groups,
                                  int32_t num_split, const float* partials, uint16_t* out16,
                                  const float2* stats, const float* scores, const float* w_in,
@@ -56,7 +56,7 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
                         const int32_t* split_groups, int32_t num_split, float* partials,
                         float* out, int32_t* status, int32_t Hq, int32_t Hkv, int32_t q_len,
                         int32_t causal, int32_t grid, float sm_scale, uint16_t* out16,
-                        float2* stats, float* part_l, float* scores, cudaStream_t stream);
+                        float2* stats, float* part_l, cudaStream_t stream);
 cudaError_t launch_tile_merge_weights(const void* groups, const int32_t* split_groups,
                                       int32_t num_split, const float* partials,
                                       const float* part_l, uint16_t* out16, float2* stats,
@@ -493,7 +493,7 @@ static kv_nvfp4_status decode_step_impl(const kv_nvfp4_layout* L, const kv_nvfp4
       L->num_q_heads, L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
       (const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, d_rope_table, rope_max_pos,
       L->rot_dim, pool, q_codes_out, q_scales_out, late_tables, nullptr, nullptr,
-      nullptr, (cudaStream_t)stream);
+      nullptr, nullptr, (cudaStream_t)stream);
   return cuda_status(e);
 }
 
@@ -539,12 +539,13 @@ static bool plan_matches(const kv_nvfp4_layout* L, const kv_nvfp4_plan_info* pla
              (int64_t)plan->num_seqs * plan->num_row_groups * (tile ? L->num_kv_heads : 1);
 }
 
-// The second workspace of kv_nvfp4_decode_attn_weights: each row's softmax statistics, on the tile
-// kernel the fp32 row sums of the split groups' partials, and the scores where they are stored.
+// The second workspace of kv_nvfp4_decode_attn_weights: each row's softmax statistics, on a tile plan
+// the fp32 row sums of the split groups' partials, and the scores where they are stored.
 //
-// With at most 8 rows per KV head the attention kernel stores its scores for the weights (8 bytes
-// of traffic per row and key), with more the weight pass computes them again from K (72 bytes per
-// key whatever the rows). 4 x 131072 tokens, 6 rows per head: 124 us with the weight pass.
+// With at most 8 rows per KV head the decode kernel runs and stores its scores for the weights (8
+// bytes of traffic per row and key), with more the tile kernel runs and the weight pass computes the
+// scores again from K (72 bytes per key whatever the rows). 4 x 131072 tokens, 6 rows per head: 74 us
+// with stored scores, 124 us with the weight pass in its first form.
 struct WeightsWorkspace {
   uint64_t off_stats, off_part_l, off_scores, bytes;
   bool scores;
@@ -754,7 +755,7 @@ kv_nvfp4_status kv_nvfp4_decode_attn(const kv_nvfp4_layout* L, const kv_nvfp4_pl
                              (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
                              (float*)(ws + plan->off_partials), out, d_status, L->num_q_heads,
                              L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
-                             nullptr, nullptr, nullptr, nullptr, (cudaStream_t)stream);
+                             nullptr, nullptr, nullptr, (cudaStream_t)stream);
   } else {
     e = kvnvfp4::launch_decode(
         q_codes, q_scales, pool, d_block_table, max_pages, num_pages, ws + plan->off_groups,
@@ -763,7 +764,7 @@ kv_nvfp4_status kv_nvfp4_decode_attn(const kv_nvfp4_layout* L, const kv_nvfp4_pl
         (float*)(ws + plan->off_partials), out, d_status,
         L->num_q_heads, L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
         nullptr, nullptr, nullptr, nullptr, 0, 0, nullptr, nullptr, nullptr, false, nullptr,
-        nullptr, nullptr, (cudaStream_t)stream);
+        nullptr, nullptr, nullptr, (cudaStream_t)stream);
   }
   return cuda_status(e);
 }
@@ -804,37 +805,36 @@ kv_nvfp4_status kv_nvfp4_decode_attn_weights(
   float2* stats = (float2*)(ww + w.off_stats);
   float* scores = w.scores ? (float*)(ww + w.off_scores) : nullptr;
   const bool tile = tile_mode(L, plan->q_len);
+  const int32_t* split = (const int32_t*)(ws + plan->off_split);
+  float* partials = (float*)(ws + plan->off_partials);
+  float* part_l = tile ? (float*)(ww + w.off_part_l) : nullptr;
   cudaError_t e;
-  if (tile) {
+  if (scores == nullptr) {
     e = kvnvfp4::launch_tile(q_codes, q_scales, pool, d_block_table, max_pages, num_pages,
                              ws + plan->off_groups, ws + plan->off_segments,
-                             (const int32_t*)(ws + plan->off_cta),
-                             (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
-                             (float*)(ws + plan->off_partials), nullptr, d_status, L->num_q_heads,
-                             L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
-                             (uint16_t*)out, stats, (float*)(ww + w.off_part_l), scores,
-                             (cudaStream_t)stream);
-    if (e == cudaSuccess && scores != nullptr)
-      e = kvnvfp4::launch_tile_merge_weights(
-          ws + plan->off_groups, (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
-          (const float*)(ws + plan->off_partials), (const float*)(ww + w.off_part_l),
-          (uint16_t*)out, stats, scores, weights_in, weights_out, weights_stride, plan->num_seqs,
-          plan->max_seq_len, plan->total_kv_tokens, num_sms, L->num_q_heads, L->num_kv_heads, plan->q_len, sm_scale,
-          (cudaStream_t)stream);
+                             (const int32_t*)(ws + plan->off_cta), split, plan->num_split_groups,
+                             partials, nullptr, d_status, L->num_q_heads, L->num_kv_heads,
+                             plan->q_len, plan->causal, plan->grid, sm_scale, (uint16_t*)out, stats,
+                             part_l, (cudaStream_t)stream);
   } else {
     e = kvnvfp4::launch_decode(
         q_codes, q_scales, pool, d_block_table, max_pages, num_pages, ws + plan->off_groups,
-        ws + plan->off_segments, (const int32_t*)(ws + plan->off_cta),
-        (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
-        (float*)(ws + plan->off_partials), nullptr, d_status, L->num_q_heads, L->num_kv_heads,
+        ws + plan->off_segments, (const int32_t*)(ws + plan->off_cta), split,
+        plan->num_split_groups, partials, nullptr, d_status, L->num_q_heads, L->num_kv_heads,
         plan->q_len, plan->causal, plan->grid, sm_scale, nullptr, nullptr, nullptr, nullptr, 0, 0,
-        nullptr, nullptr, nullptr, false, (uint16_t*)out, stats, scores, (cudaStream_t)stream);
-    if (e == cudaSuccess && scores != nullptr)
-      e = kvnvfp4::launch_merge_weights(
-          ws + plan->off_groups, (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
-          (const float*)(ws + plan->off_partials), (uint16_t*)out, stats, scores, weights_in,
-          weights_out, weights_stride, plan->num_seqs, plan->max_seq_len, plan->total_kv_tokens, num_sms, L->num_q_heads,
-          L->num_kv_heads, plan->q_len, sm_scale, (cudaStream_t)stream);
+        nullptr, nullptr, nullptr, false, (uint16_t*)out, stats, scores, part_l,
+        (cudaStream_t)stream);
+    if (e == cudaSuccess)
+      e = tile ? kvnvfp4::launch_tile_merge_weights(
+                     ws + plan->off_groups, split, plan->num_split_groups, partials, part_l,
+                     (uint16_t*)out, stats, scores, weights_in, weights_out, weights_stride,
+                     plan->num_seqs, plan->max_seq_len, plan->total_kv_tokens, num_sms,
+                     L->num_q_heads, L->num_kv_heads, plan->q_len, sm_scale, (cudaStream_t)stream)
+               : kvnvfp4::launch_merge_weights(
+                     ws + plan->off_groups, split, plan->num_split_groups, partials,
+                     (uint16_t*)out, stats, scores, weights_in, weights_out, weights_stride,
+                     plan->num_seqs, plan->max_seq_len, plan->total_kv_tokens, num_sms,
+                     L->num_q_heads, L->num_kv_heads, plan->q_len, sm_scale, (cudaStream_t)stream);
   }
   if (e != cudaSuccess || scores != nullptr) return cuda_status(e);
   return cuda_status(kvnvfp4::launch_weights(

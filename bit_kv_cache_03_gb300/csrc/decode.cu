@@ -37,6 +37,12 @@
 // 16-key step the keys are taken in a fixed permutation, the same for P and V, that keeps the
 // shared-memory reads conflict-free.
 //
+// More than four KV heads (WIDE; attention with per-key weights only). A page block no longer fits a
+// stage, and the plan's groups are (sequence, KV head). A stage then takes four consecutive pages of
+// the segment's one head in the place of four heads of one page: "virtual head" v is page 4 j + v,
+// all with the same Q rows, each with its own softmax state, and the four states merge at the end of
+// the segment. The head's K scales of two pages are gathered into the scale-factor rows of a pair.
+//
 // Warp roles (320 threads): warp 0 bulk-copy producer, warp 1 Q.K^T issuer and TMEM owner, warps
 // 2..9 attention. Every wait is an mbarrier wait bounded in time; on a timeout the kernel records
 // KV_NVFP4_DEV_TIMEOUT and carries on, so it cannot hang.
@@ -73,8 +79,25 @@ constexpr int kBoundThreads = 384;
 constexpr int kStepQ = 0, kStepK = 8192, kStepV = 16384, kStepRope = 24576;
 static_assert(kStepRope + 8 * 128 * 4 <= kMaxHkv * 9216, "step slot larger than a stage");
 
+constexpr int kTileRows = 128;                     // rows of a tile plan's partials (WIDE)
+constexpr int kTilePartFloats = kTileRows * 128 + 2 * kTileRows;
 constexpr int kPsBytes = 1024;                     // per attention warp: 32 keys x (hi 16 B, lo 16 B)
 constexpr int kMergeHeadBytes = 8 * 32 * 16 + 2 * kRows * 4;  // O: 8 float4 per lane; m[8], l[8]
+
+// WIDE: a stage holds the four pages' pieces of one head where a page block has those of four heads,
+// the pages' ids in the place of the K scales, and behind them the K scales of the head's pair (or
+// lone head) as each page has them.
+constexpr int kWideStages = 4;
+constexpr int kWidePages = 4;
+constexpr int kWidePids = 4 * 4096, kWideKs = kStageBytes;
+constexpr int kWideStageBytes = kStageBytes + kWidePages * 1024;
+static_assert(kWideStages * kWideStageBytes <= kStages * kStageBytes, "the stages' shared memory");
+
+template <bool WIDE>
+struct Ring {  // stages, their size, and KV heads (or pages) per stage are p.Hkv or kWidePages
+  static constexpr uint32_t kNum = WIDE ? kWideStages : kStages;
+  static constexpr uint32_t kBytes = WIDE ? kWideStageBytes : kStageBytes;
+};
 
 // shared memory map
 constexpr int kOffStage = 0;
@@ -146,11 +169,12 @@ struct DecodeParams {
   // attention with per-key weights: bf16 rows instead of `out`, and each row's (m, 1 / l)
   uint16_t* out16;         // [num_seqs * q_len][Hq][128]
   float2* stats;           // [num_seqs][Hkv][G * q_len]
-  float* scores;           // [pages of all groups][Hkv][G * q_len][64 keys]
+  float* scores;           // [pages of all groups][Hkv][G * q_len][64 keys]; WIDE: [pages][rows][64]
+  float* part_l;           // WIDE: l per partial row, [num_partials][128]
 };
 
 struct SegInfo {
-  int seq, rg, len, n_seg, first_part, lo, hi, part, group, page0;
+  int seq, head, rg, len, n_seg, first_part, lo, hi, part, group, page0;
 };
 
 __device__ __forceinline__ SegInfo load_seg(const DecodeParams& p, int s) {
@@ -159,7 +183,7 @@ __device__ __forceinline__ SegInfo load_seg(const DecodeParams& p, int s) {
   const int4 g1 = p.groups[2 * seg.x + 1];
   SegInfo r;
   r.group = seg.x; r.lo = seg.y; r.hi = seg.z; r.part = seg.w;
-  r.seq = g0.x; r.rg = g0.z; r.len = g0.w;
+  r.seq = g0.x; r.head = g0.y; r.rg = g0.z; r.len = g0.w;
   r.n_seg = g1.x; r.first_part = g1.y; r.page0 = g1.w;
   return r;
 }
@@ -255,6 +279,77 @@ __device__ void producer(const DecodeParams& p, uint8_t* smem, int lane) {
   }
 }
 
+// The producer of the WIDE kernel: four pages of the segment's head per stage, four copies per page.
+__device__ void wide_producer(const DecodeParams& p, uint8_t* smem, int lane) {
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bars = sbase + kOffBars;
+  const int64_t blk = (int64_t)p.Hkv * 9216;
+  const uint64_t policy = l2_evict_first_policy();
+  uint32_t k = 0;
+  bool timed_out = false;
+  const int s_begin = p.cta_seg[blockIdx.x], s_end = p.cta_seg[blockIdx.x + 1];
+  for (int s = s_begin; s < s_end; ++s) {
+    const SegInfo sg = load_seg(p, s);
+    const uint32_t ksb = (sg.head | 1) >= p.Hkv ? 512u : 1024u;  // a last head without a partner
+    for (int p0 = sg.lo; p0 < sg.hi; p0 += 32) {
+      const int n = min(32, sg.hi - p0);
+      const int32_t mine =
+          (lane < n) ? p.block_table[(int64_t)sg.seq * p.max_pages + p0 + lane] : -1;
+      for (int j = 0; j < n; j += kWidePages, ++k) {
+        int32_t pid[kWidePages];
+#pragma unroll
+        for (int v = 0; v < kWidePages; ++v) pid[v] = __shfl_sync(0xffffffffu, mine, j + v);
+        if (lane == 0) {
+          const uint32_t st = k % kWideStages;
+          if (k >= kWideStages)
+            wait_bar(bars + 8 * (kBarStageEmpty + st), ((k / kWideStages) - 1) & 1, timed_out);
+          volatile int32_t* ids =
+              reinterpret_cast<volatile int32_t*>(smem + kOffStage + st * kWideStageBytes + kWidePids);
+          uint32_t bytes = 0;
+          bool bad = false;
+#pragma unroll
+          for (int v = 0; v < kWidePages; ++v) {
+            const bool valid = pid[v] >= 0 && pid[v] < p.num_pages;
+            bad |= !valid && j + v < n;
+            if (!valid) pid[v] = -1;  // skipped, like a page past the segment (P = 0, V = 0)
+            ids[v] = pid[v];
+            bytes += valid ? 4096u + ksb + 4096u + 512u : 0u;
+          }
+          if (bad) flag_status(p.status, KV_NVFP4_DEV_BAD_PAGE);
+          const uint32_t full = bars + 8 * (kBarStageFull + st);
+          if (bytes == 0u) {
+            mbar_arrive(full);
+          } else {
+            mbar_arrive_expect_tx(full, bytes);
+            const uint32_t dst = sbase + kOffStage + st * kWideStageBytes;
+#pragma unroll
+            for (int v = 0; v < kWidePages; ++v) {
+              if (pid[v] < 0) continue;
+              const uint8_t* src = p.pool + (int64_t)pid[v] * blk;
+              bulk_g2s_hint(dst + v * 4096, src + sg.head * 4096, 4096u, full, policy);
+              bulk_g2s_hint(dst + kWideKs + v * 1024, src + p.Hkv * 4096 + (sg.head >> 1) * 1024, ksb,
+                            full, policy);
+              bulk_g2s_hint(dst + kWidePages * 4608 + v * 4096,
+                            src + (int64_t)p.Hkv * 4608 + sg.head * 4096, 4096u, full, policy);
+              bulk_g2s_hint(dst + kWidePages * 8704 + v * 512,
+                            src + (int64_t)p.Hkv * 8704 + sg.head * 512, 512u, full, policy);
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  if (lane == 0) {
+    // no copy into this CTA's shared memory may still be in flight at exit
+    for (uint32_t st = 0; st < kWideStages && st < k; ++st) {
+      const uint32_t last = k - 1 - ((k - 1 - st) % kWideStages);
+      wait_bar(bars + 8 * (kBarStageFull + st), (last / kWideStages) & 1, timed_out);
+    }
+    if (timed_out) flag_status(p.status, KV_NVFP4_DEV_TIMEOUT);
+  }
+}
+
 // --------------------------------------------------------------------------------------------
 // Q.K^T warp. Per page the 32 lanes gather the page's K scales into the order of the MMA's scale
 // factors (row i of a (pair, k-half) tile holds the 4-byte scale groups of MMA rows i, 32 + i,
@@ -263,11 +358,13 @@ __device__ void producer(const DecodeParams& p, uint8_t* smem, int lane) {
 // the copies. The warp runs ahead of the attention warps as far as the stage ring and the two S
 // buffers allow.
 // --------------------------------------------------------------------------------------------
-template <bool FUSED>
+template <bool FUSED, bool WIDE>
 __device__ void qk_warp(const DecodeParams& p, uint8_t* smem, uint32_t tbase, int lane) {
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + kOffBars;
-  const int npairs = (p.Hkv + 1) >> 1;
+  constexpr uint32_t kNum = Ring<WIDE>::kNum;
+  const int npairs = WIDE ? kWidePages / 2 : (p.Hkv + 1) >> 1;
+  const int hb = WIDE ? kWidePages : p.Hkv;  // heads (or pages) of a stage
   uint32_t k = 0, ks = 0, sgi = 0;  // pages (S buffers), stage slots, segments
   bool timed_out = false;
   const int s_begin = p.cta_seg[blockIdx.x], s_end = p.cta_seg[blockIdx.x + 1];
@@ -276,28 +373,46 @@ __device__ void qk_warp(const DecodeParams& p, uint8_t* smem, uint32_t tbase, in
     if (FUSED) {
       // this warp's share of releasing the step slot; waiting for the slot first orders the
       // arrival after the slot's previous use was released (as for a page slot)
-      const uint32_t st = ks % kStages;
-      wait_bar(bars + 8 * (kBarStageFull + st), (ks / kStages) & 1, timed_out);
+      const uint32_t st = ks % kNum;
+      wait_bar(bars + 8 * (kBarStageFull + st), (ks / kNum) & 1, timed_out);
       if (lane == 0) mbar_arrive(bars + 8 * (kBarStageEmpty + st));
       ++ks;
     }
-    for (int j = 0; j < sg.hi - sg.lo; ++j, ++k, ++ks) {
-      const uint32_t st = ks % kStages, b = k % kSBufs;
-      wait_bar(bars + 8 * (kBarStageFull + st), (ks / kStages) & 1, timed_out);
+    const int n = WIDE ? (sg.hi - sg.lo + kWidePages - 1) / kWidePages : sg.hi - sg.lo;
+    for (int j = 0; j < n; ++j, ++k, ++ks) {
+      const uint32_t st = ks % kNum, b = k % kSBufs;
+      wait_bar(bars + 8 * (kBarStageFull + st), (ks / kNum) & 1, timed_out);
       // S buffer b free: the attention warps have read S of page k - kSBufs, so that page's MMAs
       // and scale copies are complete and staging tile b may be rewritten
       if (k >= kSBufs) wait_bar(bars + 8 * (kBarSFree + b), ((k / kSBufs) - 1) & 1, timed_out);
-      const uint32_t stage = sbase + kOffStage + st * kStageBytes;
+      const uint32_t stage = sbase + kOffStage + st * Ring<WIDE>::kBytes;
       const uint32_t sfs = sbase + kOffSfStage + b * 2048;
       // K scales: a full head pair's are already in the page in the scale-copy order (32 rows of
       // 16 bytes per k-half) and are copied straight from the stage; a last unpaired head's
       // 8-byte rows are widened into the staging tile first (the absent head's half is zero)
-      const bool half_pair = (p.Hkv & 1) != 0;
+      const bool half_pair = !WIDE && (p.Hkv & 1) != 0;
+      if (WIDE) {  // the head's scales of pages 2 pr and 2 pr + 1, 8 bytes of each row
+        const bool lone = (sg.head | 1) >= p.Hkv;
+#pragma unroll
+        for (int pr = 0; pr < kWidePages / 2; ++pr)
+#pragma unroll
+          for (int kh = 0; kh < 2; ++kh) {
+            uint2 v[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t raw = stage + kWideKs + (2 * pr + u) * 1024;
+              v[u] = lone ? lds64(raw + kh * 256 + lane * 8)
+                          : lds64(raw + kh * 512 + lane * 16 + (sg.head & 1) * 8);
+            }
+            sts128(sfs + (pr * 2 + kh) * 512 + lane * 16, v[0].x, v[0].y, v[1].x, v[1].y);
+          }
+        fence_async_smem();
+      }
       if (half_pair) {
         const int pr = npairs - 1;
 #pragma unroll
         for (int kh = 0; kh < 2; ++kh) {
-          const uint2 v = lds64(stage + p.Hkv * 4096 + pr * 1024 + kh * 256 + lane * 8);
+          const uint2 v = lds64(stage + hb * 4096 + pr * 1024 + kh * 256 + lane * 8);
           sts128(sfs + (pr * 2 + kh) * 512 + lane * 16, v.x, v.y, 0u, 0u);
         }
         fence_async_smem();
@@ -307,9 +422,9 @@ __device__ void qk_warp(const DecodeParams& p, uint8_t* smem, uint32_t tbase, in
         tc_fence_after();
         for (int pr = 0; pr < npairs; ++pr)
           for (int kh = 0; kh < 2; ++kh) {
-            const uint32_t src = (half_pair && pr == npairs - 1)
+            const uint32_t src = (WIDE || (half_pair && pr == npairs - 1))
                                      ? sfs + (pr * 2 + kh) * 512
-                                     : stage + p.Hkv * 4096 + pr * 1024 + kh * 512;
+                                     : stage + hb * 4096 + pr * 1024 + kh * 512;
             tmem_cp_32x128b_x4(tbase + kColSfa + b * 16 + pr * 8 + kh * 4, smem_desc(src, 16, 128));
           }
       }
@@ -394,18 +509,23 @@ __device__ __forceinline__ void s_issue(AttnCtx& c, uint32_t kk, uint32_t (&sr)[
 // below it are real (0 when the page was skipped).
 // ACC: the scores of the page's R real rows also go to `scores` (this head's [R][64] block), -inf
 // where the row does not see the key.
-template <int NR, bool ACC>
+template <int NR, bool ACC, bool WIDE>
 __device__ __forceinline__ bool s_softmax(AttnCtx& c, uint32_t kk, uint32_t kst, int page, int len,
                                           float* scores, int R,
                                           const RowVis& rv, uint32_t (&sr)[8], float (&m)[kRows],
                                           float (&lp)[kRows], uint32_t pt, int t, float c2,
                                           float& alpha_a, float& alpha_b, int& kv_lim) {
   tmem_wait_ld_regs(sr);
-  const uint32_t st = kst % kStages;
+  constexpr uint32_t kNum = Ring<WIDE>::kNum;
+  const uint32_t st = kst % kNum;
   // the Q.K^T warp saw this stage land; waiting here as well makes the V bytes and the page id
   // visible to this warp (the wait returns at once)
-  wait_bar(c.bars + 8 * (kBarStageFull + st), (kst / kStages) & 1, c.timed_out);
-  const bool pvalid = reinterpret_cast<const volatile int32_t*>(c.smem + kOffStagePid)[st] >= 0;
+  wait_bar(c.bars + 8 * (kBarStageFull + st), (kst / kNum) & 1, c.timed_out);
+  const volatile int32_t* ids =
+      WIDE ? reinterpret_cast<const volatile int32_t*>(c.smem + kOffStage + st * kWideStageBytes +
+                                                       kWidePids) + c.head
+           : reinterpret_cast<const volatile int32_t*>(c.smem + kOffStagePid) + st;
+  const bool pvalid = *ids >= 0;
   kv_lim = pvalid ? len - page * 64 : 0;
   if (!c.active) return false;
   uint32_t vmask = 0;  // bit i: this lane's key is visible to row i
@@ -419,7 +539,7 @@ __device__ __forceinline__ bool s_softmax(AttnCtx& c, uint32_t kk, uint32_t kst,
         if (kp <= __shfl_sync(0xffffffffu, rv.mylim, i)) vmask |= 1u << i;
     }
   }
-  if (ACC) {
+  if (ACC && scores != nullptr) {
 #pragma unroll
     for (int i = 0; i < NR; ++i)
       if (i < R)
@@ -742,9 +862,11 @@ __device__ __forceinline__ void fused_prologue(const DecodeParams& p, const SegI
   if (nrows > 0 && aw == 0 && lane == 0) mbar_arrive(bars + 8 * kBarKvReady);
 }
 
-template <int NR, bool FUSED, bool ACC>
+template <int NR, bool FUSED, bool ACC, bool WIDE>
 __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t tbase, int warp,
                                 int lane) {
+  constexpr uint32_t kNum = Ring<WIDE>::kNum;
+  const int hb = WIDE ? kWidePages : p.Hkv;  // heads (or pages) of a stage
   AttnCtx c;
   c.p = &p; c.smem = smem; c.sbase = smem_u32(smem); c.bars = c.sbase + kOffBars;
   c.tbase = tbase; c.lane = lane; c.qd = warp & 3;
@@ -754,7 +876,7 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
   c.half = c.qd >> 1;                 // TMEM lanes 64..127 hold the odd head of the pair
   c.head = 2 * c.pr + c.half;
   c.key0 = 32 * (c.qd & 1);
-  c.active = c.head < p.Hkv;
+  c.active = c.head < hb;
   c.gt = (aw & 3) * 32 + lane;
   c.timed_out = false;
   const int g = lane >> 2, t = lane & 3;  // mma fragment coordinates
@@ -778,7 +900,8 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
 
   for (int s = s_begin; s < s_end; ++s) {
     const SegInfo sg = load_seg(p, s);
-    const int n = sg.hi - sg.lo;
+    const int n = WIDE ? (sg.hi - sg.lo + kWidePages - 1) / kWidePages : sg.hi - sg.lo;
+    const int head = WIDE ? sg.head : c.head;  // the KV head of this warp's rows and keys
     const int row0 = sg.rg * kRows;
     const int L0 = sg.len - p.q_len;
     // largest visible key position of row lane % 8 of the tile (-1 for a padding row); rows are
@@ -793,15 +916,15 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
 
     // ---- this pair's Q tile (B operand of Q.K^T) and its scale factors ----
     if (FUSED) {
-      const uint32_t st = ks % kStages;
-      wait_bar(c.bars + 8 * (kBarStageFull + st), (ks / kStages) & 1, c.timed_out);
-      fused_prologue<NR>(p, sg, smem, smem + kOffStage + st * kStageBytes, c.sbase, c.bars, aw,
+      const uint32_t st = ks % kNum;
+      wait_bar(c.bars + 8 * (kBarStageFull + st), (ks / kNum) & 1, c.timed_out);
+      fused_prologue<NR>(p, sg, smem, smem + kOffStage + st * Ring<WIDE>::kBytes, c.sbase, c.bars, aw,
                          lane);
       if (lane == 0) mbar_arrive(c.bars + 8 * (kBarStageEmpty + st));  // slot read by this warp
       ++ks;
     } else if (c.gt < 64) {
       const int nrow = c.gt >> 2, ch = c.gt & 3;
-      const int hh = 2 * c.pr + (nrow >> 3), r = row0 + (nrow & 7);
+      const int hh = WIDE ? sg.head : 2 * c.pr + (nrow >> 3), r = row0 + (nrow & 7);
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
       if (hh < p.Hkv && r < rows_total) {
         const int64_t qrow = ((int64_t)sg.seq * p.q_len + r / p.G) * p.Hq + hh * p.G + r % p.G;
@@ -821,7 +944,7 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
           sf[4] = qs.y;
         }
       } else if (lane < 16) {
-        const int h2 = 2 * c.pr + (lane >> 3), r2 = row0 + (lane & 7);
+        const int h2 = WIDE ? sg.head : 2 * c.pr + (lane >> 3), r2 = row0 + (lane & 7);
         if (h2 < p.Hkv && r2 < rows_total) {
           const int64_t qrow = ((int64_t)sg.seq * p.q_len + r2 / p.G) * p.Hq + h2 * p.G + r2 % p.G;
           const uint2 qs = *reinterpret_cast<const uint2*>(p.q_scales + qrow * 8);
@@ -853,16 +976,18 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
     // max grew, then two 16-key steps of O += P V.
     const RowVis rv{mylim, lim_min, rows_mask};
     for (int j = 0; j < n; ++j, ++k, ++ks) {
-      const uint32_t st = ks % kStages;
+      const uint32_t st = ks % kNum;
       uint32_t sr[8];
       float alpha_a = 1.f, alpha_b = 1.f;
       int kv_lim = 0;
       s_issue(c, k, sr);
+      const int page = WIDE ? sg.lo + kWidePages * j + c.head : sg.lo + j;
       float* scores = nullptr;  // this page's and head's block
-      if (ACC)
-        scores = p.scores + (((int64_t)sg.page0 + sg.lo + j) * p.Hkv + c.head) * rows_total * kPage;
-      const bool grow = s_softmax<NR, ACC>(c, k, ks, sg.lo + j, sg.len, scores, rows_total, rv, sr,
-                                           m, lp, ps, t, c2, alpha_a, alpha_b, kv_lim);
+      if (ACC && (!WIDE || page < sg.hi))
+        scores = p.scores + (((int64_t)sg.page0 + page) * (WIDE ? 1 : p.Hkv) + (WIDE ? 0 : c.head)) *
+                                rows_total * kPage;
+      const bool grow = s_softmax<NR, ACC, WIDE>(c, k, ks, page, sg.len, scores, rows_total, rv, sr,
+                                                 m, lp, ps, t, c2, alpha_a, alpha_b, kv_lim);
       __syncwarp();
       if (grow) {  // entries 0, 2: row 2t; entries 1, 3: row 2t + 1
 #pragma unroll
@@ -872,9 +997,9 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
         }
       }
       if (c.active) {
-        const uint32_t stage = c.sbase + kOffStage + st * kStageBytes;
-        const uint32_t vc = stage + p.Hkv * 4608 + c.head * 4096 + 8 * g;  // codes of dims 16 g ..
-        const uint32_t vs = stage + p.Hkv * 8704 + c.head * 512 + g;       // scale of block g
+        const uint32_t stage = c.sbase + kOffStage + st * Ring<WIDE>::kBytes;
+        const uint32_t vc = stage + hb * 4608 + c.head * 4096 + 8 * g;  // codes of dims 16 g ..
+        const uint32_t vs = stage + hb * 8704 + c.head * 512 + g;       // scale of block g
         pv_page(smem, lm_addr, vc - c.sbase, vs - c.sbase, c.key0, kv_lim, vk0, vk1, acc);
       }
       // the page's S buffer and stage slot are released together (the Q.K^T warp runs pages
@@ -903,7 +1028,7 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
       const uint32_t mg = c.sbase + kOffMerge + c.head * kMergeHeadBytes;
       volatile float* mml =
           reinterpret_cast<volatile float*>(smem + kOffMerge + c.head * kMergeHeadBytes + 8 * 32 * 16);
-      const uint32_t hb = kNbHead0 + c.head;
+      const uint32_t nb = kNbHead0 + c.head;
       if (c.qd & 1) {
 #pragma unroll
         for (int q = 0; q < 8; ++q)
@@ -913,10 +1038,14 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
 #pragma unroll
           for (int i = 0; i < kRows; ++i) { mml[i] = m[i]; mml[kRows + i] = lp[i]; }
         }
-        named_barrier_sync(hb, 64);  // state written
-        named_barrier_sync(hb, 64);  // state read: the area is free for the next segment
+        named_barrier_sync(nb, 64);  // state written
+        named_barrier_sync(nb, 64);  // state read: the area is free for the next segment
+        if (WIDE) {  // the pages' states merge (below)
+          named_barrier_sync(kNbAttn, 32 * kAttnWarps);
+          named_barrier_sync(kNbAttn, 32 * kAttnWarps);
+        }
       } else {
-        named_barrier_sync(hb, 64);
+        named_barrier_sync(nb, 64);
         float M[2], L[2], f1[2], f2[2];
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
@@ -937,11 +1066,71 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
           o[0][2 * q + 1] = f1[0] * acc[q][2] + f2[0] * __uint_as_float(u.z);
           o[1][2 * q + 1] = f1[1] * acc[q][3] + f2[1] * __uint_as_float(u.w);
         }
-        named_barrier_sync(hb, 64);
+        named_barrier_sync(nb, 64);
+        if (WIDE) {
+          // the states of the four pages' places: 1 to 3 hand theirs to 0, in their merge areas
+          if (c.head > 0) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float* v = &o[q >> 2][4 * (q & 3)];
+              sts128(mg + (q * 32 + lane) * 16, __float_as_uint(v[0]), __float_as_uint(v[1]),
+                     __float_as_uint(v[2]), __float_as_uint(v[3]));
+            }
+            if (g == 0) {
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                mml[2 * t + hh] = M[hh];
+                mml[kRows + 2 * t + hh] = L[hh];
+              }
+            }
+          }
+          named_barrier_sync(kNbAttn, 32 * kAttnWarps);
+          if (c.head == 0) {
+#pragma unroll 1
+            for (int v = 1; v < kWidePages; ++v) {
+              const int area = kOffMerge + v * kMergeHeadBytes;
+              const volatile float* vml =
+                  reinterpret_cast<const volatile float*>(smem + area + 8 * 32 * 16);
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh) {
+                const float m2 = vml[2 * t + hh], l2 = vml[kRows + 2 * t + hh];
+                const float top = fmaxf(M[hh], m2);
+                const float fa = (M[hh] == -INFINITY) ? 0.f : fast_exp2((M[hh] - top) * c2);
+                const float fb = (m2 == -INFINITY) ? 0.f : fast_exp2((m2 - top) * c2);
+                M[hh] = top;
+                L[hh] = fa * L[hh] + fb * l2;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const uint4 u = lds128(c.sbase + area + ((4 * hh + q) * 32 + lane) * 16);
+                  o[hh][4 * q] = fa * o[hh][4 * q] + fb * __uint_as_float(u.x);
+                  o[hh][4 * q + 1] = fa * o[hh][4 * q + 1] + fb * __uint_as_float(u.y);
+                  o[hh][4 * q + 2] = fa * o[hh][4 * q + 2] + fb * __uint_as_float(u.z);
+                  o[hh][4 * q + 3] = fa * o[hh][4 * q + 3] + fb * __uint_as_float(u.w);
+                }
+              }
+            }
+          }
+          named_barrier_sync(kNbAttn, 32 * kAttnWarps);  // read: the areas are free
+          if (c.head > 0) continue;
+        }
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const int i = 2 * t + hh, r = row0 + i;
-          if (split) {
+          if (WIDE && split) {  // the tile kernel's partials, of which only the real rows exist
+            if (r < rows_total) {
+              float* part = p.partials + (int64_t)sg.part * kTilePartFloats;
+              float4* dst = reinterpret_cast<float4*>(part + i * 128 + 16 * g);
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                dst[q] = make_float4(o[hh][4 * q], o[hh][4 * q + 1], o[hh][4 * q + 2],
+                                     o[hh][4 * q + 3]);
+              if (g == 0) {
+                part[kTileRows * 128 + i] = M[hh];
+                part[kTileRows * 128 + kTileRows + i] = L[hh];
+                p.part_l[(int64_t)sg.part * kTileRows + i] = L[hh];
+              }
+            }
+          } else if (split) {
             float* part = p.partials + (int64_t)sg.part * part_stride + c.head * kPartHeadFloats;
             float4* dst = reinterpret_cast<float4*>(part + i * 128 + 16 * g);
 #pragma unroll
@@ -953,13 +1142,13 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
             }
           } else if (ACC) {
             if (r < rows_total) {
-              const int tok = r / p.G, qh = c.head * p.G + r % p.G;
+              const int tok = r / p.G, qh = head * p.G + r % p.G;
               const float inv = L[hh] > 0.f ? 1.f / L[hh] : 0.f;
               store_bf16x16(
                   p.out16 + (((int64_t)sg.seq * p.q_len + tok) * p.Hq + qh) * 128 + 16 * g, o[hh],
                   inv);
               if (g == 0)
-                p.stats[((int64_t)sg.seq * p.Hkv + c.head) * rows_total + r] =
+                p.stats[((int64_t)sg.seq * p.Hkv + head) * rows_total + r] =
                     make_float2(M[hh], inv);
             }
           } else if (r < rows_total && L[hh] > 0.f) {
@@ -981,8 +1170,9 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
 
 // NR: query rows computed per head (6 when no tile has more real rows, else all 8); FUSED: the
 // step's append is done in the kernel (kv_nvfp4_decode_step); ACC: rows go out in bf16 with their
-// softmax statistics, for the weight pass after it (kv_nvfp4_decode_attn_weights)
-template <int NR, bool FUSED, bool ACC>
+// softmax statistics, for the weights after it (kv_nvfp4_decode_attn_weights); WIDE: groups of one KV
+// head, four pages per stage
+template <int NR, bool FUSED, bool ACC, bool WIDE = false>
 __global__ void __launch_bounds__(kBoundThreads, 1) decode_kernel(const DecodeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1031,11 +1221,12 @@ __global__ void __launch_bounds__(kBoundThreads, 1) decode_kernel(const DecodePa
   const uint32_t tbase = *reinterpret_cast<volatile uint32_t*>(smem + kOffTmemSlot);
 
   if (warp == kWarpProducer) {
-    producer<FUSED>(p, smem, lane);
+    if constexpr (WIDE) wide_producer(p, smem, lane);
+    else producer<FUSED>(p, smem, lane);
   } else if (warp == kWarpMma) {
-    qk_warp<FUSED>(p, smem, tbase, lane);
+    qk_warp<FUSED, WIDE>(p, smem, tbase, lane);
   } else {
-    attention_warps<NR, FUSED, ACC>(p, smem, tbase, warp, lane);
+    attention_warps<NR, FUSED, ACC, WIDE>(p, smem, tbase, warp, lane);
   }
 
   if (warp == kWarpMma) {
@@ -1207,7 +1398,7 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
                           const uint16_t* v_new, const float* rope, int32_t rope_max_pos,
                           int32_t rot_dim, uint8_t* pool_w, uint8_t* q_codes_out,
                           uint8_t* q_scales_out, bool late_tables, uint16_t* out16, float2* stats,
-                          float* scores, cudaStream_t stream) {
+                          float* scores, float* part_l, cudaStream_t stream) {
   // the attribute belongs to each instantiation and each device: set once per device
   static bool attr_done[64] = {};
   int dev = 0;
@@ -1217,14 +1408,17 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
     const void* kernels[] = {
         (const void*)decode_kernel<8, false, false>, (const void*)decode_kernel<6, false, false>,
         (const void*)decode_kernel<8, true, false>,  (const void*)decode_kernel<6, true, false>,
-        (const void*)decode_kernel<8, false, true>,  (const void*)decode_kernel<6, false, true>};
+        (const void*)decode_kernel<8, false, true>,  (const void*)decode_kernel<6, false, true>,
+        (const void*)decode_kernel<8, false, true, true>,
+        (const void*)decode_kernel<6, false, true, true>};
     for (const void* kf : kernels)
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kf, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_done[dev] = true;
   }
-  if (Hkv < 1 || Hkv > kMaxHkv) return cudaErrorInvalidValue;
+  const bool wide = part_l != nullptr;  // a tile plan: groups of one KV head
+  if (Hkv < 1 || (Hkv > kMaxHkv && !wide)) return cudaErrorInvalidValue;
   DecodeParams p;
   p.q_codes = q_codes; p.q_scales = q_scales; p.pool = pool;
   p.block_table = block_table; p.max_pages = max_pages; p.num_pages = num_pages;
@@ -1238,7 +1432,7 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
   p.rope_max_pos = rope_max_pos; p.rot_dim = rot_dim; p.pool_w = pool_w;
   p.q_codes_out = q_codes_out; p.q_scales_out = q_scales_out;
   p.early_tables = late_tables ? 0 : 1;
-  p.out16 = out16; p.stats = stats; p.scores = scores;
+  p.out16 = out16; p.stats = stats; p.scores = scores; p.part_l = part_l;
   const bool fused = q_new != nullptr;
   if (grid <= 0) return cudaSuccess;
   // programmatic dependent launch: the kernel is set up while the previous kernel on the stream
@@ -1257,7 +1451,9 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
     // every tile has at most G * q_len real rows: with six or fewer, rows 6 and 7 are never computed
     const bool six = p.G * q_len <= 6;
     const cudaError_t le =
-        out16 ? (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, false, true>, p)
+        wide ? (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, false, true, true>, p)
+                    : cudaLaunchKernelEx(&dc, decode_kernel<8, false, true, true>, p))
+        : out16 ? (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, false, true>, p)
                      : cudaLaunchKernelEx(&dc, decode_kernel<8, false, true>, p))
         : fused ? (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, true, false>, p)
                        : cudaLaunchKernelEx(&dc, decode_kernel<8, true, false>, p))

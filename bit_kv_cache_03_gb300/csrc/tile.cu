@@ -146,11 +146,10 @@ struct TileParams {
   uint16_t* out16;         // [num_seqs * q_len][Hq][128]
   float2* stats;           // [num_seqs][Hkv][G * q_len]
   float* part_l;           // [num_partials][128]
-  float* scores;           // [pages of all groups][G * q_len][64 keys], or null (more than 8 rows)
 };
 
 struct TSeg {
-  int seq, head, rg, len, n_seg, first_part, lo, hi, part, page0;
+  int seq, head, rg, len, n_seg, first_part, lo, hi, part;
 };
 
 __device__ __forceinline__ TSeg t_load_seg(const TileParams& p, int s) {
@@ -160,7 +159,7 @@ __device__ __forceinline__ TSeg t_load_seg(const TileParams& p, int s) {
   TSeg r;
   r.lo = seg.y; r.hi = seg.z; r.part = seg.w;
   r.seq = g0.x; r.head = g0.y; r.rg = g0.z; r.len = g0.w;
-  r.n_seg = g1.x; r.first_part = g1.y; r.page0 = g1.w;
+  r.n_seg = g1.x; r.first_part = g1.y;
   return r;
 }
 
@@ -581,15 +580,6 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
 #pragma unroll
           for (int c = 0; c < kNc; ++c) sv[c] = c < nv ? sv[c] : __float_as_uint(-INFINITY);
         }
-        if (kAcc && kDup && p.scores != nullptr && row_ok && rr < 32 && page < sg.hi) {
-          // this row's 32 scores (lanes of real rows only: at most 8)
-          float4* dst = reinterpret_cast<float4*>(
-              p.scores + (((int64_t)sg.page0 + page) * rows_total + gr) * kPage + kofs);
-#pragma unroll
-          for (int c = 0; c < kNc; c += 4)
-            dst[c >> 2] = make_float4(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1]),
-                                      __uint_as_float(sv[c + 2]), __uint_as_float(sv[c + 3]));
-        }
         // this warp's max of the row: eight chains of three-input maxima, then a tree
         float mx[8];
 #pragma unroll
@@ -960,8 +950,8 @@ __global__ void __launch_bounds__(32 * kTMergeSlices, 2) tile_merge_kernel(const
   tile_merge_row<kAcc>(p, blockIdx.x, blockIdx.y);
 }
 
-// The second launch of an attention call with per-key weights and at most 8 rows per KV head: the
-// first `merges` CTAs merge the split groups' rows, the others turn the stored scores into weights.
+// The second launch of an attention call with per-key weights on a tile plan with at most 8 rows per
+// KV head (after the decode kernel's WIDE form, which leaves this kernel's partials): the first `merges` CTAs merge the split groups' rows, the others turn the stored scores into weights.
 static_assert(32 * kTMergeSlices == kAccThreads, "one block size for both kinds of CTA");
 __global__ void __launch_bounds__(kAccThreads, kAccCtasPerSm) tile_merge_weights_kernel(const TMergeParams p,
                                                                             const AccountParams a,
@@ -990,7 +980,7 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
                         const int32_t* split_groups, int32_t num_split, float* partials,
                         float* out, int32_t* status, int32_t Hq, int32_t Hkv, int32_t q_len,
                         int32_t causal, int32_t grid, float sm_scale, uint16_t* out16,
-                        float2* stats, float* part_l, float* scores, cudaStream_t stream) {
+                        float2* stats, float* part_l, cudaStream_t stream) {
   // the attribute belongs to each device: set once per device
   static bool attr_done[64] = {};
   int dev = 0;
@@ -1013,7 +1003,7 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
   p.partials = partials; p.out = out; p.status = status;
   p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.q_len = q_len; p.causal = causal;
   p.c2 = sm_scale * 1.4426950408889634f;
-  p.out16 = out16; p.stats = stats; p.part_l = part_l; p.scores = scores;
+  p.out16 = out16; p.stats = stats; p.part_l = part_l;
   if (grid <= 0) return cudaSuccess;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1031,7 +1021,7 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
     if (le != cudaSuccess) return le;
   }
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || num_split <= 0 || scores != nullptr) return e;
+  if (e != cudaSuccess || num_split <= 0) return e;
   TMergeParams mp;
   mp.groups = p.groups; mp.split = split_groups; mp.partials = partials; mp.out = out;
   mp.Hq = Hq; mp.G = p.G; mp.q_len = q_len; mp.c2 = p.c2;
@@ -1048,7 +1038,7 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
                : cudaLaunchKernelEx(&cfg, tile_merge_kernel<false>, mp);
 }
 
-// The launch after launch_tile with scores: the merge of the split groups and the weights.
+// The launch after launch_decode on a tile plan: the merge of the split groups and the weights.
 cudaError_t launch_tile_merge_weights(const void* groups, const int32_t* split_groups,
                                       int32_t num_split, const float* partials,
                                       const float* part_l, uint16_t* out16, float2* stats,

@@ -85,6 +85,10 @@ def kv():
     ([300, 40], 1, True, 64, 8, 1),                         # one head: a lone half pair
     ([300, 40], 2, True, 64, 9, 3),                         # odd heads
     ([0, 700, 2100], 1, True, 128, 32, 8),                  # eight KV heads: the tile kernel
+    ([0, 63, 64, 65, 191, 192, 193, 255, 256, 257, 320], 1, True, 64, 20, 5),  # a lone fifth head
+    ([5000, 7, 1300], 1, True, 64, 8, 8),                   # one row per head, many splits
+    ([700, 90], 2, True, 128, 24, 6),                       # 8 rows per head
+    ([700, 90], 2, False, 128, 24, 8),
     ([500, 0, 130], 3, True, 128, 20, 5),                   # odd heads above four, 12 rows
     ([2000, 37], 8, True, 256, 24, 4),                      # 48 rows: verify
     ([1000, 120], 8, False, 256, 24, 4),
@@ -131,9 +135,10 @@ def test_attend_weights_without_and_onto_the_accounts():
     a.check(np.nan_to_num(once))
 
 
-@pytest.mark.parametrize("q_len", [1, 8])
-def test_attend_weights_of_a_bad_page_stay(q_len):
-    w = synth.Workload("bad", [500], q_len=q_len, seed=9, pool_pages=12, chunk_tokens=128)
+@pytest.mark.parametrize("q_len,Hq,Hkv", [(1, 24, 4), (8, 24, 4), (1, 32, 8)])
+def test_attend_weights_of_a_bad_page_stay(q_len, Hq, Hkv):
+    w = synth.Workload("bad", [500], q_len=q_len, seed=9, pool_pages=12, chunk_tokens=128,
+                       q_heads=Hq, kv_heads=Hkv)
     a = Attend(w, 128)
     a.c.block_table[0, 3] = 12  # outside the pool
     a.run()
@@ -142,9 +147,10 @@ def test_attend_weights_of_a_bad_page_stay(q_len):
     a.check(a.held.cpu().numpy().astype(np.float64), [good], status=kv().DEV_BAD_PAGE)
 
 
-@pytest.mark.parametrize("q_len", [1, 8])
-def test_attend_weights_with_no_good_page(q_len):
-    w = synth.Workload("none", [100], q_len=q_len, seed=9, pool_pages=12, chunk_tokens=128)
+@pytest.mark.parametrize("q_len,Hq,Hkv", [(1, 24, 4), (8, 24, 4), (1, 32, 8)])
+def test_attend_weights_with_no_good_page(q_len, Hq, Hkv):
+    w = synth.Workload("none", [100], q_len=q_len, seed=9, pool_pages=12, chunk_tokens=128,
+                       q_heads=Hq, kv_heads=Hkv)
     a = Attend(w, 128)
     a.c.block_table.fill_(-1)
     a.run()
