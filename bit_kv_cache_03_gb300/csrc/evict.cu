@@ -570,7 +570,7 @@ struct CompactParams {
 // ahead 45 us, eight rows per thread at two CTAs per SM 59 us, two rows at six 55 us.
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 4;                                // rows in flight per thread
-constexpr int kMoveMaxCluster = 8;
+constexpr int kMoveMaxCluster = 16;
 constexpr int kMoveCtasPerSm = 3;
 constexpr int kMoveTile = kMoveThreads / 4 * kMoveRows;  // rows of a CTA per wave, codes and scales
 
@@ -728,14 +728,14 @@ cudaError_t launch_evict_select(const float* weights, int64_t w_stride, const in
     if (dev >= 0 && dev < 64) attr_done[dev] = true;
   }
   // The lengths are on the device, so the cluster is sized for the longest that the accounts hold:
-  // as few CTAs as keep the keys in shared memory, and more while SMs are left and a CTA has 2048
-  // keys. Large clusters pay only on an idle GPU (measured, us): 16 sets of 131072 slots 22.6 with
-  // C = 4 or 8, 34.7 with 16; 64 sets of 32768 22.6 / 18.5 / 18.0 / 28.8 / 77 with C = 1 .. 16; 512
-  // sets of 16384 41 with C = 1, 53 with 2, 542 with 16.
+  // as few CTAs as keep the keys in shared memory, and up to eight while SMs are left and a CTA has
+  // 2048 keys. Measured (us, C = 1, 2, 4, 8, 16): 4 sets of 4000 slots 12.3, 10.3, 10.3, 10.3, 14.4;
+  // 4 of 20000 16.4, 14.4, 12.3, 12.3, 14.4; 8 of 131072 (from C = 4) 22.6, 18.4, 22.6; 16 of 131072
+  // 22.6, 22.6, 35; 48 of 40000 24.6, 18.4, 18.5, 28, 62; 128 of 4000 12.3, 12.7, 22, 43, 137.
   const int64_t sets = (int64_t)num_seqs * (per_head ? Hkv : 1);
   int64_t C = 1;
   while (C < kSelMaxCluster &&
-         (C * kSelMaxCached < w_stride || (sets * C * 2 <= num_sms && C * 2048 < w_stride)))
+         (C * kSelMaxCached < w_stride || (C < 8 && sets * C * 2 <= num_sms && C * 2048 < w_stride)))
     C *= 2;
   const int64_t slice = (w_stride + C - 1) / C + 64;
   const int64_t cached = slice < kSelMaxCached ? slice : kSelMaxCached;
@@ -768,8 +768,18 @@ cudaError_t launch_evict_compact(const int32_t* index, int64_t index_stride, int
   const CompactParams p{index,     index_stride,  per_head,  seq_lens, keep,    block_table,
                         dst_table, max_pages,     dst_max_pages, num_pages, pool, weights,
                         w_stride,  Hkv,           status};
+  static bool attr_done[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
+  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        compact_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_done[dev] = true;
+  }
   // the kept counts are on the device: sized for the most that the index holds, a wave per CTA, and
-  // no more CTAs than run at once
+  // no more CTAs than run at once (one sequence, four heads, 16384 kept of 131072: 16.8 us with
+  // clusters of 16, 24.9 with 8)
   const int64_t units = (int64_t)num_seqs * Hkv * (weights != nullptr ? 3 : 2);
   int64_t C = 1;
   while (C < kMoveMaxCluster && C * kMoveTile < index_stride && units * C * 2 <= kMoveCtasPerSm * (int64_t)num_sms)
