@@ -539,7 +539,7 @@ __device__ __forceinline__ bool s_softmax(AttnCtx& c, uint32_t kk, uint32_t kst,
         if (kp <= __shfl_sync(0xffffffffu, rv.mylim, i)) vmask |= 1u << i;
     }
   }
-  if (ACC && scores != nullptr) {
+  if (ACC && (!WIDE || scores != nullptr)) {
 #pragma unroll
     for (int i = 0; i < NR; ++i)
       if (i < R)
