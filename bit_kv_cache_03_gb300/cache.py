@@ -47,6 +47,10 @@ class PagedNVFP4Cache:
         eviction)."""
         T = int(k.shape[0])
         if slots is not None:
+            self._check_current()
+            if slots.dtype != torch.int32 or not slots.is_contiguous() or slots.numel() != T or \
+                    slots.device != self.pool.device:
+                raise ValueError("slots must be device int32, one per token")
             kv_nvfp4_append_slots(self.layout, q, k, v, seq_ids, slots, positions, T, self.rope,
                                   self.max_pos, self.block_table, self.num_seqs, self.max_pages,
                                   self.num_pages, self.pool, q_codes, q_scales, self.status, stream)
@@ -85,18 +89,26 @@ class PagedNVFP4Cache:
     def attend_weights(self, q_codes, q_scales, out, weights, weights_in=None, sm_scale=None,
                        stream=None):
         """attend() with a bf16 `out`, adding every key's attention weight to `weights` (or writing
-        weights_in plus them). On the plan of the last plan()."""
+        weights_in plus them). On the plan of the last plan(), whose workspace and this call's belong
+        to one call at a time."""
         self._check_accounts(weights, weights_in)
+        if self.plan_info is None:
+            raise ValueError("attend_weights needs a plan()")
         if weights_in is not None and weights_in.shape != weights.shape:
             raise ValueError("weights_in must have the shape of weights")
-        if out.dtype != torch.bfloat16 or not out.is_contiguous():
-            raise ValueError("out must be a contiguous bfloat16 tensor")
+        rows = self.plan_info.num_seqs * self.plan_info.q_len * self.layout.num_q_heads
+        if out.dtype != torch.bfloat16 or not out.is_contiguous() or out.numel() != rows * 128 or \
+                out.device != weights.device:
+            raise ValueError("out must be a contiguous device bfloat16 [rows, num_q_heads, 128]")
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(128)
         need = kv_nvfp4_weights_workspace_bytes(self.layout, self.plan_info)
         if self.weights_workspace is None or self.weights_workspace.numel() < need:
-            self.weights_workspace = torch.empty(max(need, 256), dtype=torch.uint8,
-                                                 device=self.device)
+            # from the allocator's memory of the stream that works in it
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int)
+                                   else stream):
+                self.weights_workspace = torch.empty(max(need, 256), dtype=torch.uint8,
+                                                     device=self.device)
         kv_nvfp4_decode_attn_weights(
             self.layout, self.plan_info, self.workspace, self.weights_workspace,
             self.weights_workspace.numel(), q_codes, q_scales, sm_scale, self.pool, self.num_pages,
@@ -115,8 +127,10 @@ class PagedNVFP4Cache:
                     x.device != weights.device:
                 raise ValueError("seq_lens and keep must be device int32 [num_seqs]")
         if index.dtype != torch.int32 or not index.is_contiguous() or index.dim() != 3 or \
-                index.shape[0] != self.num_seqs or index.shape[1] not in (1, self.layout.num_kv_heads):
-            raise ValueError("index must be a contiguous int32 [num_seqs, num_kv_heads or 1, n]")
+                index.shape[0] != self.num_seqs or index.device != weights.device or \
+                index.shape[1] not in (1, self.layout.num_kv_heads):
+            raise ValueError("index must be a contiguous device int32 "
+                             "[num_seqs, num_kv_heads or 1, n]")
         per_head = index.shape[1] != 1
         kv_nvfp4_evict_select(self.layout, weights, weights.shape[2], seq_lens, keep, self.num_seqs,
                               per_head, sink, recent, index, index.shape[2], self.status, stream)
@@ -124,9 +138,16 @@ class PagedNVFP4Cache:
                                self.num_seqs, self.block_table, self.max_pages, self.num_pages,
                                self.pool, None, 0, weights, weights.shape[2], self.status, stream)
 
+    def _check_current(self):
+        # a launch goes to the current device; with the buffers of another one it would fault
+        if self.pool.device.index != torch.cuda.current_device():
+            raise ValueError("the cache's device is not the current one")
+
     def _check_accounts(self, *tensors):
+        self._check_current()
         for w in tensors:
-            if w is not None and (not w.is_cuda or w.dtype != torch.float32 or not w.is_contiguous() or w.dim() != 3 or
+            if w is not None and (w.device != self.pool.device or w.dtype != torch.float32 or
+                                  not w.is_contiguous() or w.dim() != 3 or
                                   tuple(w.shape[:2]) != (self.num_seqs, self.layout.num_kv_heads)):
                 raise ValueError("weights must be a contiguous device float32 "
                                  "[num_seqs, num_kv_heads, slots]")

@@ -61,9 +61,9 @@ cudaError_t launch_tile_merge_weights(const void* groups, const int32_t* split_g
                                       int32_t num_split, const float* partials,
                                       const float* part_l, uint16_t* out16, float2* stats,
                                       const float* scores, const float* w_in, float* w_out,
-                                      int64_t w_stride, int32_t num_seqs, int32_t max_seq_len, int64_t total_tokens,
-                                 int32_t num_sms,
-                                      int32_t Hq, int32_t Hkv, int32_t q_len, float sm_scale,
+                                      int64_t w_stride, int32_t num_seqs, int32_t max_seq_len,
+                                      int64_t total_tokens, int32_t num_sms, int32_t Hq,
+                                      int32_t Hkv, int32_t q_len, float sm_scale,
                                       cudaStream_t stream);
 cudaError_t launch_weights(const uint8_t* q_codes, const uint8_t* q_scales, const uint8_t* pool,
                            const int32_t* block_table, int32_t max_pages, int32_t num_pages,

@@ -1362,9 +1362,8 @@ __global__ void __launch_bounds__(32 * kMergeSlices, 2) merge_kernel(const Merge
 // split groups' rows (as merge_kernel), the others turn the stored scores into weights. The merge
 // and the weights need only what the attention kernel wrote, so they run side by side.
 static_assert(32 * kMergeSlices == kAccThreads, "one block size for both kinds of CTA");
-__global__ void __launch_bounds__(kAccThreads, kAccCtasPerSm) merge_weights_kernel(const MergeParams p,
-                                                                       const AccountParams a,
-                                                                       int32_t merges) {
+__global__ void __launch_bounds__(kAccThreads, kAccCtasPerSm)
+    merge_weights_kernel(const MergeParams p, const AccountParams a, int32_t merges) {
   asm volatile("griddepcontrol.launch_dependents;");
   if ((int)blockIdx.x < merges) {
     merge_row<false, true>(p, blockIdx.x / (p.Hkv * kRows), blockIdx.x % (p.Hkv * kRows));
@@ -1454,7 +1453,7 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
         wide ? (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, false, true, true>, p)
                     : cudaLaunchKernelEx(&dc, decode_kernel<8, false, true, true>, p))
         : out16 ? (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, false, true>, p)
-                     : cudaLaunchKernelEx(&dc, decode_kernel<8, false, true>, p))
+                       : cudaLaunchKernelEx(&dc, decode_kernel<8, false, true>, p))
         : fused ? (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, true, false>, p)
                        : cudaLaunchKernelEx(&dc, decode_kernel<8, true, false>, p))
                 : (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, false, false>, p)

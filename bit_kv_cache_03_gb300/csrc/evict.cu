@@ -357,7 +357,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   uint32_t* list = sh.hist[pass & 1];
   const uint32_t span = done > 0 ? 0xFFFFFFFFu >> (32 - done) : 0u, top = prefix + span;
   const int32_t part = (int32_t)((((int64_t)n + kSelWarps - 1) / kSelWarps + 127) & ~127);
-  const int32_t i_begin = max(i_lo, min(n, warp * part)), i_end = max(i_begin, min(n, (warp + 1) * part));
+  const int32_t i_begin = max(i_lo, min(n, warp * part));
+  const int32_t i_end = max(i_begin, min(n, (warp + 1) * part));
   {
     int32_t above = 0, equal = 0;
     each_key(i_begin, i_end, lane, 32, [&](uint32_t k, int32_t i) {
@@ -782,7 +783,8 @@ cudaError_t launch_evict_compact(const int32_t* index, int64_t index_stride, int
   // clusters of 16, 24.9 with 8)
   const int64_t units = (int64_t)num_seqs * Hkv * (weights != nullptr ? 3 : 2);
   int64_t C = 1;
-  while (C < kMoveMaxCluster && C * kMoveTile < index_stride && units * C * 2 <= kMoveCtasPerSm * (int64_t)num_sms)
+  while (C < kMoveMaxCluster && C * kMoveTile < index_stride &&
+         units * C * 2 <= kMoveCtasPerSm * (int64_t)num_sms)
     C *= 2;
   if (units * C > 0x7FFFFFFF) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[1];

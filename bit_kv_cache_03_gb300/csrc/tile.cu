@@ -951,11 +951,11 @@ __global__ void __launch_bounds__(32 * kTMergeSlices, 2) tile_merge_kernel(const
 }
 
 // The second launch of an attention call with per-key weights on a tile plan with at most 8 rows per
-// KV head (after the decode kernel's WIDE form, which leaves this kernel's partials): the first `merges` CTAs merge the split groups' rows, the others turn the stored scores into weights.
+// KV head (after the decode kernel's WIDE form, which leaves this file's partials): the first `merges`
+// CTAs merge the split groups' rows, the others turn the stored scores into weights.
 static_assert(32 * kTMergeSlices == kAccThreads, "one block size for both kinds of CTA");
-__global__ void __launch_bounds__(kAccThreads, kAccCtasPerSm) tile_merge_weights_kernel(const TMergeParams p,
-                                                                            const AccountParams a,
-                                                                            int32_t merges) {
+__global__ void __launch_bounds__(kAccThreads, kAccCtasPerSm)
+    tile_merge_weights_kernel(const TMergeParams p, const AccountParams a, int32_t merges) {
   asm volatile("griddepcontrol.launch_dependents;");
   if ((int)blockIdx.x < merges) {
     tile_merge_row<true>(p, blockIdx.x / a.R, blockIdx.x % a.R);
@@ -1043,9 +1043,9 @@ cudaError_t launch_tile_merge_weights(const void* groups, const int32_t* split_g
                                       int32_t num_split, const float* partials,
                                       const float* part_l, uint16_t* out16, float2* stats,
                                       const float* scores, const float* w_in, float* w_out,
-                                      int64_t w_stride, int32_t num_seqs, int32_t max_seq_len, int64_t total_tokens,
-                                 int32_t num_sms,
-                                      int32_t Hq, int32_t Hkv, int32_t q_len, float sm_scale,
+                                      int64_t w_stride, int32_t num_seqs, int32_t max_seq_len,
+                                      int64_t total_tokens, int32_t num_sms, int32_t Hq,
+                                      int32_t Hkv, int32_t q_len, float sm_scale,
                                       cudaStream_t stream) {
   TMergeParams mp;
   mp.groups = static_cast<const int4*>(groups); mp.split = split_groups; mp.partials = partials;

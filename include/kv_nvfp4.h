@@ -312,9 +312,10 @@ kv_nvfp4_status kv_nvfp4_decode_attn_weights(
  * as evict_select's does. All other slots keep their bytes.
  *   d_block_table: DEVICE int32 [num_seqs][max_pages], the old cache
  *   d_dst_block_table: DEVICE int32 [num_seqs][dst_max_pages], the new one, whose first
- *              ceil(kept / 64) pages per sequence belong to no other table row; or null (and
- *              dst_max_pages 0): in place, in the old cache's pages. Pages shared by several rows
- *              of d_block_table (a common prefix) must not be compacted in place.
+ *              ceil(kept / 64) pages per sequence stand nowhere else in it, and in d_block_table
+ *              nowhere but at the same place of the same sequence; or null (and dst_max_pages 0):
+ *              in place, in the old cache's pages. Pages shared by several rows of d_block_table
+ *              (a common prefix) must not be compacted in place.
  *   weights:   DEVICE fp32 as above, moved in place like the rows, with 0 for kept <= t < seq_len
  *              (ready for new tokens in those slots); or null
  * A sequence with a negative length or keep, kept above index_stride or dst_max_pages * 64, or a

@@ -510,6 +510,55 @@ def test_the_cache_checks_its_arguments():
             c.evict(w, lens, keep, ix)
 
 
+def test_the_cache_refuses_other_devices_and_sizes(monkeypatch):
+    k = kv()
+    c = k.PagedNVFP4Cache(4, np.arange(4, dtype=np.int32).reshape(2, 2), 100, 4, 2)
+    w = c.weight_accounts()
+    i32 = torch.tensor([5, 5], dtype=torch.int32, device="cuda")
+    index = torch.zeros(2, 2, 5, dtype=torch.int32, device="cuda")
+    out = torch.zeros(2, 4, 128, dtype=torch.bfloat16, device="cuda")
+    qc, qs = c.quantized_q_buffers(2)
+    x = torch.zeros(2, 2, 128, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):  # no plan yet
+        c.attend_weights(qc, qs, out, w)
+    c.plan([10, 10], 1)
+    for bad in (out.cpu(), out[:1]):
+        with pytest.raises(ValueError):
+            c.attend_weights(qc, qs, bad, w)
+    with pytest.raises(ValueError):
+        c.evict(w, i32, i32, index.cpu())
+    for slots in (i32.long(), i32[:1], i32.cpu()):
+        with pytest.raises(ValueError):
+            c.append(x, x, i32, i32, slots=slots)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError):
+        c.attend_weights(qc, qs, out, w)
+    with pytest.raises(ValueError):
+        c.evict(w, i32, i32, index)
+    with pytest.raises(ValueError):
+        c.append(x, x, i32, i32, slots=i32)
+
+
+def test_attend_weights_grows_its_workspace_on_the_stream_it_is_given():
+    k = kv()
+    c = k.PagedNVFP4Cache(32, np.arange(32, dtype=np.int32).reshape(2, 16), 1100, 4, 2)
+    c.pool.zero_()
+    w = c.weight_accounts()
+    qc, qs = c.quantized_q_buffers(2)
+    qc.zero_(), qs.zero_()  # scores of 0: every key of n gets 1 / n from each of the two rows
+    out = torch.empty(2, 4, 128, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    for n, stream in ((64, side), (1024, side.cuda_stream), (1024, None)):
+        c.plan([n, n], 1)
+        w.zero_()
+        torch.cuda.synchronize()
+        c.attend_weights(qc, qs, out, w, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(w[..., :n], torch.full_like(w[..., :n], 2.0 / n))  # powers of two: exact
+        assert not w[..., n:].any() and not out.any()
+    assert int(c.status.item()) == 0
+
+
 # ---- together ----------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("per_head", [True, False])
