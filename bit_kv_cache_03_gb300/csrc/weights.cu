@@ -531,7 +531,6 @@ cudaError_t launch_weights(const uint8_t* q_codes, const uint8_t* q_scales, cons
   const int64_t places = (int64_t)num_sms * kCtasPerSm;
   const int64_t per = (blocks + places - 1) / places;
   p.blocks_per_cta = (int32_t)(per < 1 ? 1 : per > 256 ? 256 : per);
-  if (p.blocks_per_cta > 1) p.blocks_per_cta = (p.blocks_per_cta + 1) & ~1;  // whole pairs
   const int64_t most = ((int64_t)max_seq_len + 127) / 128;
   p.chunks = (int32_t)((most + p.blocks_per_cta - 1) / p.blocks_per_cta);
   const int64_t grid = (int64_t)p.chunks * Hkv * num_seqs;
