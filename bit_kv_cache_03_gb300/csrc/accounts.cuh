@@ -1,17 +1,19 @@
-// Per-key weights from stored scores, shared by the decode and the tile path of
-// kv_nvfp4_decode_attn_weights when a KV head has at most 8 query rows. The attention kernel leaves
-// the raw scores of every page it visits (-inf where a row does not see the key), [page][R rows][64
-// keys] per KV head; here one thread takes four keys and adds, row by row,
+// Per-key weights from stored scores, for kv_nvfp4_decode_attn_weights when a KV head has at most 8
+// query rows: in the launch after either form of the decode kernel (with groups over all KV heads, or
+// of one). The attention kernel leaves the raw scores of every page it visits (-inf where a row does
+// not see the key), [page][R rows][64 keys] per KV head; here one thread takes four keys and adds, row
+// by row,
 //   exp2((s - m_r) c2) / l_r
 // onto the accounts. The row statistics come from the split-K partials themselves, so this work
 // needs no merge before it: it runs in the same launch as the merge of the outputs.
 //
 // For 6 rows the scores are 24 bytes per key and KV head, written once and read once, against 72
-// bytes of K to read again and a second Q.K^T (the call of 4 x 131072 tokens: 73.5 us, and 124 us
+// bytes of K to read again and a second Q.K^T (the call of 4 x 131072 tokens: 75.7 us, and 124 us
 // with the weight pass in its first form); most of them stay in the L2 between the kernels (the pages
-// of the cache are marked first for eviction). What is left beside the attention kernel, about 12 us,
-// is the latency of a launch, of the statistics and of three rounds of loads; the scores' stores cost
-// the attention kernel nothing that could be measured.
+// of the cache are marked first for eviction). The scores' stores cost the attention kernel nothing
+// that could be measured; what is left beside it, about 13 us, is a launch, the statistics and the
+// way of 50 MB of scores through the L2. It is not the loads' latency: bulk copies of the scores into
+// a ring in shared memory, two to four times as many bytes in flight, took the same 75.7 us.
 #pragma once
 
 #include "nvfp4_device.cuh"
@@ -22,7 +24,7 @@ constexpr int kAccThreads = 256;
 constexpr int kAccPages = kAccThreads / 16;  // pages of a CTA: 16 threads per page, 4 keys each
 constexpr int kAccRows = 8;
 // Four (64 registers: the loads in flight spilled) took a decode call of 4 x 131072 tokens 78.0 us,
-// three 73.5, two 74.5; twice as many, shorter CTAs 76.3
+// three 73.5, two 74.5; twice as many, shorter CTAs 76.3 (in one run; 75.7 for three since)
 constexpr int kAccCtasPerSm = 3;
 
 struct AccountParams {

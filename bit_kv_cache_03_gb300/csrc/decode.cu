@@ -41,7 +41,9 @@
 // stage, and the plan's groups are (sequence, KV head). A stage then takes four consecutive pages of
 // the segment's one head in the place of four heads of one page: "virtual head" v is page 4 j + v,
 // all with the same Q rows, each with its own softmax state, and the four states merge at the end of
-// the segment. The head's K scales of two pages are gathered into the scale-factor rows of a pair.
+// the segment. The head's K scales of two pages are gathered into the scale-factor rows of a pair. With
+// at most 8 of its 128 rows real, the tile kernel took 38 us (caches cold) for 8 sequences of up to
+// 32769 tokens, 32 query and 8 KV heads, this form 33; the call went from 39 to 33 us.
 //
 // Warp roles (320 threads): warp 0 bulk-copy producer, warp 1 Q.K^T issuer and TMEM owner, warps
 // 2..9 attention. Every wait is an mbarrier wait bounded in time; on a timeout the kernel records

@@ -65,7 +65,7 @@ __device__ __forceinline__ float set_weight(const float* w, int64_t stride, int 
 // Bounds: the weights are read once (8.4 MB for 4 sequences x 4 KV heads x 131072 slots: 1.2 us of
 // HBM time), but the passes over the cached keys, each a few instructions per key on the few SMs of
 // a cluster, and the meetings follow one another: load 4 us, digit 1 and its sum 4, exchange and
-// search 6, listing 2.5 of that case's 22.6 us. One CTA per set without a cluster took 386 us there
+// search 6, listing 2.5 of that case's 22.6 us (the launch and the clusters' start are the rest). One CTA per set without a cluster took 386 us there
 // (2838 us for one set of 600000 slots and four heads, now 31 us).
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048, kCoarse = kBins / 64;
@@ -568,7 +568,9 @@ struct CompactParams {
 // 16-byte pieces in sectors that hold a neighbour's piece as well, its scales two words in two more,
 // and DRAM gives 64 bytes at a time. 4 x 4 sets, 16384 kept of 131072: 78 MB of rows move, 184 MB
 // cross the memory bus, in 43 us (4.3 TB/s). One CTA per part took 272 us, waves without reads
-// ahead 45 us, eight rows per thread at two CTAs per SM 59 us, two rows at six 55 us.
+// ahead 45 us, eight rows per thread at two CTAs per SM 59 us, two rows at six 55 us, clusters of nine
+// instead of eight (432 CTAs, not 384) the same 43. A gather of the same K and V rows into another
+// buffer, without any order or meeting, takes 37 us whatever its grid.
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 4;                                // rows in flight per thread
 constexpr int kMoveMaxCluster = 16;
