@@ -559,6 +559,48 @@ def test_attend_weights_grows_its_workspace_on_the_stream_it_is_given():
     assert int(c.status.item()) == 0
 
 
+@pytest.mark.parametrize("q_len,Hq,Hkv", [(1, 24, 4), (1, 16, 8), (8, 24, 4)])
+def test_offsets_beyond_32_bits(q_len, Hq, Hkv):
+    # the same session in a pool of 5 GB, on its last pages, with accounts 600 M slots apart, and in a
+    # small one: the same bits
+    k = kv()
+    gen = torch.Generator(device="cuda").manual_seed(q_len + Hkv)
+    many = (5 << 30) // (9216 * Hkv)
+    n, stride = 170, 600_000_000
+    caches = [k.PagedNVFP4Cache(pages, [table], 512, Hq, Hkv) for pages, table in
+              ((many, [many - 1, 2, many - 70]), (3, [0, 1, 2]))]
+    rand = lambda *d: torch.randn(*d, device="cuda", generator=gen).bfloat16()  # noqa: E731
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    kk, vv, q = rand(n, Hkv, 128), rand(n, Hkv, 128), rand(n, Hq, 128)
+    k2, v2 = rand(1, Hkv, 128), rand(1, Hkv, 128)
+    seen = []
+    for c, apart in zip(caches, (stride, 192)):
+        qc, qs = c.quantized_q_buffers(n)
+        c.append(kk, vv, torch.zeros(n, dtype=torch.int32, device="cuda"),
+                 torch.arange(n, dtype=torch.int32, device="cuda"), q, qc, qs)
+        w = torch.empty(1, Hkv, apart, device="cuda")
+        w[..., :192] = 0.25
+        out = torch.empty(q_len, Hq, 128, dtype=torch.bfloat16, device="cuda")
+        c.plan([n], q_len, True, 64)
+        c.attend_weights(qc.view(n, -1)[-q_len:], qs.view(n, -1)[-q_len:], out, w)
+        index = torch.zeros(1, Hkv, 100, dtype=torch.int32, device="cuda")
+        before = w[..., :192].clone()
+        c.evict(w, i32([n]), i32([100]), index, 4, 20)
+        c.append(k2, v2, i32([0]), i32([n]), slots=i32([100]))
+        torch.cuda.synchronize()
+        assert int(c.status.item()) == 0
+        pages = c.pool.view(c.num_pages, -1)[c.block_table[0].long()].clone()
+        # bytes behind the last token were never written
+        pages[2, :] = 0
+        seen.append((out, before, w[..., :192].clone(), index, pages))
+        c.pool = w = None
+    (out, before, w, index, pages), other = seen
+    assert torch.equal(out, other[0]) and torch.equal(index, other[3])
+    assert torch.equal(before, other[1]) and torch.equal(w, other[2])
+    assert before[..., :n].sum() > 0.25 * n * Hkv  # weight was added
+    assert torch.equal(pages, other[4])
+
+
 # ---- together ----------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("per_head", [True, False])
