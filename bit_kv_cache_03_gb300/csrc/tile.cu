@@ -621,18 +621,28 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
         // taken as 0)
         const float mc2 = m == -INFINITY ? 0.f : m * c2;
         uint32_t pk[kNc / 2];
-        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t l2[2] = {};  // kAcc: the sums of even and odd columns, in two chains
+        const uint64_t c2c2 = pair_of(c2, c2), mm = pair_of(-mc2, -mc2);
 #pragma unroll
         for (int c = 0; c < kNc; c += 2) {
-          const float p0 = fast_exp2(fmaf(__uint_as_float(sv[c]), c2, -mc2));
-          const float p1 = fast_exp2(fmaf(__uint_as_float(sv[c + 1]), c2, -mc2));
-          pk[c >> 1] = pack_f16x2(p0, p1);
-          if (kAcc) {
-            l4[c & 2] += p0;
-            l4[(c & 2) + 1] += p1;
+          float p0, p1;
+          if (kDup) {  // (in pairs: verify 110 -> 107 us; with all of a page's columns it spills)
+            halves_of(fma2(pair_of(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), c2c2, mm),
+                      p0, p1);
+            p0 = fast_exp2(p0);
+            p1 = fast_exp2(p1);
+          } else {
+            p0 = fast_exp2(fmaf(__uint_as_float(sv[c]), c2, -mc2));
+            p1 = fast_exp2(fmaf(__uint_as_float(sv[c + 1]), c2, -mc2));
           }
+          pk[c >> 1] = pack_f16x2(p0, p1);
+          if (kAcc) l2[(c >> 1) & 1] = add2(l2[(c >> 1) & 1], pair_of(p0, p1));
         }
-        if (kAcc) ls = fmaf(ls, alpha, (l4[0] + l4[1]) + (l4[2] + l4[3]));
+        if (kAcc) {
+          float even, odd;
+          halves_of(add2(l2[0], l2[1]), even, odd);
+          ls = fmaf(ls, alpha, even + odd);
+        }
         if constexpr (kDup) {
           tmem_st16(scol, pk);
           // zeros over the same keys of the other page (columns no warp of this quadrant reads)
@@ -835,7 +845,8 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const TileParams p) 
 
 // --------------------------------------------------------------------------------------------
 // Split-K merge of the tile kernel's partials (second launch): one CTA per (split group, row of
-// the tile); its 256 threads are 8 slices of the group's partials x 32 four-dim columns:
+// the tile), or one warp; its kSlices warps are slices of the group's partials, each 32 four-dim
+// columns wide:
 //   M = max_q m_q,  L = sum_q 2^((m_q - M) c2) l_q,  o = sum_q 2^((m_q - M) c2) O_q / L.
 // --------------------------------------------------------------------------------------------
 struct TMergeParams {
@@ -854,30 +865,30 @@ struct TMergeParams {
 constexpr int kTMergeSlices = 8;
 constexpr int kTMergePerRound = 8;  // partials a slice requests at once (64 per CTA and round)
 
-template <bool kAcc>
+template <bool kAcc, int kSlices>
 __device__ __forceinline__ void tile_merge_row(const TMergeParams& p, int split_index, int i) {
-  __shared__ float s_m[kTMergeSlices], s_l[kTMergeSlices], s_w[kTMergeSlices];
-  __shared__ float4 s_o[kTMergeSlices][32];
+  __shared__ float s_m[kSlices], s_l[kSlices], s_w[kSlices];
+  __shared__ float4 s_o[kSlices][32];
   const int gi = p.split[split_index];  // plan tables: written before the attention launch
   const int4 g0 = p.groups[2 * gi], g1 = p.groups[2 * gi + 1];
   const int r = g0.z * kTRows + i, head = g0.y;
   // the partials are visible only after the attention grid has completed and flushed
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (r >= p.G * p.q_len) return;  // uniform over the CTA
+  if (i >= kTRows || r >= p.G * p.q_len) return;  // uniform over the row's threads
   const int n_seg = g1.x;
-  const int slice = threadIdx.x >> 5, d4 = threadIdx.x & 31;
+  const int slice = kSlices == 1 ? 0 : threadIdx.x >> 5, d4 = threadIdx.x & 31;
   const float* base = p.partials + (int64_t)g1.y * kTPartFloats;
   const float* lbase = kAcc ? p.part_l + (int64_t)g1.y * kTRows + i : nullptr;
   // per round a slice requests its partials q = q0 + 8 u (u < 8) at once (one L2 round trip for a
   // group of up to 64 segments) and combines them with independent weights
   float M = -INFINITY, L = 0.f, W = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int q0 = slice; q0 < n_seg; q0 += kTMergeSlices * kTMergePerRound) {
+  for (int q0 = slice; q0 < n_seg; q0 += kSlices * kTMergePerRound) {
     float mq[kTMergePerRound], lq[kTMergePerRound], wq[kTMergePerRound];
     float4 ov[kTMergePerRound];
 #pragma unroll
     for (int u = 0; u < kTMergePerRound; ++u) {
-      const int q = q0 + kTMergeSlices * u;
+      const int q = q0 + kSlices * u;
       mq[u] = -INFINITY;
       lq[u] = 0.f;
       ov[u] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -907,17 +918,20 @@ __device__ __forceinline__ void tile_merge_row(const TMergeParams& p, int split_
     }
     M = mn;
   }
-  s_o[slice][d4] = O;
-  if (d4 == 0) { s_m[slice] = M; s_l[slice] = L; s_w[slice] = W; }
-  __syncthreads();
-  if (slice == 0) {
-    float Mt = s_m[0];
+  float Mt = M, Lt = L, Wt = W;
+  float4 Ot = O;
+  if (kSlices > 1) {
+    s_o[slice][d4] = O;
+    if (d4 == 0) { s_m[slice] = M; s_l[slice] = L; s_w[slice] = W; }
+    __syncthreads();
+    if (slice != 0) return;
+    Mt = s_m[0];
 #pragma unroll
-    for (int j = 1; j < kTMergeSlices; ++j) Mt = fmaxf(Mt, s_m[j]);
-    float Lt = 0.f, Wt = 0.f;
-    float4 Ot = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 1; j < kSlices; ++j) Mt = fmaxf(Mt, s_m[j]);
+    Lt = Wt = 0.f;
+    Ot = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < kTMergeSlices; ++j) {
+    for (int j = 0; j < kSlices; ++j) {
       if (s_m[j] == -INFINITY) continue;
       const float f = fast_exp2((s_m[j] - Mt) * p.c2);
       const float4 v = s_o[j][d4];
@@ -925,29 +939,37 @@ __device__ __forceinline__ void tile_merge_row(const TMergeParams& p, int split_
       if (kAcc) Wt += f * s_w[j];
       Ot.x += f * v.x; Ot.y += f * v.y; Ot.z += f * v.z; Ot.w += f * v.w;
     }
-    if (kAcc) {
-      const int tok = r / p.G, qh = head * p.G + r % p.G;
-      const float inv = Lt > 0.f ? 1.f / Lt : 0.f;
-      *reinterpret_cast<uint2*>(
-          p.out16 + (((int64_t)g0.x * p.q_len + tok) * p.Hq + qh) * 128 + 4 * d4) =
-          make_uint2(pack_bf16x2(Ot.x * inv, Ot.y * inv), pack_bf16x2(Ot.z * inv, Ot.w * inv));
-      if (d4 == 0)
-        p.stats[((int64_t)g0.x * p.Hkv + head) * (p.G * p.q_len) + r] =
-            make_float2(Mt, Wt > 0.f ? 1.f / Wt : 0.f);
-    } else if (Lt > 0.f) {
-      const int tok = r / p.G, qh = head * p.G + r % p.G;
-      float4* dst = reinterpret_cast<float4*>(
-          p.out + (((int64_t)g0.x * p.q_len + tok) * p.Hq + qh) * 128 + 4 * d4);
-      const float inv = 1.f / Lt;
-      *dst = make_float4(Ot.x * inv, Ot.y * inv, Ot.z * inv, Ot.w * inv);
-    }
+  }
+  if (kAcc) {
+    const int tok = r / p.G, qh = head * p.G + r % p.G;
+    const float inv = Lt > 0.f ? 1.f / Lt : 0.f;
+    *reinterpret_cast<uint2*>(
+        p.out16 + (((int64_t)g0.x * p.q_len + tok) * p.Hq + qh) * 128 + 4 * d4) =
+        make_uint2(pack_bf16x2(Ot.x * inv, Ot.y * inv), pack_bf16x2(Ot.z * inv, Ot.w * inv));
+    if (d4 == 0)
+      p.stats[((int64_t)g0.x * p.Hkv + head) * (p.G * p.q_len) + r] =
+          make_float2(Mt, Wt > 0.f ? 1.f / Wt : 0.f);
+  } else if (Lt > 0.f) {
+    const int tok = r / p.G, qh = head * p.G + r % p.G;
+    float4* dst = reinterpret_cast<float4*>(
+        p.out + (((int64_t)g0.x * p.q_len + tok) * p.Hq + qh) * 128 + 4 * d4);
+    const float inv = 1.f / Lt;
+    *dst = make_float4(Ot.x * inv, Ot.y * inv, Ot.z * inv, Ot.w * inv);
   }
 }
 
 template <bool kAcc>
 __global__ void __launch_bounds__(32 * kTMergeSlices, 2) tile_merge_kernel(const TMergeParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
-  tile_merge_row<kAcc>(p, blockIdx.x, blockIdx.y);
+  tile_merge_row<kAcc, kTMergeSlices>(p, blockIdx.x, blockIdx.y);
+}
+
+// The same with a warp per row and eight rows of a group per CTA. With many rows a group has few
+// partials, and a CTA for each row is mostly its start: 3072 rows of 7 partials took 15 us, this 3.
+__global__ void __launch_bounds__(32 * kTMergeSlices, 3)
+    tile_merge_rows_kernel(const TMergeParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  tile_merge_row<true, 1>(p, blockIdx.x, blockIdx.y * kTMergeSlices + (threadIdx.x >> 5));
 }
 
 // The second launch of an attention call with per-key weights on a tile plan with at most 8 rows per
@@ -958,7 +980,7 @@ __global__ void __launch_bounds__(kAccThreads, kAccCtasPerSm)
     tile_merge_weights_kernel(const TMergeParams p, const AccountParams a, int32_t merges) {
   asm volatile("griddepcontrol.launch_dependents;");
   if ((int)blockIdx.x < merges) {
-    tile_merge_row<true>(p, blockIdx.x / a.R, blockIdx.x % a.R);
+    tile_merge_row<true, kTMergeSlices>(p, blockIdx.x / a.R, blockIdx.x % a.R);
     return;
   }
   account_chunk(
@@ -1034,6 +1056,14 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  // A warp per row where a CTA per row would take more than three rounds of two per SM. Calls with
+  // weights on 152 SMs (us, CTA / warp per row): 192 rows of 38 partials 24.9 / 33.2, 384 of 19 38.8 /
+  // 41.9, 768 of 11 64.2 / 63.6 and 52.4 / 53.6, 1024 of 20 52.0 / 52.9, 1536 of 13 79.4 / 74.6, 1536
+  // of 6 73.9 / 68.2, 3072 of 7 98.4 / 85.6. (Without weights always a CTA: other sums, other bits.)
+  if (out16 && (int64_t)num_split * cfg.gridDim.y > 6 * (int64_t)grid) {
+    cfg.gridDim.y = (cfg.gridDim.y + kTMergeSlices - 1) / kTMergeSlices;
+    return cudaLaunchKernelEx(&cfg, tile_merge_rows_kernel, mp);
+  }
   return out16 ? cudaLaunchKernelEx(&cfg, tile_merge_kernel<true>, mp)
                : cudaLaunchKernelEx(&cfg, tile_merge_kernel<false>, mp);
 }

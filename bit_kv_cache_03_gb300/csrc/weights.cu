@@ -316,21 +316,6 @@ __device__ __forceinline__ void issue_products(const WeightParams& p, const Span
   if (to && lane == 0) flag_status(p.status, KV_NVFP4_DEV_TIMEOUT);
 }
 
-// Pairs of fp32 in one 64-bit register, computed by one instruction; each half rounds on its own.
-__device__ __forceinline__ uint64_t pair_of(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void halves_of(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // Adds 16 rows' exp2(s c2 - m c2) / l for each of the thread's two keys. The product m c2 is rounded
 // once per row, as in the tile kernel's P, whose sum l divides by: the two roundings cancel.
 // kMasked: only rows from r0 on see a key.
