@@ -20,14 +20,16 @@
 // wait is bounded in time, as in the attention kernels.
 //
 // Bounds. 48 rows over 4 x 100000 tokens, 4 KV heads: 115 MB of K and 13 MB of accounts, 19 us of HBM
-// time; the pass takes 32 us of that call's 110. 384 rows over 2 x 32768 tokens: 0.1 G exponentials
-// and as many fused multiply-adds; the pass takes 37 us of that call's 98. Neither memory (43 % and
-// 6 % of DRAM throughput) nor issue slots (45 % and 40 %) are full: the MMA warp sets the pace, of
-// whose 2.3K cycles per step of 96 x 128 products each MMA takes 210, a scale copy 175, the commit 200
-// and each wait on a completed barrier 290. Hence two key blocks per step and one commit. Tried and
-// slower (us, the two calls; 110 / 99 then): tiles of 96 rows with two sets of summing warps 117 / 101,
-// a second group of summing warps 112 / 99, unpaired fp32 arithmetic 120 / 109. The same: an issuing
-// thread chosen by elect.sync, polling without the suspending wait.
+// time; the pass takes 32 us of that call's 107, most of it with the sums left out too (28). 384 rows
+// over 2 x 32768 tokens: 0.1 G exponentials; the pass takes 29 to 37 us of that call's 86. Neither
+// memory (43 % and 6 % of DRAM throughput) nor issue slots (45 % and 40 %) are full. Of the second
+// call's 2.0K cycles per step and CTA, 0.8K are left when the warps only hand over (no product, load or
+// sum), the MMAs add 0.5K, the loads nothing, the exponentials 0.3K, the statistics' loads and the rest
+// of the sums 0.4K: hence two key blocks per step, one commit, and statistics read once for two keys.
+// Tried and slower (us, the two calls; 110 / 99 then): tiles of 96 rows with two sets of summing warps
+// 117 / 101, a second group of summing warps 112 / 99, a second MMA warp (and 8 columns at a time, for
+// registers) 114 / 103, unpaired fp32 arithmetic 120 / 109, the S buffer released before its last sums
+// 2 % more. The same: four slots for Q tiles, an issuing thread chosen by elect.sync, no suspending.
 
 #include <cstdint>
 #include <cuda_runtime.h>
