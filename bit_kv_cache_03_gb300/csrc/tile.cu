@@ -965,7 +965,8 @@ __global__ void __launch_bounds__(32 * kTMergeSlices, 2) tile_merge_kernel(const
 }
 
 // The same with a warp per row and eight rows of a group per CTA. With many rows a group has few
-// partials, and a CTA for each row is mostly its start: 24 groups of 128 rows, 7 partials each, took 15 us, this 3.
+// partials, and a CTA for each row is mostly its start: 24 groups of 128 rows, 7 partials each, took
+// 15 us, this 3.
 __global__ void __launch_bounds__(32 * kTMergeSlices, 3)
     tile_merge_rows_kernel(const TMergeParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
@@ -1057,9 +1058,10 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   // A warp per row where a CTA per row would take more than three rounds of two per SM. Calls with
-  // weights on 152 SMs (us, CTA / warp per row): 192 rows of 38 partials 24.9 / 33.2, 384 of 19 38.8 /
-  // 41.9, 768 of 11 64.2 / 63.6 and 52.4 / 53.6, 1024 of 20 52.0 / 52.9, 1536 of 13 79.4 / 74.6, 1536
-  // of 6 73.9 / 68.2, 24 x 128 of 7 98.4 / 85.6. (Without weights always a CTA: other sums, other bits.)
+  // weights on 152 SMs (us, CTA / warp per row): 192 rows of 38 partials 24.9 / 33.2, 384 of 19
+  // 38.8 / 41.9, 768 of 11 64.2 / 63.6 and 52.4 / 53.6, 1024 of 20 52.0 / 52.9, 1536 of 13 79.4 /
+  // 74.6, 1536 of 6 73.9 / 68.2, 24 x 128 of 7 98.4 / 85.6. (Without weights always a CTA: a warp
+  // adds in another order, and that call's results stay as they are.)
   if (out16 && (int64_t)num_split * cfg.gridDim.y > 6 * (int64_t)grid) {
     cfg.gridDim.y = (cfg.gridDim.y + kTMergeSlices - 1) / kTMergeSlices;
     return cudaLaunchKernelEx(&cfg, tile_merge_rows_kernel, mp);

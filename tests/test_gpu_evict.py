@@ -124,6 +124,19 @@ def test_attend_weights_onto_aligned_accounts(lens, q_len, Hq, Hkv):
     a.check(a.held.cpu().numpy().astype(np.float64))
 
 
+@pytest.mark.parametrize("lens,q_len,chunk,Hq,Hkv", [
+    ([600], 32, 64, 24, 4),       # 8 groups of up to 128 rows, 10 partials each
+    ([1300, 5], 30, 64, 24, 4),   # 20 partials and none, padding rows in the last tile
+    ([90, 700], 43, 128, 15, 5),  # 129 rows: a tile of one row
+])
+def test_attend_weights_merges_many_rows(lens, q_len, chunk, Hq, Hkv):
+    w = synth.Workload("rows", lens, q_len=q_len, seed=q_len, q_heads=Hq, kv_heads=Hkv,
+                       chunk_tokens=chunk)
+    a = Attend(w, chunk)
+    a.run()
+    a.check(a.held.cpu().numpy().astype(np.float64))
+
+
 def test_attend_weights_without_and_onto_the_accounts():
     w = synth.Workload("accounts", [70, 900], q_len=1, seed=3, chunk_tokens=64)
     a = Attend(w, 64)
