@@ -65,8 +65,9 @@ __device__ __forceinline__ float set_weight(const float* w, int64_t stride, int 
 // Bounds: the weights are read once (8.4 MB for 4 sequences x 4 KV heads x 131072 slots: 1.2 us of
 // HBM time), but the passes over the cached keys, each a few instructions per key on the few SMs of
 // a cluster, and the meetings follow one another: load 4 us, digit 1 and its sum 4, exchange and
-// search 6, listing 2.5 of that case's 22.6 us (the launch and the clusters' start are the rest). One CTA per set without a cluster took 386 us there
-// (2838 us for one set of 600000 slots and four heads, now 31 us).
+// search 6, listing 2.5 of that case's 20.0 us (the launch and the clusters' start are the rest).
+// One CTA per set without a cluster took 386 us there (2838 us for one set of 600000 slots and four
+// heads, now 28 us).
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048, kCoarse = kBins / 64;
 constexpr int kSelMaxCluster = 16;
@@ -144,6 +145,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   const int64_t seq = unit / sets;
   const int set = (int)(unit % sets);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < 2 * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
+  if (tid < 256) (&sh.bins7[0][0])[tid] = 0;
+  if (tid == 0) sh.over = sh.listed = 0u;
+  // Launched as a programmatic dependent of the kernel before it on the stream, which may have written
+  // the weights or lengths: started while that one ends, 2 to 3 us per call. Neither kernel of this
+  // file lets the next one start before its own end: clusters placed beside a running grid were packed
+  // unevenly over the SMs (16 sets of 131072 slots 22.8 us, 20.0 so).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t len = p.seq_lens[seq], keep = p.keep[seq];
   const int32_t kept = min(len, keep);
   // the exits below are the same for every CTA of the cluster
@@ -174,9 +183,6 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   };
 
   // the slice's keys, the smallest and the largest
-  for (int i = tid; i < 2 * kBins; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
-  if (tid < 256) (&sh.bins7[0][0])[tid] = 0;
-  if (tid == 0) sh.over = sh.listed = 0u;
   uint32_t low = 0xFFFFFFFFu, high = 0u;
   auto take4 = [&](const float4& v, int32_t i) {
     const uint32_t k[4] = {order_key(v.x), order_key(v.y), order_key(v.z), order_key(v.w)};
@@ -584,6 +590,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) compact_kernel(c
   const int part = (int)(unit % parts), head = (int)(unit / parts % p.Hkv);
   const int64_t seq = unit / parts / p.Hkv;
   const int tid = threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // e.g. for the selection's index
   const int32_t len = p.seq_lens[seq], keep = p.keep[seq];
   const int32_t kept = min(len, keep);
   // the same for every CTA of the cluster
@@ -746,17 +753,19 @@ cudaError_t launch_evict_select(const float* weights, int64_t w_stride, const in
                        Hkv,     per_head, sink,     recent, (int32_t)cached, status};
   const int64_t grid = sets * C;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)C;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = sizeof(SelectShared) + 4 * (size_t)cached;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   const bool vec = w_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(weights) & 15u) == 0;
   return vec ? cudaLaunchKernelEx(&cfg, select_kernel<true>, p)
              : cudaLaunchKernelEx(&cfg, select_kernel<false>, p);
@@ -789,16 +798,18 @@ cudaError_t launch_evict_compact(const int32_t* index, int64_t index_stride, int
          units * C * 2 <= kMoveCtasPerSm * (int64_t)num_sms)
     C *= 2;
   if (units * C > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)C;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * C));
   cfg.blockDim = dim3(kMoveThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, compact_kernel, p);
 }
 
