@@ -564,11 +564,12 @@ struct CompactParams {
   int32_t* status;
 };
 
-// One cluster per (sequence, KV head, part): part 0 the K rows, 1 the V rows, 2 the weights. The
-// cluster takes its rows in waves: in a wave every thread loads what it moves into registers (a
-// 16-byte code piece, and for half of the threads four scales, of kMoveRows rows), the cluster
-// meets, and the wave is stored. The next wave's reads, which lie behind the wave's rows, are on
-// their way meanwhile.
+// One cluster per (sequence, KV head, part): the K rows, the V rows, the weights; or, with few sequences
+// and heads, two clusters for the K and two for the V rows, each with two of the four 16-byte pieces
+// of a row's codes and one of its two words of scales (bytes that no other part touches). The cluster
+// takes its rows in waves: in a wave every thread loads what it moves into registers (a piece of the
+// codes, and for half of the threads four scales, of kMoveRows rows), the cluster meets, and the wave
+// is stored. The next wave's reads, which lie behind the wave's rows, are on their way meanwhile.
 //
 // Bounds: 296 bytes per kept row and KV head, but the rows lie apart: a K row's codes are four
 // 16-byte pieces in sectors that hold a neighbour's piece as well, its scales two words in two more,
@@ -581,11 +582,15 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 4;                                // rows in flight per thread
 constexpr int kMoveMaxCluster = 16;
 constexpr int kMoveCtasPerSm = 3;
-constexpr int kMoveTile = kMoveThreads / 4 * kMoveRows;  // rows of a CTA per wave, codes and scales
+// rows of a CTA per wave, codes and scales, when a part has kPieces of a row's pieces
+template <int kPieces>
+constexpr int kMoveTile = kMoveThreads / kPieces * kMoveRows;
 
+template <int kPieces>
 __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) compact_kernel(const CompactParams p) {
   const uint32_t C = cluster_size(), rank = cluster_rank();
-  const int parts = p.weights != nullptr ? 3 : 2;
+  constexpr int kSplit = 4 / kPieces, kTile = kMoveTile<kPieces>;
+  const int parts = 2 * kSplit + (p.weights != nullptr ? 1 : 0);
   const int64_t unit = blockIdx.x / C;
   const int part = (int)(unit % parts), head = (int)(unit / parts % p.Hkv);
   const int64_t seq = unit / parts / p.Hkv;
@@ -601,7 +606,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) compact_kernel(c
   }
   const int32_t* index =
       p.index + (seq * (p.per_head ? p.Hkv : 1) + (p.per_head ? head : 0)) * p.index_stride;
-  if (part == 2) {
+  if (part == 2 * kSplit) {
     float* w = p.weights + (seq * p.Hkv + head) * p.w_stride;
     const int64_t wave = (int64_t)C * kMoveThreads * kMoveRows;
     for (int64_t j0 = 0; j0 < kept; j0 += wave) {
@@ -632,19 +637,22 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) compact_kernel(c
   const int32_t* src_table = p.block_table + seq * p.max_pages;
   const int32_t* dst_table = p.dst_table + seq * p.dst_max_pages;
   const int64_t block = (int64_t)p.Hkv * 9216;
-  const int piece = tid & 3;
-  // byte offsets of this thread's 16 code bytes and (pieces 0, 1) four scales of a slot
+  const bool keys = part < kSplit;
+  const int half = part % kSplit, piece = half * kPieces + tid % kPieces;
+  const int word = kSplit == 1 ? piece & 1 : half;
+  const bool with_scales = kSplit == 1 ? piece < 2 : tid % kPieces == 0;
+  // byte offsets of this thread's 16 code bytes and four scales of a slot
   auto code_at = [&](int slot) {
-    return part == 0 ? head * 4096 + (slot >> 3) * 512 + piece * 128 + (slot & 7) * 16
-                     : p.Hkv * 4608 + head * 4096 + slot * 64 + piece * 16;
+    return keys ? head * 4096 + (slot >> 3) * 512 + piece * 128 + (slot & 7) * 16
+                : p.Hkv * 4608 + head * 4096 + slot * 64 + piece * 16;
   };
   auto scale_at = [&](int slot) {
-    return part == 0 ? kscale_offset(p.Hkv, head, slot, piece & 1)
-                     : p.Hkv * 8704 + head * 512 + slot * 8 + 4 * (piece & 1);
+    return keys ? kscale_offset(p.Hkv, head, slot, word)
+                : p.Hkv * 8704 + head * 512 + slot * 8 + 4 * word;
   };
-  const int64_t wave = (int64_t)C * kMoveTile;
-  constexpr int kApart = kMoveThreads / 4;  // rows between a thread's rows
-  const int64_t first = (int64_t)rank * kMoveTile + (tid >> 2);
+  const int64_t wave = (int64_t)C * kTile;
+  constexpr int kApart = kMoveThreads / kPieces;  // rows between a thread's rows
+  const int64_t first = (int64_t)rank * kTile + tid / kPieces;
   int32_t bad = 0;
   struct Rows {
     uint4 c[kMoveRows];
@@ -686,7 +694,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) compact_kernel(c
       const int slot = (int)((j + u * kApart) % kPage);
       uint8_t* dst = p.pool + r.to[u] * block;
       *reinterpret_cast<uint4*>(dst + code_at(slot)) = r.c[u];
-      if (piece < 2) *reinterpret_cast<uint32_t*>(dst + scale_at(slot)) = r.sc[u];
+      if (with_scales) *reinterpret_cast<uint32_t*>(dst + scale_at(slot)) = r.sc[u];
     }
   };
   Rows a, b;
@@ -739,7 +747,7 @@ cudaError_t launch_evict_select(const float* weights, int64_t w_stride, const in
   }
   // The lengths are on the device, so the cluster is sized for the longest that the accounts hold:
   // as few CTAs as keep the keys in shared memory, and up to eight while SMs are left and a CTA has
-  // 2048 keys. Measured (us, C = 1, 2, 4, 8, 16): 4 sets of 4000 slots 12.3, 10.3, 10.3, 10.3, 14.4;
+  // 2048 keys. Measured (us, before the programmatic launch, C = 1, 2, 4, 8, 16): 4 sets of 4000 slots 12.3, 10.3, 10.3, 10.3, 14.4;
   // 4 of 20000 16.4, 14.4, 12.3, 12.3, 14.4; 8 of 131072 (from C = 4) 22.6, 18.4, 22.6; 16 of 131072
   // 22.6, 22.6, 35; 48 of 40000 24.6, 18.4, 18.5, 28, 62; 128 of 4000 12.3, 12.7, 22, 43, 137.
   const int64_t sets = (int64_t)num_seqs * (per_head ? Hkv : 1);
@@ -784,19 +792,24 @@ cudaError_t launch_evict_compact(const int32_t* index, int64_t index_stride, int
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
   if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        compact_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
+    for (const void* kf : {(const void*)compact_kernel<4>, (const void*)compact_kernel<2>}) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(kf, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+    }
     if (dev >= 0 && dev < 64) attr_done[dev] = true;
   }
   // the kept counts are on the device: sized for the most that the index holds, a wave per CTA, and
-  // no more CTAs than run at once (one sequence, four heads, 16384 kept of 131072: 16.8 us with
-  // clusters of 16, 24.9 with 8)
-  const int64_t units = (int64_t)num_seqs * Hkv * (weights != nullptr ? 3 : 2);
+  // no more CTAs than run at once; in halves when clusters of the most CTAs still find places. One
+  // sequence, four heads, 16384 kept of 131072: 22.7 us with clusters of 8, 14.6 of 16, 9.9 in halves;
+  // two heads, 60000 of 600000: 88.9, 46.8, 29.2; one head, 5000 of 20000: 7.2 of 16, 6.6 in halves
+  const int64_t places = kMoveCtasPerSm * (int64_t)num_sms, pairs = (int64_t)num_seqs * Hkv;
+  const int extra = weights != nullptr ? 1 : 0;
+  const bool halves = pairs * (4 + extra) * kMoveMaxCluster <= places;
+  const int64_t units = pairs * ((halves ? 4 : 2) + extra);
+  const int64_t tile = halves ? kMoveTile<2> : kMoveTile<4>;
   int64_t C = 1;
-  while (C < kMoveMaxCluster && C * kMoveTile < index_stride &&
-         units * C * 2 <= kMoveCtasPerSm * (int64_t)num_sms)
-    C *= 2;
+  while (C < kMoveMaxCluster && C * tile < index_stride && units * C * 2 <= places) C *= 2;
   if (units * C > 0x7FFFFFFF) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -810,7 +823,8 @@ cudaError_t launch_evict_compact(const int32_t* index, int64_t index_stride, int
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, compact_kernel, p);
+  return halves ? cudaLaunchKernelEx(&cfg, compact_kernel<2>, p)
+                : cudaLaunchKernelEx(&cfg, compact_kernel<4>, p);
 }
 
 }  // namespace kvnvfp4

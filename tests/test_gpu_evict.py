@@ -397,6 +397,20 @@ def test_compact(lens, keep, H, per_head, in_place):
     assert w is None and np.array_equal(got, want)
 
 
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("lens,keep,H", [
+    ([9000, 300], [7000, 100], 4),              # clusters of 16 for whole rows, two waves
+    ([9000, 8000, 1, 7000, 64], [8990, 2000, 1, 3500, 0], 4),  # clusters of 4, many waves
+    ([12000], [9000], 5),                       # halves of rows, odd heads
+    ([2100] * 60, [1100] * 60, 3),              # no clusters
+])
+def test_compact_of_many_waves(lens, keep, H, in_place):
+    pool, table, dst, index, weights = _compact_case(lens, keep, H, True, sum(keep))
+    got, w, status = _compact(pool, table, None if in_place else dst, index, weights, lens, keep, H)
+    want, ww = evictref.compact(pool, table, table if in_place else dst, H, index, lens, keep, weights)
+    assert status == 0 and np.array_equal(got, want) and np.array_equal(w, ww)
+
+
 @pytest.mark.parametrize("shape", ["dense", "first", "last", "alternate"])
 def test_compact_patterns_in_place(shape):
     # few holes, none, all rows moved far, every second row: the order of reads and writes
