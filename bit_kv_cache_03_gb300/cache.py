@@ -104,11 +104,8 @@ class PagedNVFP4Cache:
             sm_scale = 1.0 / math.sqrt(128)
         need = kv_nvfp4_weights_workspace_bytes(self.layout, self.plan_info)
         if self.weights_workspace is None or self.weights_workspace.numel() < need:
-            # from the allocator's memory of the stream that works in it
-            with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int)
-                                   else stream):
-                self.weights_workspace = torch.empty(max(need, 256), dtype=torch.uint8,
-                                                     device=self.device)
+            old, self.weights_workspace = self.weights_workspace, None
+            self.weights_workspace = self._larger(old, need, stream)
         kv_nvfp4_decode_attn_weights(
             self.layout, self.plan_info, self.workspace, self.weights_workspace,
             self.weights_workspace.numel(), q_codes, q_scales, sm_scale, self.pool, self.num_pages,
@@ -137,6 +134,16 @@ class PagedNVFP4Cache:
         kv_nvfp4_evict_compact(self.layout, index, index.shape[2], per_head, seq_lens, keep,
                                self.num_seqs, self.block_table, self.max_pages, self.num_pages,
                                self.pool, None, 0, weights, weights.shape[2], self.status, stream)
+
+    def _larger(self, old, need, stream):
+        """A workspace of `need` bytes in place of `old`, from the allocator's memory of the stream that
+        works in it. `old` may be another stream's memory, which takes it back the moment it is dropped:
+        the allocator is told to wait for this call's stream, behind which the calls that used it lie."""
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int)
+                               else stream):
+            if old is not None:
+                old.record_stream(torch.cuda.current_stream())
+            return torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
 
     def _check_current(self):
         # a launch goes to the current device; with the buffers of another one it would fault

@@ -1,0 +1,59 @@
+"""The lives of the workspaces that PagedNVFP4Cache keeps: over streams, plans and captured graphs."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+HOLD = 400_000_000  # clock cycles of a kernel that only waits: 0.2 s and more
+
+
+class Session:
+    """One sequence whose slots are all in the pool's one page (zeros), with a short and a long plan.
+    The short plan's weights workspace takes 13 MB: the allocator hands such a block out whole."""
+
+    def __init__(self):
+        import bit_kv_cache_03_gb300 as k
+        self.c = k.PagedNVFP4Cache(1, np.zeros((1, 4096), np.int32), 64, 24, 4)
+        self.c.pool.zero_()
+        self.w = self.c.weight_accounts()
+        self.qc, self.qs = self.c.quantized_q_buffers(1)
+        self.qc.zero_(), self.qs.zero_()
+        self.out = torch.empty(1, 24, 128, dtype=torch.bfloat16, device="cuda")
+        self.plans = []
+        for n in (131072, 262144):
+            self.c.workspace = None
+            self.plans.append((self.c.plan([n], 1), self.c.workspace))
+        self.use(0)
+
+    def use(self, i):
+        self.c.plan_info, self.c.workspace = self.plans[i]
+
+    def attend(self, stream=None):
+        self.c.attend_weights(self.qc, self.qs, self.out, self.w, stream=stream)
+
+
+def _overlaps(start, size, n=8):
+    """Whether one of n further blocks of the current stream's memory lies in [start, start + size)."""
+    blocks = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(n)]
+    return any(b.data_ptr() < start + size and start < b.data_ptr() + size for b in blocks)
+
+
+def test_the_weights_workspace_is_not_handed_out_under_a_call_of_another_stream():
+    s = Session()
+    s.attend()  # allocated for the current stream
+    torch.cuda.synchronize()
+    start, size = s.c.weights_workspace.data_ptr(), s.c.weights_workspace.numel()
+    assert size > 12 << 20
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(HOLD)
+        s.attend()
+    s.use(1)
+    s.attend(stream=side)  # grows
+    assert s.c.weights_workspace.data_ptr() != start
+    lent = _overlaps(start, size)
+    assert not side.query()  # the first call on `side` has still to run
+    assert not lent
+    torch.cuda.synchronize()
+    assert not s.out.any() and int(s.c.status.item()) == 0
