@@ -66,9 +66,11 @@ class PagedNVFP4Cache:
 
     # -- split-K plan + attention -----------------------------------------------------------
     def plan(self, seq_lens, q_len, causal=True, chunk_tokens=1024, stream=None):
+        """Builds the work list of the next attention calls (seq_lens include the new tokens), on
+        `stream`, behind the calls that use the last one."""
         need = kv_nvfp4_plan_workspace_bytes(self.layout, seq_lens, q_len, causal, chunk_tokens)
         if self.workspace is None or self.workspace.numel() < need:
-            self.workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+            self._enlarge("workspace", need, stream)
         self.plan_info = kv_nvfp4_plan(self.layout, seq_lens, q_len, causal, chunk_tokens,
                                        self.workspace, self.workspace.numel(), stream)
         return self.plan_info
@@ -104,8 +106,7 @@ class PagedNVFP4Cache:
             sm_scale = 1.0 / math.sqrt(128)
         need = kv_nvfp4_weights_workspace_bytes(self.layout, self.plan_info)
         if self.weights_workspace is None or self.weights_workspace.numel() < need:
-            old, self.weights_workspace = self.weights_workspace, None
-            self.weights_workspace = self._larger(old, need, stream)
+            self._enlarge("weights_workspace", need, stream)
         kv_nvfp4_decode_attn_weights(
             self.layout, self.plan_info, self.workspace, self.weights_workspace,
             self.weights_workspace.numel(), q_codes, q_scales, sm_scale, self.pool, self.num_pages,
@@ -135,15 +136,19 @@ class PagedNVFP4Cache:
                                self.num_seqs, self.block_table, self.max_pages, self.num_pages,
                                self.pool, None, 0, weights, weights.shape[2], self.status, stream)
 
-    def _larger(self, old, need, stream):
-        """A workspace of `need` bytes in place of `old`, from the allocator's memory of the stream that
-        works in it. `old` may be another stream's memory, which takes it back the moment it is dropped:
-        the allocator is told to wait for this call's stream, behind which the calls that used it lie."""
+    def _enlarge(self, name, need, stream):
+        """Replaces a workspace by one of `need` bytes, from the allocator's memory of the stream that
+        works in it. The old one may be another stream's memory, which takes it back the moment it is
+        dropped: the allocator is told to wait for this call's stream, behind which the calls that used
+        it lie."""
         with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int)
                                else stream):
+            old = getattr(self, name)
             if old is not None:
                 old.record_stream(torch.cuda.current_stream())
-            return torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+            old = None
+            setattr(self, name, None)  # before the new one is made: the two need not fit together
+            setattr(self, name, torch.empty(max(need, 256), dtype=torch.uint8, device=self.device))
 
     def _check_current(self):
         # a launch goes to the current device; with the buffers of another one it would fault

@@ -57,3 +57,45 @@ def test_the_weights_workspace_is_not_handed_out_under_a_call_of_another_stream(
     assert not lent
     torch.cuda.synchronize()
     assert not s.out.any() and int(s.c.status.item()) == 0
+
+
+def test_the_plan_workspace_is_not_handed_out_under_a_call_of_another_stream(monkeypatch):
+    import bit_kv_cache_03_gb300.cache as cache
+    s = Session()
+    s.attend()
+    torch.cuda.synchronize()
+    start, size = s.c.workspace.data_ptr(), s.c.workspace.numel()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(HOLD)
+        s.attend()
+    # the buffers alone: a work list from pageable memory may wait for the stream
+    monkeypatch.setattr(cache, "kv_nvfp4_plan", lambda *a: None)
+    monkeypatch.setattr(cache, "kv_nvfp4_plan_workspace_bytes", lambda *a: size + 1)
+    s.plans = None  # the cache alone holds its workspace
+    s.c.plan([64], 1, stream=side)  # grows
+    assert s.c.workspace.data_ptr() != start
+    lent = _overlaps(start, size)
+    assert not side.query()
+    assert not lent
+    torch.cuda.synchronize()
+    assert not s.out.any() and int(s.c.status.item()) == 0
+
+
+def test_a_plan_workspace_is_memory_of_the_stream_it_is_planned_on(monkeypatch):
+    import bit_kv_cache_03_gb300.cache as cache
+    s = Session()
+    size = 64 << 20
+    monkeypatch.setattr(cache, "kv_nvfp4_plan", lambda *a: None)
+    monkeypatch.setattr(cache, "kv_nvfp4_plan_workspace_bytes", lambda *a: size)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(HOLD)
+    x = torch.ones(size, dtype=torch.uint8, device="cuda")  # written when the wait is over
+    start = x.data_ptr()
+    del x  # free to the current stream, behind its work; not to another one
+    s.plans = None
+    s.c.plan([64], 1, stream=side)
+    busy = not torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
+    assert busy and not (start <= s.c.workspace.data_ptr() < start + size)
