@@ -9,7 +9,7 @@ import math
 import numpy as np
 import torch
 
-from . import (kv_nvfp4_append, kv_nvfp4_append_slots, kv_nvfp4_decode_attn,
+from . import (_stream, kv_nvfp4_append, kv_nvfp4_append_slots, kv_nvfp4_decode_attn,
                kv_nvfp4_decode_attn_weights, kv_nvfp4_decode_step, kv_nvfp4_decode_step_host,
                kv_nvfp4_evict_compact, kv_nvfp4_evict_select, kv_nvfp4_plan,
                kv_nvfp4_plan_workspace_bytes, kv_nvfp4_pool_bytes, kv_nvfp4_rope_table_init,
@@ -39,6 +39,7 @@ class PagedNVFP4Cache:
         self.workspace = None
         self.weights_workspace = None
         self.plan_info = None
+        self._captured = []
 
     # -- fused quantize-append --------------------------------------------------------------
     def append(self, k, v, seq_ids, positions, q=None, q_codes=None, q_scales=None, stream=None,
@@ -78,6 +79,7 @@ class PagedNVFP4Cache:
     def attend(self, q_codes, q_scales, out, sm_scale=None, stream=None):
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(128)
+        self._hold_captured(stream)
         kv_nvfp4_decode_attn(self.layout, self.plan_info, self.workspace, q_codes, q_scales,
                              sm_scale, self.pool, self.num_pages, self.block_table, self.max_pages,
                              out, self.status, stream)
@@ -107,6 +109,7 @@ class PagedNVFP4Cache:
         need = kv_nvfp4_weights_workspace_bytes(self.layout, self.plan_info)
         if self.weights_workspace is None or self.weights_workspace.numel() < need:
             self._enlarge("weights_workspace", need, stream)
+        self._hold_captured(stream)
         kv_nvfp4_decode_attn_weights(
             self.layout, self.plan_info, self.workspace, self.weights_workspace,
             self.weights_workspace.numel(), q_codes, q_scales, sm_scale, self.pool, self.num_pages,
@@ -141,14 +144,30 @@ class PagedNVFP4Cache:
         works in it. The old one may be another stream's memory, which takes it back the moment it is
         dropped: the allocator is told to wait for this call's stream, behind which the calls that used
         it lie."""
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int)
-                               else stream):
+        with self._on(stream):
             old = getattr(self, name)
             if old is not None:
                 old.record_stream(torch.cuda.current_stream())
             old = None
             setattr(self, name, None)  # before the new one is made: the two need not fit together
             setattr(self, name, torch.empty(max(need, 256), dtype=torch.uint8, device=self.device))
+
+    def _hold_captured(self, stream):
+        """A graph replays a captured call on the workspaces that the call had: they live as long as the
+        cache does, outgrown or not."""
+        if _stream(stream) == _stream(None):
+            capturing = torch.cuda.is_current_stream_capturing()
+        else:
+            with self._on(stream):
+                capturing = torch.cuda.is_current_stream_capturing()
+        if capturing:
+            self._captured += [b for b in (self.workspace, self.weights_workspace)
+                               if b is not None and all(b is not x for x in self._captured)]
+
+    @staticmethod
+    def _on(stream):
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int)
+                                 else stream)
 
     def _check_current(self):
         # a launch goes to the current device; with the buffers of another one it would fault
@@ -170,6 +189,7 @@ class PagedNVFP4Cache:
         lengths given to the last plan) appended and attended in one kernel launch."""
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(128)
+        self._hold_captured(stream)
         kv_nvfp4_decode_step(self.layout, self.plan_info, self.workspace, q, k, v, self.rope,
                              self.max_pos, self.block_table, self.max_pages, self.num_pages,
                              self.pool, q_codes, q_scales, sm_scale, out, self.status, stream)

@@ -99,3 +99,35 @@ def test_a_plan_workspace_is_memory_of_the_stream_it_is_planned_on(monkeypatch):
     busy = not torch.cuda.current_stream().query()
     torch.cuda.synchronize()
     assert busy and not (start <= s.c.workspace.data_ptr() < start + size)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_a_captured_call_keeps_its_workspaces(given):
+    s = Session()
+    s.plans = s.c.workspace = s.c.weights_workspace = None
+    s.c.plan([640], 1)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    stream = side if given else None
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        s.attend(stream)
+        want = s.w.clone(), s.out.clone()
+        with torch.cuda.graph(graph, stream=side):
+            s.attend(stream)
+    torch.cuda.synchronize()
+    held = [(b.data_ptr(), b.numel()) for b in (s.c.workspace, s.c.weights_workspace)]
+    s.c.plan([262144], 1)
+    s.attend()  # both grow
+    torch.cuda.synchronize()
+    assert all(b.data_ptr() != at for b, (at, _) in
+               zip((s.c.workspace, s.c.weights_workspace), held))
+    lent = [_overlaps(at, size, 64) for at, size in held]
+    with torch.cuda.stream(side):
+        lent += [_overlaps(at, size, 64) for at, size in held]
+    assert not any(lent)
+    s.w.zero_(), s.out.fill_(1)
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(s.w, want[0]) and torch.equal(s.out, want[1])
+    assert int(s.c.status.item()) == 0
