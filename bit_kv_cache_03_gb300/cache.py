@@ -104,6 +104,10 @@ class PagedNVFP4Cache:
         if out.dtype != torch.bfloat16 or not out.is_contiguous() or out.numel() != rows * 128 or \
                 out.device != weights.device:
             raise ValueError("out must be a contiguous device bfloat16 [rows, num_q_heads, 128]")
+        for x, each in ((q_codes, 64), (q_scales, 8)):
+            if x.device != weights.device or not x.is_contiguous() or x.nbytes < rows * each:
+                raise ValueError("q_codes and q_scales must be contiguous, on the device, and hold "
+                                 "64 and 8 bytes per row of the plan")
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(128)
         need = kv_nvfp4_weights_workspace_bytes(self.layout, self.plan_info)
