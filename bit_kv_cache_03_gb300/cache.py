@@ -98,6 +98,8 @@ class PagedNVFP4Cache:
         self._check_accounts(weights, weights_in)
         if self.plan_info is None:
             raise ValueError("attend_weights needs a plan()")
+        if self.plan_info.num_seqs > self.num_seqs:
+            raise ValueError("the plan has more sequences than the cache")
         if weights_in is not None and weights_in.shape != weights.shape:
             raise ValueError("weights_in must have the shape of weights")
         rows = self.plan_info.num_seqs * self.plan_info.q_len * self.layout.num_q_heads

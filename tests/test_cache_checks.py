@@ -42,3 +42,13 @@ def test_attend_weights_wants_every_row_of_the_queries(calls):
         with pytest.raises(ValueError, match="q_codes"):
             c.attend_weights(q, s, out, w)
     assert len(calls) == 2
+
+
+def test_attend_weights_refuses_a_plan_of_more_sequences(calls):
+    c, (codes, scales), out, w = _cache(num_seqs=2, plan=(10, 10, 10))
+    with pytest.raises(ValueError, match="sequences"):  # its third one has no table row and no accounts
+        c.attend_weights(codes, scales, out, w)
+    assert not calls
+    c, (codes, scales), out, w = _cache(num_seqs=3, plan=(10, 10))
+    c.attend_weights(codes, scales, out, w)  # the first two of three
+    assert calls == ["kv_nvfp4_decode_attn_weights"]
