@@ -149,11 +149,12 @@ class PagedNVFP4Cache:
         """Replaces a workspace by one of `need` bytes, from the allocator's memory of the stream that
         works in it. The old one may be another stream's memory, which takes it back the moment it is
         dropped: the allocator is told to wait for this call's stream, behind which the calls that used
-        it lie."""
+        it lie. What was outgrown once gets a sixteenth more: a sequence's need grows with every page."""
         with self._on(stream):
             old = getattr(self, name)
             if old is not None:
                 old.record_stream(torch.cuda.current_stream())
+                need += need // 16
             old = None
             setattr(self, name, None)  # before the new one is made: the two need not fit together
             setattr(self, name, torch.empty(max(need, 256), dtype=torch.uint8, device=self.device))

@@ -131,3 +131,21 @@ def test_a_captured_call_keeps_its_workspaces(given):
     torch.cuda.synchronize()
     assert torch.equal(s.w, want[0]) and torch.equal(s.out, want[1])
     assert int(s.c.status.item()) == 0
+
+
+def test_a_growing_sequence_seldom_needs_another_workspace(monkeypatch):
+    import bit_kv_cache_03_gb300 as k
+    s = Session()
+    s.plans = s.c.workspace = None
+    grown = []
+    real = k.PagedNVFP4Cache._enlarge
+    monkeypatch.setattr(k.PagedNVFP4Cache, "_enlarge",
+                        lambda self, name, *a: (grown.append(name), real(self, name, *a))[1])
+    for n in range(131072, 131072 + 64 * 64, 64):  # a page more each time
+        s.c.plan([n], 1)
+        s.attend()
+        need = k.kv_nvfp4_weights_workspace_bytes(s.c.layout, s.c.plan_info)
+        assert need <= s.c.weights_workspace.numel() <= need + need // 16
+    assert grown.count("weights_workspace") == 2  # the first, and one with room for more
+    torch.cuda.synchronize()
+    assert int(s.c.status.item()) == 0
