@@ -125,7 +125,8 @@ class PagedNVFP4Cache:
     def evict(self, weights, seq_lens, keep, index, sink=0, recent=0, stream=None):
         """Keeps min(seq_len, keep) tokens of each sequence by accumulated weight, the first `sink`
         and the last `recent` ahead of the others, and compacts the cache and the weights to them
-        in place. seq_lens, keep: device int32 [num_seqs]; index: device int32
+        in place. Tokens so protected rank by slot alone: a keep below sink + recent drops the newest of
+        them, the last token first. seq_lens, keep: device int32 [num_seqs]; index: device int32
         [num_seqs, num_kv_heads, n] (every KV head keeps its own tokens) or [num_seqs, 1, n] (one
         set for all), n at least the largest kept count; receives the kept slots, ascending."""
         self._check_accounts(weights)

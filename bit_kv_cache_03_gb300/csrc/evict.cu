@@ -2,7 +2,7 @@
 // (kv_nvfp4_evict_select) and the compaction of the cache to them (kv_nvfp4_evict_compact).
 //
 // Select. Per set of slots (a KV head's, or a sequence's when all heads share one set) the slots
-// [0, sink) and [len - recent, len) come first, then the rest by weight, ties to the lowest slot;
+// [0, sink) and [len - recent, len) come first, by slot, then the rest by weight, ties to the lowest slot;
 // the first min(len, keep) of that order are listed in ascending slot order. The weights are mapped
 // to unsigned keys of the same order (NaN to 0, below every value) and the smallest kept key is
 // found by a radix select.

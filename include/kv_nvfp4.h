@@ -295,10 +295,11 @@ kv_nvfp4_status kv_nvfp4_decode_attn_weights(
  *
  * Select: per sequence and KV head (per_head != 0), or per sequence with one set for all its heads
  * (per_head == 0), the kept = min(seq_len, keep) slots that come first when ordered by
- *   1. slots below `sink` and slots >= seq_len - recent, ahead of all others;
- *   2. the larger weight (per_head == 0: the heads' weights added in fp32, head 0 first); -0 equals
- *      0, NaN counts below every other value;
- *   3. the lower slot.
+ *   1. slots below `sink` and slots >= seq_len - recent, ahead of all others and, among themselves,
+ *      by slot alone, the lower first: a keep below their number leaves out the newest of them;
+ *   2. the others by weight, the larger first (per_head == 0: the heads' weights added in fp32, head
+ *      0 first); -0 equals 0, NaN counts below every other value;
+ *   3. of equal weights the lower slot first.
  *   weights:   DEVICE fp32 [num_seqs][num_kv_heads][weights_stride]
  *   d_seq_lens, d_keep: DEVICE int32 [num_seqs]
  *   d_index:   DEVICE int32 [num_seqs][num_kv_heads, or 1][index_stride]: the kept slots in
