@@ -317,12 +317,14 @@ kv_nvfp4_status kv_nvfp4_decode_attn_weights(
  *              nowhere but at the same place of the same sequence; or null (and dst_max_pages 0):
  *              in place, in the old cache's pages. Pages shared by several rows of d_block_table
  *              (a common prefix) must not be compacted in place.
- *   weights:   DEVICE fp32 as above, moved in place like the rows, with 0 for kept <= t < seq_len
- *              (ready for new tokens in those slots); or null
+ *   weights:   DEVICE fp32 as above, moved in place by the index alone (a row that is skipped for its
+ *              page does not hold its weight back), with 0 for kept <= t < seq_len (ready for new
+ *              tokens in those slots); or null
  * A sequence with a negative length or keep, kept above index_stride or dst_max_pages * 64, or a
  * length above max_pages * 64 or (with weights) weights_stride sets KV_NVFP4_DEV_BAD_POS and is
- * skipped; so are a row whose index lies outside [0, seq_len) (BAD_POS) and one whose old or new
- * page lies outside the pool (BAD_PAGE). One kernel launch. num_seqs = 0 does nothing. */
+ * skipped; so are a row and weight whose index lies outside [0, seq_len) (BAD_POS) and a row whose old
+ * or new page lies outside the pool (BAD_PAGE: its new slot then has its old bytes and another token's
+ * weight). One kernel launch. num_seqs = 0 does nothing. */
 kv_nvfp4_status kv_nvfp4_evict_select(const kv_nvfp4_layout *layout, const float *weights,
                                       int64_t weights_stride, const int32_t *d_seq_lens,
                                       const int32_t *d_keep, int32_t num_seqs, int32_t per_head,
