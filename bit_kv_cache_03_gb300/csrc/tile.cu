@@ -1057,11 +1057,13 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // A warp per row where a CTA per row would take more than three rounds of two per SM. Calls with
-  // weights on 152 SMs (us, CTA / warp per row): 192 rows of 38 partials 24.9 / 33.2, 384 of 19
+  // A warp per row where there are more than six rows per CTA of the attention's grid. Calls with
+  // weights (us, CTA / warp per row), grids of 152: 192 rows of 38 partials 24.9 / 33.2, 384 of 19
   // 38.8 / 41.9, 768 of 11 64.2 / 63.6 and 52.4 / 53.6, 1024 of 20 52.0 / 52.9, 1536 of 13 79.4 /
-  // 74.6, 1536 of 6 73.9 / 68.2, 24 x 128 of 7 98.4 / 85.6. (Without weights always a CTA: a warp
-  // adds in another order, and that call's results stay as they are.)
+  // 74.6, 1536 of 6 73.9 / 68.2, 24 x 128 of 7 98.4 / 85.6. Grids of 16, which coarse chunks give, have
+  // few partials a row: 192 rows of 4 17.0 / 16.9, 504 of 4 24.3 / 22.3, 33.1 / 31.4 and 50.4 / 48.9.
+  // (Without weights always a CTA: a warp adds in another order, and that call's results stay as they
+  // are.)
   if (out16 && (int64_t)num_split * cfg.gridDim.y > 6 * (int64_t)grid) {
     cfg.gridDim.y = (cfg.gridDim.y + kTMergeSlices - 1) / kTMergeSlices;
     return cudaLaunchKernelEx(&cfg, tile_merge_rows_kernel, mp);
