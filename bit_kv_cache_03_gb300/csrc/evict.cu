@@ -725,6 +725,26 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtasPerSm) compact_kernel(c
   if (bad != 0) flag_status(p.status, bad);
 }
 
+// The largest cluster, a power of two up to `most`, of which the current device can place one.
+int largest_cluster(const void* kernel, int threads, size_t smem, int most) {
+  for (int C = most; C > 1; C /= 2) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)C);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0) return C;
+    cudaGetLastError();  // too large a cluster is no launch error: do not leave it set
+  }
+  return 1;
+}
+
 }  // namespace
 
 cudaError_t launch_evict_select(const float* weights, int64_t w_stride, const int32_t* seq_lens,
@@ -732,10 +752,11 @@ cudaError_t launch_evict_select(const float* weights, int64_t w_stride, const in
                                 int32_t sink, int32_t recent, int32_t* index, int64_t index_stride,
                                 int32_t Hkv, int32_t num_sms, int32_t* status,
                                 cudaStream_t stream) {
-  static bool attr_done[64] = {};
+  static int of_device[64] = {};  // clusters of CTAs with all of the shared memory
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
-  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+  int largest = dev >= 0 && dev < 64 ? of_device[dev] : 0;
+  if (largest == 0) {
     for (const void* kf : {(const void*)select_kernel<false>, (const void*)select_kernel<true>}) {
       cudaError_t e = cudaFuncSetAttribute(kf, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (int)sizeof(SelectShared) + 4 * kSelMaxCached);
@@ -743,7 +764,9 @@ cudaError_t launch_evict_select(const float* weights, int64_t w_stride, const in
         e = cudaFuncSetAttribute(kf, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
     }
-    if (dev >= 0 && dev < 64) attr_done[dev] = true;
+    largest = largest_cluster((const void*)select_kernel<true>, kSelThreads,
+                              sizeof(SelectShared) + 4 * kSelMaxCached, kSelMaxCluster);
+    if (dev >= 0 && dev < 64) of_device[dev] = largest;
   }
   // The lengths are on the device, so the cluster is sized for the longest that the accounts hold:
   // as few CTAs as keep the keys in shared memory, and up to eight while SMs are left and a CTA has
@@ -752,7 +775,7 @@ cudaError_t launch_evict_select(const float* weights, int64_t w_stride, const in
   // 22.6, 22.6, 35; 48 of 40000 24.6, 18.4, 18.5, 28, 62; 128 of 4000 12.3, 12.7, 22, 43, 137.
   const int64_t sets = (int64_t)num_seqs * (per_head ? Hkv : 1);
   int64_t C = 1;
-  while (C < kSelMaxCluster &&
+  while (C < largest &&
          (C * kSelMaxCached < w_stride || (C < 8 && sets * C * 2 <= num_sms && C * 2048 < w_stride)))
     C *= 2;
   const int64_t slice = (w_stride + C - 1) / C + 64;
@@ -788,16 +811,18 @@ cudaError_t launch_evict_compact(const int32_t* index, int64_t index_stride, int
   const CompactParams p{index,     index_stride,  per_head,  seq_lens, keep,    block_table,
                         dst_table, max_pages,     dst_max_pages, num_pages, pool, weights,
                         w_stride,  Hkv,           status};
-  static bool attr_done[64] = {};
+  static int of_device[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
-  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+  int largest = dev >= 0 && dev < 64 ? of_device[dev] : 0;
+  if (largest == 0) {
     for (const void* kf : {(const void*)compact_kernel<4>, (const void*)compact_kernel<2>}) {
       const cudaError_t e =
           cudaFuncSetAttribute(kf, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
     }
-    if (dev >= 0 && dev < 64) attr_done[dev] = true;
+    largest = largest_cluster((const void*)compact_kernel<4>, kMoveThreads, 0, kMoveMaxCluster);
+    if (dev >= 0 && dev < 64) of_device[dev] = largest;
   }
   // the kept counts are on the device: sized for the most that the index holds, a wave per CTA, and
   // no more CTAs than run at once; in halves when clusters of the most CTAs still find places. One
@@ -809,7 +834,7 @@ cudaError_t launch_evict_compact(const int32_t* index, int64_t index_stride, int
   const int64_t units = pairs * ((halves ? 4 : 2) + extra);
   const int64_t tile = halves ? kMoveTile<2> : kMoveTile<4>;
   int64_t C = 1;
-  while (C < kMoveMaxCluster && C * tile < index_stride && units * C * 2 <= places) C *= 2;
+  while (C < largest && C * tile < index_stride && units * C * 2 <= places) C *= 2;
   if (units * C > 0x7FFFFFFF) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
