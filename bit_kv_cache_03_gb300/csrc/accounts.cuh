@@ -23,8 +23,9 @@ namespace kvnvfp4 {
 constexpr int kAccThreads = 256;
 constexpr int kAccPages = kAccThreads / 16;  // pages of a CTA: 16 threads per page, 4 keys each
 constexpr int kAccRows = 8;
-// Four (64 registers: the loads in flight spilled) took a decode call of 4 x 131072 tokens 78.0 us,
-// three 73.5, two 74.5; twice as many, shorter CTAs 76.3 (in one run; 75.7 for three since)
+// Four (64 registers: 56 bytes of spills, 88 in the tile plan's kernel) took a decode call of 4 x
+// 131072 tokens 78.0 us, three (80 registers: none, and 8 bytes) 73.5, two 74.5; twice as many, shorter
+// CTAs 76.3 (in one run; 75.7 for three since)
 constexpr int kAccCtasPerSm = 3;
 
 struct AccountParams {

@@ -501,8 +501,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_kernel(const SelectPara
   tied += __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_tied[lane] : 0);
   const uint32_t below = (1u << lane) - 1u;
   // keys equal to the edge: a part before the left-th of them keeps them all, one behind it none
-  // (written as comparisons: built from max(0, min(left - tied, my_tied)), nvcc 13.0.88 gave 0 for
-  // the part that keeps some of them)
+  // (written as comparisons: of int32 a, b and q = max(0, min(a, b)), nvcc 13.0.88 compiles q == b to
+  // false where it holds, as a kernel of that line alone shows, unless ptxas runs at -O0; q is right)
   const int32_t to_come = (int32_t)left - tied;
   const int32_t quota = to_come <= 0 ? 0 : to_come < my_tied ? to_come : my_tied;
   int32_t* dst = out + lo + over + (to_come > 0 ? tied : (int32_t)left);
@@ -574,8 +574,9 @@ struct CompactParams {
 // Bounds: 296 bytes per kept row and KV head, but the rows lie apart: a K row's codes are four
 // 16-byte pieces in sectors that hold a neighbour's piece as well, its scales two words in two more,
 // and DRAM gives 64 bytes at a time. 4 x 4 sets, 16384 kept of 131072: 78 MB of rows move, 184 MB
-// cross the memory bus, in 43 us (4.3 TB/s). One CTA per part took 272 us, waves without reads
-// ahead 45 us, eight rows per thread at two CTAs per SM 59 us, two rows at six 55 us, clusters of nine
+// cross the memory bus, in 43 us (4.3 TB/s). One CTA per part took 272 us, waves with branches
+// around the loads (and 144 bytes of spills) 74 us, unconditional loads without reads ahead 45 us (8
+// bytes; 20 now, and none in halves), eight rows per thread at two CTAs per SM 59 us, two rows at six 55 us, clusters of nine
 // instead of eight (432 CTAs, not 384) the same 43. A gather of the same K and V rows into another
 // buffer, without any order or meeting, takes 37 us whatever its grid.
 constexpr int kMoveThreads = 256;

@@ -20,8 +20,8 @@
 // wait is bounded in time, as in the attention kernels.
 //
 // Bounds. 48 rows over 4 x 100000 tokens, 4 KV heads: 115 MB of K and 13 MB of accounts, 19 us of HBM
-// time; the pass takes 32 us of that call's 107, most of it with the sums left out too (28). 384 rows
-// over 2 x 32768 tokens: 0.1 G exponentials; the pass takes 29 to 37 us of that call's 86. Neither
+// time; the call takes 107 us with the pass and 74 without it, most of the difference with the sums left
+// out too (28). 384 rows over 2 x 32768 tokens: 0.1 G exponentials; 86 us with the pass, 50 without. Neither
 // memory (43 % and 6 % of DRAM throughput) nor issue slots (45 % and 40 %) are full. Of the second
 // call's 2.0K cycles per step and CTA, 0.8K are left when the warps only hand over (no product, load or
 // sum), the MMAs add 0.5K, the loads nothing, the exponentials 0.3K, the statistics' loads and the rest
