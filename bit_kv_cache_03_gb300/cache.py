@@ -86,7 +86,9 @@ class PagedNVFP4Cache:
 
     # -- attention that accounts for each key's weight, and eviction by it -----------------------
     def weight_accounts(self):
-        """Zeroed accounts [num_seqs, num_kv_heads, slots] for attend_weights and evict."""
+        """Zeroed accounts [num_seqs, num_kv_heads, slots] for attend_weights and evict, for every slot
+        of the block table (evict is sized by their width: accounts no wider than the longest sequence
+        will be also do, and are faster to choose from when there are many sequences)."""
         return torch.zeros(self.num_seqs, self.layout.num_kv_heads, self.max_pages * 64,
                            dtype=torch.float32, device=self.device)
 
@@ -94,7 +96,10 @@ class PagedNVFP4Cache:
                        stream=None):
         """attend() with a bf16 `out`, adding every key's attention weight to `weights` (or writing
         weights_in plus them). On the plan of the last plan(), whose workspace and this call's belong
-        to one call at a time."""
+        to one call at a time: a call on another stream has to be ordered behind the one before it.
+        With at most 8 query rows per KV head this call's workspace takes 4 bytes per row and cached
+        token of every KV head. A captured call replays on the plan that it was captured with: a later
+        plan() that fits the same workspace overwrites it."""
         self._check_accounts(weights, weights_in)
         if self.plan_info is None:
             raise ValueError("attend_weights needs a plan()")
@@ -128,7 +133,10 @@ class PagedNVFP4Cache:
         in place. Tokens so protected rank by slot alone: a keep below sink + recent drops the newest of
         them, the last token first. seq_lens, keep: device int32 [num_seqs]; index: device int32
         [num_seqs, num_kv_heads, n] (every KV head keeps its own tokens) or [num_seqs, 1, n] (one
-        set for all), n at least the largest kept count; receives the kept slots, ascending."""
+        set for all), n at least the largest kept count; receives the kept slots, ascending. A sequence
+        holds min(seq_len, keep) tokens afterwards; its next ones go behind them with append(slots=...)
+        under their own positions (decode_step takes the position from the slot, which is no longer
+        right). No page may belong to two sequences."""
         self._check_accounts(weights)
         for x in (seq_lens, keep):
             if x.dtype != torch.int32 or not x.is_contiguous() or x.numel() != self.num_seqs or \
@@ -194,7 +202,8 @@ class PagedNVFP4Cache:
     # -- append of the step's new tokens + attention, one launch ------------------------------
     def decode_step(self, q, k, v, out, q_codes=None, q_scales=None, sm_scale=None, stream=None):
         """New tokens of every sequence (sequence-major rows, at the last q_len positions of the
-        lengths given to the last plan) appended and attended in one kernel launch."""
+        lengths given to the last plan) appended and attended in one kernel launch. The positions are
+        the slots too: not for a cache that evict() compacted, whose tokens have other positions."""
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(128)
         self._hold_captured(stream)

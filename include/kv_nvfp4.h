@@ -266,7 +266,9 @@ kv_nvfp4_status kv_nvfp4_decode_attn(const kv_nvfp4_layout *layout,
  *              as for kv_nvfp4_decode_attn (any plan that it takes)
  *   d_weights_workspace, ww_bytes: DEVICE, 16-byte aligned, at least
  *              kv_nvfp4_weights_workspace_bytes(layout, plan) bytes; belongs to the call like
- *              d_workspace (calls that overlap on it race)
+ *              d_workspace (calls that overlap on it race). With at most 8 rows per KV head it holds
+ *              the fp32 score of every row and cached slot: 24 bytes per token and KV head for 6
+ *              rows, 32 for 8, beside the 144 that the cache has
  *   out:       DEVICE bf16 [num_seqs * q_len][num_q_heads][128], 16-byte aligned: the fp32 result
  *              of kv_nvfp4_decode_attn rounded once to bf16. A row all of whose pages are bad
  *              gets zeros and adds no weight.
@@ -292,6 +294,8 @@ kv_nvfp4_status kv_nvfp4_decode_attn_weights(
  * kv_nvfp4_evict_compact moves them to the front of the sequence's cache, after which the pages
  * behind ceil(kept / 64) are free, kv_nvfp4_plan takes the kept count as the sequence's length,
  * and kv_nvfp4_append_slots appends behind it. K rows keep the RoPE angle of their own position.
+ * kv_nvfp4_decode_step and kv_nvfp4_decode_step_host take a new token's position from its slot, so
+ * they are not for a sequence that was compacted and has RoPE: they would turn by the wrong angle.
  *
  * Select: per sequence and KV head (per_head != 0), or per sequence with one set for all its heads
  * (per_head == 0), the kept = min(seq_len, keep) slots that come first when ordered by
@@ -300,7 +304,9 @@ kv_nvfp4_status kv_nvfp4_decode_attn_weights(
  *   2. the others by weight, the larger first (per_head == 0: the heads' weights added in fp32, head
  *      0 first); -0 equals 0, NaN counts below every other value;
  *   3. of equal weights the lower slot first.
- *   weights:   DEVICE fp32 [num_seqs][num_kv_heads][weights_stride]
+ *   weights:   DEVICE fp32 [num_seqs][num_kv_heads][weights_stride]; the launch is sized by the
+ *              stride (the lengths are on the device), so far wider accounts than the sequences are
+ *              long cost time when there are many sets
  *   d_seq_lens, d_keep: DEVICE int32 [num_seqs]
  *   d_index:   DEVICE int32 [num_seqs][num_kv_heads, or 1][index_stride]: the kept slots in
  *              ascending order, entries from kept on left as they were
@@ -346,7 +352,8 @@ kv_nvfp4_status kv_nvfp4_evict_compact(const kv_nvfp4_layout *layout, const int3
  * by the CTA that reads their page, and the Q rows used straight from shared memory.
  *   plan, d_workspace: from kv_nvfp4_plan over the lengths INCLUDING the new tokens (same stream)
  *   q, k, v:   DEVICE bf16 [num_seqs * q_len][num_q_heads | num_kv_heads][128], sequence-major:
- *              row s * q_len + i is new token i of sequence s, at position seq_len_s - q_len + i
+ *              row s * q_len + i is new token i of sequence s, at position seq_len_s - q_len + i, the
+ *              same for its slot and its RoPE angle
  *   d_rope_table, rope_max_pos, d_block_table, max_pages, num_pages, pool: as for the append
  *   q_codes_out, q_scales_out: optional (both or neither) DEVICE copy of the encoded Q rows,
  *              [num_seqs * q_len][num_q_heads][64 | 8] (q_codes_out 16-byte aligned, else EINVAL)
