@@ -169,6 +169,15 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
+def _capturing(stream) -> bool:
+    """Whether a stream (an object or its handle) is being captured into a graph; asked of the runtime
+    that the library is linked with, since torch answers for its current stream only (and to make
+    another one current for the question takes 8 us)."""
+    state = ctypes.c_int(0)
+    return lib().cudaStreamIsCapturing(_P(_stream(stream)), ctypes.byref(state)) == 0 and \
+        state.value != 0
+
+
 def make_layout(num_q_heads=24, num_kv_heads=4, head_dim=128, page_size=64, rot_dim=32) -> Layout:
     L = Layout(num_q_heads, num_kv_heads, head_dim, page_size, rot_dim)
     _check(lib().kv_nvfp4_layout_check(ctypes.byref(L)), "kv_nvfp4_layout_check")

@@ -9,7 +9,7 @@ import math
 import numpy as np
 import torch
 
-from . import (_stream, kv_nvfp4_append, kv_nvfp4_append_slots, kv_nvfp4_decode_attn,
+from . import (_capturing, kv_nvfp4_append, kv_nvfp4_append_slots, kv_nvfp4_decode_attn,
                kv_nvfp4_decode_attn_weights, kv_nvfp4_decode_step, kv_nvfp4_decode_step_host,
                kv_nvfp4_evict_compact, kv_nvfp4_evict_select, kv_nvfp4_plan,
                kv_nvfp4_plan_workspace_bytes, kv_nvfp4_pool_bytes, kv_nvfp4_rope_table_init,
@@ -171,12 +171,7 @@ class PagedNVFP4Cache:
     def _hold_captured(self, stream):
         """A graph replays a captured call on the workspaces that the call had: they live as long as the
         cache does, outgrown or not."""
-        if _stream(stream) == _stream(None):
-            capturing = torch.cuda.is_current_stream_capturing()
-        else:
-            with self._on(stream):
-                capturing = torch.cuda.is_current_stream_capturing()
-        if capturing:
+        if torch.cuda.is_current_stream_capturing() if stream is None else _capturing(stream):
             self._captured += [b for b in (self.workspace, self.weights_workspace)
                                if b is not None and all(b is not x for x in self._captured)]
 

@@ -52,3 +52,8 @@ def test_attend_weights_refuses_a_plan_of_more_sequences(calls):
     c, (codes, scales), out, w = _cache(num_seqs=3, plan=(10, 10))
     c.attend_weights(codes, scales, out, w)  # the first two of three
     assert calls == ["kv_nvfp4_decode_attn_weights"]
+
+
+def test_the_runtime_that_the_library_is_linked_with_is_reached():
+    import bit_kv_cache_03_gb300 as kv
+    assert kv.lib().cudaStreamIsCapturing

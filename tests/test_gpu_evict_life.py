@@ -149,3 +149,17 @@ def test_a_growing_sequence_seldom_needs_another_workspace(monkeypatch):
     assert grown.count("weights_workspace") == 2  # the first, and one with room for more
     torch.cuda.synchronize()
     assert int(s.c.status.item()) == 0
+
+
+def test_capturing_is_asked_of_the_given_stream():
+    import bit_kv_cache_03_gb300 as k
+    side, other, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    x = torch.zeros(4, device="cuda")
+    assert not k._capturing(side) and not k._capturing(0)
+    with torch.cuda.graph(graph, stream=side):
+        x += 1
+        seen = [k._capturing(s) for s in (side, side.cuda_stream, other, other.cuda_stream)]
+    assert seen == [True, True, False, False] and not k._capturing(side)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert x.tolist() == [1] * 4
