@@ -22,6 +22,9 @@ KV_NVFP4_EINVAL = -1
 KV_NVFP4_ECUDA = -2
 KV_NVFP4_ENOSPACE = -3
 DEV_BAD_PAGE, DEV_BAD_POS, DEV_BAD_SEQ, DEV_BAD_ROPE, DEV_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x10
+DEV_NO_PAGE = 0x20
+MAX_TREE = 256  # KV_NVFP4_MAX_TREE
+MAX_ACCOUNTED_SEQS = 8192  # KV_NVFP4_MAX_ACCOUNTED_SEQS
 NOALLOC_SCRATCH_BYTES = 32 << 20  # KV_NVFP4_NOALLOC_SCRATCH_BYTES
 
 
@@ -40,6 +43,13 @@ class PlanInfo(ctypes.Structure):
         ("total_kv_tokens", ctypes.c_int64), ("total_pages", ctypes.c_int64)] + [
         (n, ctypes.c_uint64) for n in ("off_groups", "off_segments", "off_cta", "off_split",
                                        "off_partials", "workspace_bytes")]
+
+
+class Pages(ctypes.Structure):
+    """kv_nvfp4_pages; `buffers` holds what the addresses point to"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("block_table", "held", "refs", "free_list",
+                                               "free_count", "workspace")] + [
+        (n, ctypes.c_int32) for n in ("num_seqs", "max_pages", "num_pages")]
 
 
 class KVNVFP4Error(RuntimeError):
@@ -90,6 +100,16 @@ _SIG = {
                                _P, _I64, _P, _P], _I32),
     "kv_nvfp4_evict_compact": ([ctypes.POINTER(Layout), _P, _I64, _I32, _P, _P, _I32, _P, _I32,
                                 _I32, _P, _P, _I32, _P, _I64, _P, _P], _I32),
+    "kv_nvfp4_tree_mask": ([_P, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P], _I32),
+    "kv_nvfp4_tree_attn": ([ctypes.POINTER(Layout), ctypes.POINTER(PlanInfo), _P, _P, _P, _P,
+                            ctypes.c_float, _P, _I32, _P, _I32, _P, _P, _P], _I32),
+    "kv_nvfp4_tree_accept": ([ctypes.POINTER(Layout), _P, _P, _P, _P, _I32, _I32, _P, _P, _I32, _I32,
+                              _P, _P, _P, _P, _P, _P, _P], _I32),
+    "kv_nvfp4_pages_workspace_bytes": ([_I32], ctypes.c_size_t),
+    "kv_nvfp4_pages_init": ([ctypes.POINTER(Pages), _P], _I32),
+    "kv_nvfp4_pages_fork": ([ctypes.POINTER(Pages), _P, _P, _P, _I32, _P, _P], _I32),
+    "kv_nvfp4_pages_resize": ([ctypes.POINTER(Pages), _P, _P, _P, _P, _P], _I32),
+    "kv_nvfp4_copy_pages": ([ctypes.POINTER(Layout), _P, _I32, _P, _I32, _P, _P], _I32),
     "kv_cmp_page_bytes": ([ctypes.POINTER(Layout), _I32], ctypes.c_size_t),
     "kv_cmp_append": ([ctypes.POINTER(Layout), _I32, _P, _P, _P, _P, _P, _I32, _P, _I32, _P, _I32,
                        _I32, _I32, _P, _P, _P, _P], _I32),
@@ -331,6 +351,82 @@ def kv_nvfp4_evict_compact(layout, index, index_stride, per_head, seq_lens, keep
         num_seqs, _ptr(block_table), max_pages, num_pages, _ptr(pool), _ptr(dst_block_table),
         dst_max_pages, _ptr(weights), weights_stride, _ptr(status), _stream(stream)),
         "kv_nvfp4_evict_compact")
+
+
+def kv_nvfp4_tree_mask(parents, num_seqs, n, lens, first_pos, mask, seq_ids=None, slots=None,
+                       positions=None, status=None, stream=None):
+    """Masks of drafted trees from their parents, with each node's sequence, slot and position as
+    kv_nvfp4_append_slots takes them (first_pos None: the position is counted from the length)."""
+    _check(lib().kv_nvfp4_tree_mask(
+        _ptr(parents), num_seqs, n, _ptr(lens), _ptr(first_pos), _ptr(mask), _ptr(seq_ids),
+        _ptr(slots), _ptr(positions), _ptr(status), _stream(stream)), "kv_nvfp4_tree_mask")
+
+
+def kv_nvfp4_tree_attn(layout, plan: PlanInfo, workspace, q_codes, q_scales, mask, sm_scale, pool,
+                       num_pages, block_table, max_pages, out, status=None, stream=None):
+    """Attention of a tree's nodes (bf16 output): each sees the cache and the nodes in its mask."""
+    _check(lib().kv_nvfp4_tree_attn(
+        ctypes.byref(layout), ctypes.byref(plan), _ptr(workspace), _ptr(q_codes), _ptr(q_scales),
+        _ptr(mask), float(sm_scale), _ptr(pool), num_pages, _ptr(block_table), max_pages, _ptr(out),
+        _ptr(status), _stream(stream)), "kv_nvfp4_tree_attn")
+
+
+def kv_nvfp4_tree_accept(layout, parents, draft, target, expected, num_seqs, n, lens, block_table,
+                         max_pages, num_pages, pool, path, count, next_token, new_lens=None,
+                         status=None, stream=None):
+    """The path that the model agrees with, and its rows moved behind the cache (pool None: not
+    moved; parents, draft, target, expected, next_token None: path and count are given)."""
+    _check(lib().kv_nvfp4_tree_accept(
+        ctypes.byref(layout), _ptr(parents), _ptr(draft), _ptr(target), _ptr(expected), num_seqs, n,
+        _ptr(lens), _ptr(block_table), max_pages, num_pages, _ptr(pool), _ptr(path), _ptr(count),
+        _ptr(next_token), _ptr(new_lens), _ptr(status), _stream(stream)), "kv_nvfp4_tree_accept")
+
+
+def kv_nvfp4_pages_workspace_bytes(num_pages) -> int:
+    return int(lib().kv_nvfp4_pages_workspace_bytes(num_pages))
+
+
+def make_pages(block_table, held, refs, free_list, free_count, workspace) -> Pages:
+    """The accounts over device int32 tensors block_table [num_seqs, max_pages], held [num_seqs], refs
+    and free_list [num_pages], free_count [1] and a workspace of kv_nvfp4_pages_workspace_bytes, all of
+    which it keeps alive."""
+    S, P = block_table.shape
+    N = refs.numel()
+    for x, size in ((block_table, S * P), (held, S), (refs, N), (free_list, N), (free_count, 1)):
+        if x.element_size() != 4 or not x.is_contiguous() or x.numel() != size or \
+                x.device != refs.device or x.is_floating_point():
+            raise ValueError("the accounts are contiguous int32 on one device")
+    if workspace.device != refs.device or not workspace.is_contiguous() or \
+            workspace.nbytes < kv_nvfp4_pages_workspace_bytes(N):
+        raise ValueError("the accounts' workspace is too small")
+    p = Pages(*(_ptr(x) for x in (block_table, held, refs, free_list, free_count, workspace)), S, P, N)
+    p.buffers = (block_table, held, refs, free_list, free_count, workspace)
+    return p
+
+
+def kv_nvfp4_pages_init(pages: Pages, stream=None):
+    """Every page free, no sequence holds one."""
+    _check(lib().kv_nvfp4_pages_init(ctypes.byref(pages), _stream(stream)), "kv_nvfp4_pages_init")
+
+
+def kv_nvfp4_pages_fork(pages: Pages, src, dst, lens, n, status=None, stream=None):
+    """Sequences dst[i] share the pages of the first lens[i] tokens of sequences src[i]."""
+    _check(lib().kv_nvfp4_pages_fork(ctypes.byref(pages), _ptr(src), _ptr(dst), _ptr(lens), n,
+                                     _ptr(status), _stream(stream)), "kv_nvfp4_pages_fork")
+
+
+def kv_nvfp4_pages_resize(pages: Pages, keep_lens, new_lens, copies, status=None, stream=None):
+    """Room for new_lens tokens of each sequence, of which keep_lens stay; copies receives the page
+    pairs for kv_nvfp4_copy_pages."""
+    _check(lib().kv_nvfp4_pages_resize(ctypes.byref(pages), _ptr(keep_lens), _ptr(new_lens),
+                                       _ptr(copies), _ptr(status), _stream(stream)),
+           "kv_nvfp4_pages_resize")
+
+
+def kv_nvfp4_copy_pages(layout, pool, num_pages, pairs, n, status=None, stream=None):
+    """Pool page pairs[i][1] <- page pairs[i][0]; (-1, -1) is skipped."""
+    _check(lib().kv_nvfp4_copy_pages(ctypes.byref(layout), _ptr(pool), num_pages, _ptr(pairs), n,
+                                     _ptr(status), _stream(stream)), "kv_nvfp4_copy_pages")
 
 
 def kv_nvfp4_decode_step(layout, plan: PlanInfo, workspace, q, k, v, rope, rope_max_pos,

@@ -29,7 +29,7 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
                           const uint16_t* v_new, const float* rope, int32_t rope_max_pos,
                           int32_t rot_dim, uint8_t* pool_w, uint8_t* q_codes_out,
                           uint8_t* q_scales_out, bool late_tables, uint16_t* out16, float2* stats,
-                          float* scores, float* part_l, cudaStream_t stream);
+                          float* scores, float* part_l, const uint32_t* mask, cudaStream_t stream);
 cudaError_t launch_merge_weights(const void* groups, const int32_t* split_groups,
                                  int32_t num_split, const float* partials, uint16_t* out16,
                                  const float2* stats, const float* scores, const float* w_in,
@@ -56,7 +56,7 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
                         const int32_t* split_groups, int32_t num_split, float* partials,
                         float* out, int32_t* status, int32_t Hq, int32_t Hkv, int32_t q_len,
                         int32_t causal, int32_t grid, float sm_scale, uint16_t* out16,
-                        float2* stats, float* part_l, cudaStream_t stream);
+                        float2* stats, float* part_l, const uint32_t* mask, cudaStream_t stream);
 cudaError_t launch_tile_merge_weights(const void* groups, const int32_t* split_groups,
                                       int32_t num_split, const float* partials,
                                       const float* part_l, uint16_t* out16, float2* stats,
@@ -90,6 +90,25 @@ cudaError_t launch_step_inputs(const void* const src[3], void* const dst[3],
                                const uint32_t n16[3], const void* plan, uint32_t plan_bytes,
                                void* workspace, cudaStream_t stream);
 int inline_plan_bytes();
+cudaError_t launch_tree_mask(const int32_t* parents, int32_t num_seqs, int32_t n,
+                             const int32_t* lens, const int32_t* first_pos, uint32_t* mask,
+                             int32_t* seq_ids, int32_t* slots, int32_t* positions, int32_t* status,
+                             cudaStream_t stream);
+cudaError_t launch_tree_accept(const int32_t* parents, const int32_t* draft, const int32_t* target,
+                               const int32_t* expected, int32_t num_seqs, int32_t n,
+                               const int32_t* lens, const int32_t* block_table, int32_t max_pages,
+                               int32_t num_pages, uint8_t* pool, int32_t* path, int32_t* count,
+                               int32_t* next, int32_t* new_lens, int32_t Hkv, int32_t* status,
+                               cudaStream_t stream);
+uint64_t pages_workspace_bytes(int32_t num_pages);
+cudaError_t launch_pages_init(const kv_nvfp4_pages* p, int32_t num_sms, cudaStream_t stream);
+cudaError_t launch_pages_fork(const kv_nvfp4_pages* p, const int32_t* src, const int32_t* dst,
+                              const int32_t* lens, int32_t n, int32_t* status,
+                              cudaStream_t stream);
+cudaError_t launch_pages_resize(const kv_nvfp4_pages* p, const int32_t* keep, const int32_t* room,
+                                int32_t* copies, int32_t* status, cudaStream_t stream);
+cudaError_t launch_copy_pages(uint8_t* pool, const int32_t* pairs, int32_t n, int32_t num_pages,
+                              int32_t Hkv, int32_t num_sms, int32_t* status, cudaStream_t stream);
 }  // namespace kvnvfp4
 
 namespace {
@@ -122,6 +141,7 @@ kv_nvfp4_status cuda_status(cudaError_t e) {
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int num_sms_current_device() {
@@ -493,7 +513,7 @@ static kv_nvfp4_status decode_step_impl(const kv_nvfp4_layout* L, const kv_nvfp4
       L->num_q_heads, L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
       (const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, d_rope_table, rope_max_pos,
       L->rot_dim, pool, q_codes_out, q_scales_out, late_tables, nullptr, nullptr,
-      nullptr, nullptr, (cudaStream_t)stream);
+      nullptr, nullptr, nullptr, (cudaStream_t)stream);
   return cuda_status(e);
 }
 
@@ -537,6 +557,18 @@ static bool plan_matches(const kv_nvfp4_layout* L, const kv_nvfp4_plan_info* pla
   return plan->num_row_groups == (rows + tile_rows - 1) / tile_rows &&
          plan->num_groups ==
              (int64_t)plan->num_seqs * plan->num_row_groups * (tile ? L->num_kv_heads : 1);
+}
+
+// Whether accounts can be worked on.
+static bool pages_valid(const kv_nvfp4_pages* p) {
+  if (p == nullptr || p->num_seqs <= 0 || p->num_seqs > KV_NVFP4_MAX_ACCOUNTED_SEQS ||
+      p->max_pages <= 0 || p->num_pages <= 0 ||
+      (int64_t)p->num_seqs * p->max_pages > 0x7FFFFFFF)
+    return false;
+  const void* words[] = {p->block_table, p->held, p->refs, p->free_list, p->free_count};
+  for (const void* w : words)
+    if (w == nullptr || !aligned4(w)) return false;
+  return p->workspace != nullptr && aligned8(p->workspace);
 }
 
 // The second workspace of kv_nvfp4_decode_attn_weights: each row's softmax statistics, on a tile plan
@@ -755,7 +787,7 @@ kv_nvfp4_status kv_nvfp4_decode_attn(const kv_nvfp4_layout* L, const kv_nvfp4_pl
                              (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
                              (float*)(ws + plan->off_partials), out, d_status, L->num_q_heads,
                              L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
-                             nullptr, nullptr, nullptr, (cudaStream_t)stream);
+                             nullptr, nullptr, nullptr, nullptr, (cudaStream_t)stream);
   } else {
     e = kvnvfp4::launch_decode(
         q_codes, q_scales, pool, d_block_table, max_pages, num_pages, ws + plan->off_groups,
@@ -764,7 +796,7 @@ kv_nvfp4_status kv_nvfp4_decode_attn(const kv_nvfp4_layout* L, const kv_nvfp4_pl
         (float*)(ws + plan->off_partials), out, d_status,
         L->num_q_heads, L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
         nullptr, nullptr, nullptr, nullptr, 0, 0, nullptr, nullptr, nullptr, false, nullptr,
-        nullptr, nullptr, nullptr, (cudaStream_t)stream);
+        nullptr, nullptr, nullptr, nullptr, (cudaStream_t)stream);
   }
   return cuda_status(e);
 }
@@ -815,7 +847,7 @@ kv_nvfp4_status kv_nvfp4_decode_attn_weights(
                              (const int32_t*)(ws + plan->off_cta), split, plan->num_split_groups,
                              partials, nullptr, d_status, L->num_q_heads, L->num_kv_heads,
                              plan->q_len, plan->causal, plan->grid, sm_scale, (uint16_t*)out, stats,
-                             part_l, (cudaStream_t)stream);
+                             part_l, nullptr, (cudaStream_t)stream);
   } else {
     e = kvnvfp4::launch_decode(
         q_codes, q_scales, pool, d_block_table, max_pages, num_pages, ws + plan->off_groups,
@@ -823,7 +855,7 @@ kv_nvfp4_status kv_nvfp4_decode_attn_weights(
         plan->num_split_groups, partials, nullptr, d_status, L->num_q_heads, L->num_kv_heads,
         plan->q_len, plan->causal, plan->grid, sm_scale, nullptr, nullptr, nullptr, nullptr, 0, 0,
         nullptr, nullptr, nullptr, false, (uint16_t*)out, stats, scores, part_l,
-        (cudaStream_t)stream);
+        nullptr, (cudaStream_t)stream);
     if (e == cudaSuccess)
       e = tile ? kvnvfp4::launch_tile_merge_weights(
                      ws + plan->off_groups, split, plan->num_split_groups, partials, part_l,
@@ -887,6 +919,135 @@ kv_nvfp4_status kv_nvfp4_evict_compact(const kv_nvfp4_layout* L, const int32_t* 
       num_pages, pool, in_place ? d_block_table : d_dst_block_table,
       in_place ? max_pages : dst_max_pages, weights, weights_stride, L->num_kv_heads,
       num_sms_current_device(), d_status, (cudaStream_t)stream));
+}
+
+// ---- trees of drafted tokens -------------------------------------------------------------------
+kv_nvfp4_status kv_nvfp4_tree_mask(const int32_t* d_parents, int32_t num_seqs, int32_t n,
+                                   const int32_t* d_lens, const int32_t* d_first_pos,
+                                   uint32_t* d_mask, int32_t* d_seq_ids, int32_t* d_slots,
+                                   int32_t* d_positions, int32_t* d_status, void* stream) {
+  if (num_seqs < 0 || n < 1 || n > KV_NVFP4_MAX_TREE) return KV_NVFP4_EINVAL;
+  if (num_seqs == 0) return KV_NVFP4_OK;
+  if (!d_parents || !d_lens || !d_mask) return KV_NVFP4_EINVAL;
+  const bool some = d_seq_ids || d_slots || d_positions;
+  if (some && !(d_seq_ids && d_slots && d_positions)) return KV_NVFP4_EINVAL;
+  const void* words[] = {d_parents, d_lens, d_first_pos, d_mask, d_seq_ids, d_slots, d_positions};
+  for (const void* p : words)
+    if (!aligned4(p)) return KV_NVFP4_EINVAL;
+  return cuda_status(kvnvfp4::launch_tree_mask(d_parents, num_seqs, n, d_lens, d_first_pos, d_mask,
+                                               d_seq_ids, d_slots, d_positions, d_status,
+                                               (cudaStream_t)stream));
+}
+
+kv_nvfp4_status kv_nvfp4_tree_attn(const kv_nvfp4_layout* L, const kv_nvfp4_plan_info* plan,
+                                   void* d_workspace, const uint8_t* q_codes,
+                                   const uint8_t* q_scales, const uint32_t* d_mask, float sm_scale,
+                                   const uint8_t* pool, int32_t num_pages,
+                                   const int32_t* d_block_table, int32_t max_pages, void* out,
+                                   int32_t* d_status, void* stream) {
+  if (!plan_matches(L, plan) || plan->causal != 0 || plan->q_len > KV_NVFP4_MAX_TREE)
+    return KV_NVFP4_EINVAL;
+  if (!d_workspace || !q_codes || !q_scales || !d_mask || !pool || !d_block_table || !out ||
+      num_pages <= 0 || max_pages <= 0)
+    return KV_NVFP4_EINVAL;
+  if ((int64_t)plan->max_seq_len > (int64_t)max_pages * L->page_size) return KV_NVFP4_EINVAL;
+  const void* ptrs[] = {d_workspace, q_codes, q_scales, pool, out};
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return KV_NVFP4_EINVAL;
+  if (!aligned4(d_mask) || !aligned4(d_block_table)) return KV_NVFP4_EINVAL;
+  if (!(sm_scale > 0.0f)) sm_scale = 1.0f / std::sqrt((float)L->head_dim);
+  char* ws = (char*)d_workspace;
+  if (tile_mode(L, plan->q_len))
+    return cuda_status(kvnvfp4::launch_tile(
+        q_codes, q_scales, pool, d_block_table, max_pages, num_pages, ws + plan->off_groups,
+        ws + plan->off_segments, (const int32_t*)(ws + plan->off_cta),
+        (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
+        (float*)(ws + plan->off_partials), nullptr, d_status, L->num_q_heads, L->num_kv_heads,
+        plan->q_len, 0, plan->grid, sm_scale, (uint16_t*)out, nullptr, nullptr, d_mask,
+        (cudaStream_t)stream));
+  return cuda_status(kvnvfp4::launch_decode(
+      q_codes, q_scales, pool, d_block_table, max_pages, num_pages, ws + plan->off_groups,
+      ws + plan->off_segments, (const int32_t*)(ws + plan->off_cta),
+      (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
+      (float*)(ws + plan->off_partials), nullptr, d_status, L->num_q_heads, L->num_kv_heads,
+      plan->q_len, 0, plan->grid, sm_scale, nullptr, nullptr, nullptr, nullptr, 0, 0, nullptr,
+      nullptr, nullptr, false, (uint16_t*)out, nullptr, nullptr, nullptr, d_mask,
+      (cudaStream_t)stream));
+}
+
+kv_nvfp4_status kv_nvfp4_tree_accept(const kv_nvfp4_layout* L, const int32_t* d_parents,
+                                     const int32_t* d_draft, const int32_t* d_target,
+                                     const int32_t* d_expected, int32_t num_seqs, int32_t n,
+                                     const int32_t* d_lens, const int32_t* d_block_table,
+                                     int32_t max_pages, int32_t num_pages, uint8_t* pool,
+                                     int32_t* d_path, int32_t* d_count, int32_t* d_next,
+                                     int32_t* d_new_lens, int32_t* d_status, void* stream) {
+  if (kv_nvfp4_layout_check(L) != KV_NVFP4_OK || num_seqs < 0 || n < 1 || n > KV_NVFP4_MAX_TREE)
+    return KV_NVFP4_EINVAL;
+  if (num_seqs == 0) return KV_NVFP4_OK;
+  if (!d_lens || !d_path || !d_count) return KV_NVFP4_EINVAL;
+  const bool walk = d_parents != nullptr;
+  if ((d_draft != nullptr) != walk || (d_target != nullptr) != walk ||
+      (d_expected != nullptr) != walk || (d_next != nullptr) != walk)
+    return KV_NVFP4_EINVAL;
+  if (pool != nullptr
+          ? !d_block_table || max_pages <= 0 || num_pages <= 0 || !aligned16(pool)
+          : d_block_table != nullptr || max_pages != 0 || num_pages != 0 || !walk)
+    return KV_NVFP4_EINVAL;
+  const void* words[] = {d_parents, d_draft, d_target, d_expected, d_lens,
+                         d_block_table, d_path, d_count, d_next, d_new_lens};
+  for (const void* p : words)
+    if (!aligned4(p)) return KV_NVFP4_EINVAL;
+  return cuda_status(kvnvfp4::launch_tree_accept(
+      d_parents, d_draft, d_target, d_expected, num_seqs, n, d_lens, d_block_table, max_pages,
+      num_pages, pool, d_path, d_count, d_next, d_new_lens, L->num_kv_heads, d_status,
+      (cudaStream_t)stream));
+}
+
+// ---- page accounts -----------------------------------------------------------------------------
+size_t kv_nvfp4_pages_workspace_bytes(int32_t num_pages) {
+  return num_pages < 0 ? 0 : (size_t)kvnvfp4::pages_workspace_bytes(num_pages);
+}
+
+kv_nvfp4_status kv_nvfp4_pages_init(const kv_nvfp4_pages* pages, void* stream) {
+  if (!pages_valid(pages)) return KV_NVFP4_EINVAL;
+  const int sms = num_sms_current_device();
+  if (sms <= 0) return cuda_status(cudaErrorNoDevice);
+  return cuda_status(kvnvfp4::launch_pages_init(pages, sms, (cudaStream_t)stream));
+}
+
+kv_nvfp4_status kv_nvfp4_pages_fork(const kv_nvfp4_pages* pages, const int32_t* d_src,
+                                    const int32_t* d_dst, const int32_t* d_lens, int32_t n,
+                                    int32_t* d_status, void* stream) {
+  if (!pages_valid(pages) || n < 0 || n > pages->num_seqs) return KV_NVFP4_EINVAL;
+  if (n == 0) return KV_NVFP4_OK;
+  if (!d_src || !d_dst || !d_lens || !aligned4(d_src) || !aligned4(d_dst) || !aligned4(d_lens))
+    return KV_NVFP4_EINVAL;
+  return cuda_status(
+      kvnvfp4::launch_pages_fork(pages, d_src, d_dst, d_lens, n, d_status, (cudaStream_t)stream));
+}
+
+kv_nvfp4_status kv_nvfp4_pages_resize(const kv_nvfp4_pages* pages, const int32_t* d_keep_lens,
+                                      const int32_t* d_new_lens, int32_t* d_copies,
+                                      int32_t* d_status, void* stream) {
+  if (!pages_valid(pages) || !d_keep_lens || !d_new_lens || !d_copies) return KV_NVFP4_EINVAL;
+  if (!aligned4(d_keep_lens) || !aligned4(d_new_lens) || !aligned4(d_copies))
+    return KV_NVFP4_EINVAL;
+  return cuda_status(kvnvfp4::launch_pages_resize(pages, d_keep_lens, d_new_lens, d_copies,
+                                                  d_status, (cudaStream_t)stream));
+}
+
+kv_nvfp4_status kv_nvfp4_copy_pages(const kv_nvfp4_layout* L, uint8_t* pool, int32_t num_pages,
+                                    const int32_t* d_pairs, int32_t n, int32_t* d_status,
+                                    void* stream) {
+  if (kv_nvfp4_layout_check(L) != KV_NVFP4_OK || n < 0) return KV_NVFP4_EINVAL;
+  if (n == 0) return KV_NVFP4_OK;
+  if (!pool || !d_pairs || num_pages <= 0 || !aligned16(pool) || !aligned4(d_pairs))
+    return KV_NVFP4_EINVAL;
+  const int sms = num_sms_current_device();
+  if (sms <= 0) return cuda_status(cudaErrorNoDevice);
+  return cuda_status(kvnvfp4::launch_copy_pages(pool, d_pairs, n, num_pages, L->num_kv_heads, sms,
+                                                d_status, (cudaStream_t)stream));
 }
 
 kv_nvfp4_status kv_nvfp4_decode_step(const kv_nvfp4_layout* L, const kv_nvfp4_plan_info* plan,

@@ -173,6 +173,8 @@ struct DecodeParams {
   float2* stats;           // [num_seqs][Hkv][G * q_len]
   float* scores;           // [pages of all groups][Hkv][G * q_len][64 keys]; WIDE: [pages][rows][64]
   float* part_l;           // WIDE: l per partial row, [num_partials][128]
+  // TREE: which of the step's nodes a node sees, bit j of word j / 32; bf16 rows to out16
+  const uint32_t* mask;    // [num_seqs][q_len][ceil(q_len / 32)]
 };
 
 struct SegInfo {
@@ -491,8 +493,10 @@ __device__ __forceinline__ float pick8(const float (&v)[kRows], int i) {
 
 // Visibility of keys to the rows of the segment's row tile.
 struct RowVis {
-  int mylim;           // largest visible key position of row lane % 8 (-1 for a padding row)
-  int lim_min;         // the smallest limit over the real rows (that of row 0)
+  int mylim;           // largest visible key position of row lane % 8 (-1 for a padding row); TREE:
+                       // the nodes that it sees, as bits (at most 8 rows are at most 8 nodes)
+  int lim_min;         // the smallest limit over the real rows (that of row 0); TREE: the last key
+                       // before the nodes
   uint32_t rows_mask;  // bit i: row i is a real row
 };
 
@@ -511,7 +515,9 @@ __device__ __forceinline__ void s_issue(AttnCtx& c, uint32_t kk, uint32_t (&sr)[
 // below it are real (0 when the page was skipped).
 // ACC: the scores of the page's R real rows also go to `scores` (this head's [R][64] block), -inf
 // where the row does not see the key.
-template <int NR, bool ACC, bool WIDE>
+// TREE: a node's key whose V row holds a NaN makes NaN of the rows that see it, and its V scales turn
+// into zeros in the stage, so that the rows that do not see it (P = 0) take nothing from it.
+template <int NR, bool ACC, bool WIDE, bool TREE>
 __device__ __forceinline__ bool s_softmax(AttnCtx& c, uint32_t kk, uint32_t kst, int page, int len,
                                           float* scores, int R,
                                           const RowVis& rv, uint32_t (&sr)[8], float (&m)[kRows],
@@ -531,9 +537,28 @@ __device__ __forceinline__ bool s_softmax(AttnCtx& c, uint32_t kk, uint32_t kst,
   kv_lim = pvalid ? len - page * 64 : 0;
   if (!c.active) return false;
   uint32_t vmask = 0;  // bit i: this lane's key is visible to row i
+  bool v_nan = false;  // TREE: the key is a node's, and its V row holds a NaN
   if (pvalid) {
     if (page * 64 + 63 <= rv.lim_min) {
       vmask = rv.rows_mask;
+    } else if (TREE) {
+      const int node = page * 64 + c.key0 + c.lane - rv.lim_min - 1;
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        const uint32_t sees = (uint32_t)__shfl_sync(0xffffffffu, rv.mylim, i);
+        if (node < 0 || (node < 8 && ((sees >> node) & 1u))) vmask |= 1u << i;
+      }
+      vmask &= rv.rows_mask;
+      if (node >= 0 && node < 8) {
+        const uint32_t vs = c.sbase + kOffStage + st * Ring<WIDE>::kBytes + c.p->Hkv * 8704 +
+                            c.head * 512 + (c.key0 + c.lane) * 8;
+        const uint2 sc = lds64(vs);
+        v_nan = e4m3x4_any_nan(sc.x) || e4m3x4_any_nan(sc.y);
+        if (v_nan) {
+          asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(vs), "r"(0u) : "memory");
+          fence_async_smem();  // the stage's next page comes through the async proxy
+        }
+      }
     } else {
       const int kp = page * 64 + c.key0 + c.lane;
 #pragma unroll
@@ -580,6 +605,16 @@ __device__ __forceinline__ bool s_softmax(AttnCtx& c, uint32_t kk, uint32_t kst,
     lp[i] += p0;
     lp[i + 1] += p1;
     hi[i / 2] = pack_f16x2(p0, p1);
+  }
+  if (TREE && v_nan) {
+#pragma unroll
+    for (int i = 0; i < kRows; i += 2) {
+      const bool a = (vmask >> i) & 1u, b = (vmask >> (i + 1)) & 1u;
+      const float nan = __uint_as_float(0x7FC00000u);
+      if (a) lp[i] = nan;
+      if (b) lp[i + 1] = nan;
+      hi[i / 2] = (a ? 0x7E00u : 0u) | (b ? 0x7E000000u : 0u);  // f16 NaN
+    }
   }
   sts128(p_addr(pt, c.lane, 0), hi[0], hi[1], hi[2], hi[3]);
   return grow;
@@ -864,7 +899,7 @@ __device__ __forceinline__ void fused_prologue(const DecodeParams& p, const SegI
   if (nrows > 0 && aw == 0 && lane == 0) mbar_arrive(bars + 8 * kBarKvReady);
 }
 
-template <int NR, bool FUSED, bool ACC, bool WIDE>
+template <int NR, bool FUSED, bool ACC, bool WIDE, bool TREE>
 __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t tbase, int warp,
                                 int lane) {
   constexpr uint32_t kNum = Ring<WIDE>::kNum;
@@ -911,10 +946,16 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
     int mylim;
     {
       const int r = row0 + (lane & 7);
-      mylim = (r < rows_total) ? (p.causal ? L0 + r / p.G : sg.len - 1) : -1;
+      if (TREE)  // the nodes that the row's node sees; bits from q_len on count for nothing
+        mylim = r < rows_total
+                    ? (int)(__ldg(p.mask + (int64_t)sg.seq * p.q_len + r / p.G) & ((1u << p.q_len) - 1u))
+                    : 0;
+      else
+        mylim = (r < rows_total) ? (p.causal ? L0 + r / p.G : sg.len - 1) : -1;
     }
-    const int lim_min = __shfl_sync(0xffffffffu, mylim, 0);
-    const uint32_t rows_mask = __ballot_sync(0xffffffffu, mylim >= 0) & 0xFFu;
+    const int lim_min = TREE ? L0 - 1 : __shfl_sync(0xffffffffu, mylim, 0);
+    const uint32_t rows_mask =
+        __ballot_sync(0xffffffffu, TREE ? row0 + (lane & 7) < rows_total : mylim >= 0) & 0xFFu;
 
     // ---- this pair's Q tile (B operand of Q.K^T) and its scale factors ----
     if (FUSED) {
@@ -988,7 +1029,7 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
       if (ACC && (!WIDE || page < sg.hi))
         scores = p.scores + (((int64_t)sg.page0 + page) * (WIDE ? 1 : p.Hkv) + (WIDE ? 0 : c.head)) *
                                 rows_total * kPage;
-      const bool grow = s_softmax<NR, ACC, WIDE>(c, k, ks, page, sg.len, scores, rows_total, rv, sr,
+      const bool grow = s_softmax<NR, ACC, WIDE, TREE>(c, k, ks, page, sg.len, scores, rows_total, rv, sr,
                                                  m, lp, ps, t, c2, alpha_a, alpha_b, kv_lim);
       __syncwarp();
       if (grow) {  // entries 0, 2: row 2t; entries 1, 3: row 2t + 1
@@ -1142,14 +1183,14 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
               part[kRows * 128 + i] = M[hh];
               part[kRows * 128 + kRows + i] = L[hh];
             }
-          } else if (ACC) {
+          } else if (ACC || TREE) {
             if (r < rows_total) {
               const int tok = r / p.G, qh = head * p.G + r % p.G;
               const float inv = L[hh] > 0.f ? 1.f / L[hh] : 0.f;
               store_bf16x16(
                   p.out16 + (((int64_t)sg.seq * p.q_len + tok) * p.Hq + qh) * 128 + 16 * g, o[hh],
                   inv);
-              if (g == 0)
+              if (ACC && g == 0)
                 p.stats[((int64_t)sg.seq * p.Hkv + head) * rows_total + r] =
                     make_float2(M[hh], inv);
             }
@@ -1173,8 +1214,9 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
 // NR: query rows computed per head (6 when no tile has more real rows, else all 8); FUSED: the
 // step's append is done in the kernel (kv_nvfp4_decode_step); ACC: rows go out in bf16 with their
 // softmax statistics, for the weights after it (kv_nvfp4_decode_attn_weights); WIDE: groups of one KV
-// head, four pages per stage
-template <int NR, bool FUSED, bool ACC, bool WIDE = false>
+// head, four pages per stage; TREE: the new tokens are the nodes of a tree (kv_nvfp4_tree_attn), rows
+// go out in bf16
+template <int NR, bool FUSED, bool ACC, bool WIDE = false, bool TREE = false>
 __global__ void __launch_bounds__(kBoundThreads, 1) decode_kernel(const DecodeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1228,7 +1270,7 @@ __global__ void __launch_bounds__(kBoundThreads, 1) decode_kernel(const DecodePa
   } else if (warp == kWarpMma) {
     qk_warp<FUSED, WIDE>(p, smem, tbase, lane);
   } else {
-    attention_warps<NR, FUSED, ACC, WIDE>(p, smem, tbase, warp, lane);
+    attention_warps<NR, FUSED, ACC, WIDE, TREE>(p, smem, tbase, warp, lane);
   }
 
   if (warp == kWarpMma) {
@@ -1267,7 +1309,9 @@ constexpr int kMergePerRound = 8;  // partials a slice requests at once (64 per 
 
 // LATE_TABLES: the plan tables were written by a kernel earlier in the same step (not by a copy
 // before the attention launch), so they are read only after the wait as well.
-template <bool LATE_TABLES, bool ACC>
+// TREE: a partial without a maximum may hold NaN (a row whose keys' scores are all NaN), so it is added
+// rather than skipped; without a visible key it holds zeros.
+template <bool LATE_TABLES, bool ACC, bool TREE = false>
 __device__ __forceinline__ void merge_row(const MergeParams& p, int split_index, int row) {
   __shared__ float s_m[kMergeSlices], s_l[kMergeSlices];
   __shared__ float4 s_o[kMergeSlices][32];
@@ -1308,14 +1352,15 @@ __device__ __forceinline__ void merge_row(const MergeParams& p, int split_index,
     float mn = M;
 #pragma unroll
     for (int u = 0; u < kMergePerRound; ++u) mn = fmaxf(mn, mq[u]);
-    if (mn == -INFINITY) continue;  // no visible key in any partial so far
-    const float a = fast_exp2((M - mn) * p.c2);  // 0 while M is -inf
+    if (!TREE && mn == -INFINITY) continue;  // no visible key in any partial so far
+    // 0 while M is -inf
+    const float a = TREE && M == -INFINITY ? 0.f : fast_exp2((M - mn) * p.c2);
     L *= a;
     O.x *= a; O.y *= a; O.z *= a; O.w *= a;
 #pragma unroll
     for (int u = 0; u < kMergePerRound; ++u) {
-      if (mq[u] == -INFINITY) continue;  // a segment with no visible key, or none at all
-      const float f = fast_exp2((mq[u] - mn) * p.c2);
+      if (!TREE && mq[u] == -INFINITY) continue;  // a segment with no visible key, or none at all
+      const float f = TREE && mq[u] == -INFINITY ? 0.f : fast_exp2((mq[u] - mn) * p.c2);
       L += f * lq[u];
       O.x += f * ov[u].x; O.y += f * ov[u].y; O.z += f * ov[u].z; O.w += f * ov[u].w;
     }
@@ -1332,8 +1377,8 @@ __device__ __forceinline__ void merge_row(const MergeParams& p, int split_index,
     float4 Ot = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < kMergeSlices; ++j) {
-      if (s_m[j] == -INFINITY) continue;
-      const float f = fast_exp2((s_m[j] - Mt) * p.c2);
+      if (!TREE && s_m[j] == -INFINITY) continue;
+      const float f = TREE && s_m[j] == -INFINITY ? 0.f : fast_exp2((s_m[j] - Mt) * p.c2);
       const float4 v = s_o[j][d4];
       Lt += f * s_l[j];
       Ot.x += f * v.x; Ot.y += f * v.y; Ot.z += f * v.z; Ot.w += f * v.w;
@@ -1358,6 +1403,11 @@ template <bool LATE_TABLES>
 __global__ void __launch_bounds__(32 * kMergeSlices, 2) merge_kernel(const MergeParams p) {
   asm volatile("griddepcontrol.launch_dependents;");  // the next kernel may begin its launch
   merge_row<LATE_TABLES, false>(p, blockIdx.x, blockIdx.y);
+}
+
+__global__ void __launch_bounds__(32 * kMergeSlices, 2) merge_tree_kernel(const MergeParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  merge_row<false, true, true>(p, blockIdx.x, blockIdx.y);
 }
 
 // The second launch of an attention call with per-key weights: the first `merges` CTAs merge the
@@ -1387,7 +1437,7 @@ int decode_smem_bytes() { return kSmemBytes; }
 cudaError_t launch_split_merge(const void* groups, const int32_t* split_groups,
                                const float* partials, float* out, int32_t Hq, int32_t Hkv,
                                int32_t G, int32_t q_len, float c2, int32_t num_split,
-                               bool late_tables, cudaStream_t stream);
+                               bool late_tables, uint16_t* tree_out, cudaStream_t stream);
 
 cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const uint8_t* pool,
                           const int32_t* block_table, int32_t max_pages, int32_t num_pages,
@@ -1399,7 +1449,7 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
                           const uint16_t* v_new, const float* rope, int32_t rope_max_pos,
                           int32_t rot_dim, uint8_t* pool_w, uint8_t* q_codes_out,
                           uint8_t* q_scales_out, bool late_tables, uint16_t* out16, float2* stats,
-                          float* scores, float* part_l, cudaStream_t stream) {
+                          float* scores, float* part_l, const uint32_t* mask, cudaStream_t stream) {
   // the attribute belongs to each instantiation and each device: set once per device
   static bool attr_done[64] = {};
   int dev = 0;
@@ -1411,7 +1461,9 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
         (const void*)decode_kernel<8, true, false>,  (const void*)decode_kernel<6, true, false>,
         (const void*)decode_kernel<8, false, true>,  (const void*)decode_kernel<6, false, true>,
         (const void*)decode_kernel<8, false, true, true>,
-        (const void*)decode_kernel<6, false, true, true>};
+        (const void*)decode_kernel<6, false, true, true>,
+        (const void*)decode_kernel<8, false, false, false, true>,
+        (const void*)decode_kernel<6, false, false, false, true>};
     for (const void* kf : kernels)
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(kf, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
@@ -1434,6 +1486,7 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
   p.q_codes_out = q_codes_out; p.q_scales_out = q_scales_out;
   p.early_tables = late_tables ? 0 : 1;
   p.out16 = out16; p.stats = stats; p.scores = scores; p.part_l = part_l;
+  p.mask = mask;
   const bool fused = q_new != nullptr;
   if (grid <= 0) return cudaSuccess;
   // programmatic dependent launch: the kernel is set up while the previous kernel on the stream
@@ -1452,7 +1505,9 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
     // every tile has at most G * q_len real rows: with six or fewer, rows 6 and 7 are never computed
     const bool six = p.G * q_len <= 6;
     const cudaError_t le =
-        wide ? (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, false, true, true>, p)
+        mask ? (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, false, false, false, true>, p)
+                    : cudaLaunchKernelEx(&dc, decode_kernel<8, false, false, false, true>, p))
+        : wide ? (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, false, true, true>, p)
                     : cudaLaunchKernelEx(&dc, decode_kernel<8, false, true, true>, p))
         : out16 ? (six ? cudaLaunchKernelEx(&dc, decode_kernel<6, false, true>, p)
                        : cudaLaunchKernelEx(&dc, decode_kernel<8, false, true>, p))
@@ -1463,9 +1518,9 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
     if (le != cudaSuccess) return le;
   }
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || num_split <= 0 || out16 != nullptr) return e;
+  if (e != cudaSuccess || num_split <= 0 || (out16 != nullptr && mask == nullptr)) return e;
   return launch_split_merge(p.groups, split_groups, partials, out, Hq, Hkv, p.G, q_len, p.c2,
-                            num_split, late_tables, stream);
+                            num_split, late_tables, mask != nullptr ? out16 : nullptr, stream);
 }
 
 // The launch after launch_decode with out16: the merge of the split groups and the weights.
@@ -1488,18 +1543,18 @@ cudaError_t launch_merge_weights(const void* groups, const int32_t* split_groups
                               merges + (int64_t)num_seqs * Hkv * a.parts, stream);
 }
 
-// The split-K merge launch (also used by the comparator decode): one CTA per (split group, KV
+// The split-K merge launch (also used by the comparator decode; with tree_out rows go there in bf16): one CTA per (split group, KV
 // head, row of the tile), as a programmatic dependent of the attention kernel before it on the
 // stream (it waits for that grid to complete before reading the partials).
 cudaError_t launch_split_merge(const void* groups, const int32_t* split_groups,
                                const float* partials, float* out, int32_t Hq, int32_t Hkv,
                                int32_t G, int32_t q_len, float c2, int32_t num_split,
-                               bool late_tables, cudaStream_t stream) {
+                               bool late_tables, uint16_t* tree_out, cudaStream_t stream) {
   if (num_split <= 0) return cudaSuccess;
   MergeParams mp;
   mp.groups = static_cast<const int4*>(groups); mp.split = split_groups; mp.partials = partials;
   mp.out = out; mp.Hq = Hq; mp.Hkv = Hkv; mp.G = G; mp.q_len = q_len; mp.c2 = c2;
-  mp.out16 = nullptr;
+  mp.out16 = tree_out;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)num_split, (unsigned)(Hkv * kRows));
   cfg.blockDim = dim3(32 * kMergeSlices);
@@ -1510,8 +1565,9 @@ cudaError_t launch_split_merge(const void* groups, const int32_t* split_groups,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return late_tables ? cudaLaunchKernelEx(&cfg, merge_kernel<true>, mp)
-                     : cudaLaunchKernelEx(&cfg, merge_kernel<false>, mp);
+  return tree_out      ? cudaLaunchKernelEx(&cfg, merge_tree_kernel, mp)
+         : late_tables ? cudaLaunchKernelEx(&cfg, merge_kernel<true>, mp)
+                       : cudaLaunchKernelEx(&cfg, merge_kernel<false>, mp);
 }
 
 }  // namespace kvnvfp4

@@ -39,6 +39,12 @@ __device__ __forceinline__ float e4m3_decode_pos(uint32_t c) {
   return __uint_as_float(((e + 120u) << 23) | (m << 20));  // 2^(e-7) * (1 + m/8)
 }
 
+// Whether one of four E4M3 codes is a NaN (0x7F or 0xFF: without the signs the only bytes that a step of
+// one carries into bit 7).
+__device__ __forceinline__ bool e4m3x4_any_nan(uint32_t w) {
+  return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;
+}
+
 // Two f32 -> two E2M1 codes with the sm_100-family converter: round to nearest, ties to the even
 // code, saturating at 6, sign kept (a negative value that rounds to zero gives the negative-zero
 // code 8). a goes to bits 4..7, b to bits 0..3.

@@ -1,0 +1,464 @@
+// Page accounts of sequences that share a pool: which pages each one holds, how many hold each page,
+// and the stack of free pages (kv_nvfp4_pages_init, _fork, _resize), and the copy of pages that a
+// resize asks for (kv_nvfp4_copy_pages). No counterpart in the pages.
+//
+// Everything is decided in one order, sequence by sequence and place by place, so that equal calls
+// give equal tables: counts go up and down by integer atomics, whose order does not show, and what is
+// taken from the stack or pushed onto it is ranked by prefix sums.
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "nvfp4_device.cuh"
+
+namespace kvnvfp4 {
+
+namespace {
+
+// The workspace: per page, the call (high word) and the place in its order (low word) of the last
+// drop; per page, the last call that found it shared; per page, a page freed by the call; the calls
+// so far.
+struct PagesWork {
+  unsigned long long* last_drop;
+  uint32_t* shared_in;
+  int32_t* freed;
+  uint32_t* calls;
+};
+
+__host__ __device__ inline PagesWork pages_work(void* workspace, int64_t num_pages) {
+  PagesWork w;
+  w.last_drop = static_cast<unsigned long long*>(workspace);
+  w.shared_in = reinterpret_cast<uint32_t*>(w.last_drop + num_pages);
+  w.freed = reinterpret_cast<int32_t*>(w.shared_in + num_pages);
+  w.calls = reinterpret_cast<uint32_t*>(w.freed + num_pages);
+  return w;
+}
+
+__global__ void __launch_bounds__(256) pages_init_kernel(const kv_nvfp4_pages p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+  const PagesWork w = pages_work(p.workspace, p.num_pages);
+  for (int64_t i = first; i < p.num_pages; i += step) {
+    p.refs[i] = 0;
+    p.free_list[i] = (int32_t)(p.num_pages - 1 - i);  // page 0 is taken first
+    w.last_drop[i] = 0;
+    w.shared_in[i] = 0;
+  }
+  for (int64_t i = first; i < (int64_t)p.num_seqs * p.max_pages; i += step) p.block_table[i] = -1;
+  for (int64_t i = first; i < p.num_seqs; i += step) p.held[i] = 0;
+  if (first == 0) {
+    *p.free_count = p.num_pages;
+    *w.calls = 0;
+  }
+}
+
+struct ForkParams {
+  kv_nvfp4_pages p;
+  const int32_t* src;   // [n]
+  const int32_t* dst;   // [n]
+  const int32_t* lens;  // [n]
+  int32_t n;
+  int32_t* status;
+};
+
+constexpr int kForkThreads = 512;
+
+// One CTA per fork: the row's entries copied, the pages' counts raised. A fork reads only what no fork
+// of the call writes: its own target's count of pages, and its source's, which must not be a target.
+__global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const ForkParams f) {
+  const kv_nvfp4_pages& p = f.p;
+  const int tid = threadIdx.x, i = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int32_t src = f.src[i], dst = f.dst[i], len = f.lens[i];
+  bool bad = src < 0 || src >= p.num_seqs || dst < 0 || dst >= p.num_seqs;
+  for (int j = tid; j < f.n; j += kForkThreads) {
+    const int32_t other = f.dst[j];
+    bad = bad || other == src || (j < i && other == dst);
+  }
+  const bool inside = src >= 0 && src < p.num_seqs && dst >= 0 && dst < p.num_seqs;
+  const int32_t have = inside ? p.held[dst] : 0, room = inside ? p.held[src] : 0;
+  // (the barrier also stands between the reads of held[dst] and its write)
+  if (__syncthreads_or(bad || have != 0)) {
+    if (tid == 0) flag_status(f.status, KV_NVFP4_DEV_BAD_SEQ);
+    return;
+  }
+  const int32_t pages = len < 0 ? -1 : (int32_t)(((int64_t)len + kPage - 1) / kPage);
+  if (pages < 0 || pages > room || pages > p.max_pages) {
+    if (tid == 0) flag_status(f.status, KV_NVFP4_DEV_BAD_POS);
+    return;
+  }
+  const int32_t* from = p.block_table + (int64_t)src * p.max_pages;
+  int32_t* to = p.block_table + (int64_t)dst * p.max_pages;
+  bool lost = false;
+  for (int j = tid; j < pages; j += kForkThreads) {
+    const int32_t page = from[j];
+    to[j] = page;
+    if (page >= 0 && page < p.num_pages) atomicAdd(p.refs + page, 1);
+    else lost = true;
+  }
+  if (lost) flag_status(f.status, KV_NVFP4_DEV_BAD_PAGE);
+  if (tid == 0) p.held[dst] = pages;
+}
+
+struct ResizeParams {
+  kv_nvfp4_pages p;
+  const int32_t* keep;   // [num_seqs]
+  const int32_t* room;   // [num_seqs]
+  int32_t* copies;       // [num_seqs][2]
+  int32_t* status;
+};
+
+constexpr int kResizeThreads = 1024;
+constexpr int kResizeMaxCluster = 8;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of the cluster meets; what was written before is read after it.
+__device__ __forceinline__ void cluster_meet() {
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_load(const void* shared, uint32_t rank) {
+  uint32_t remote, v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(shared)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+  return v;
+}
+
+// Exclusive sum over the block's threads, and the block's sum; v < 2^31 in all.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sums, uint32_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // the sums of a scan before have been read
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  const uint32_t mine = warp_sums[lane];  // 32 warps
+  const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0u);
+  total = __reduce_add_sync(0xffffffffu, mine);
+  return before + x - v;
+}
+
+// One cluster. The entries that a call can touch (places keep / 64 .. max(held, need) of every sequence)
+// lie end to end in the order of sequences and places; a CTA takes a contiguous share of them, and
+// every CTA knows every sequence's numbers (it works them out itself). An entry is
+//   dropped  behind the new need, or shared (more than one holder before the call) although it is to be
+//            written,
+//   taken    behind what the sequence held, or in the place of a shared one.
+// Steps, with a meeting of the cluster after each: shared entries found and the sequences' demands
+// summed up, so that it is known who gets pages; counts lowered, each page's last drop noted; freed
+// (dropped last, nobody left) and taken entries counted; the freed pages listed and the fresh ones
+// entered by rank; the list pushed onto the stack.
+__global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(const ResizeParams r) {
+  extern __shared__ int32_t per_seq[];  // [num_seqs + 1] entries before, [num_seqs] need, held, demand
+  __shared__ uint32_t warp_sums[32];
+  __shared__ uint32_t out_counts[2];    // freed and taken entries of this CTA's share
+  __shared__ uint32_t all_taken;
+  const kv_nvfp4_pages& p = r.p;
+  const int tid = threadIdx.x, S = p.num_seqs;
+  const uint32_t C = cluster_size(), rank = cluster_rank();
+  int32_t* const before = per_seq;
+  int32_t* const need_of = before + S + 1;
+  int32_t* const held_of = need_of + S;
+  int32_t* const demand = held_of + S;  // then 1: gets its pages, 0: stays as it was
+  const PagesWork w = pages_work(p.workspace, p.num_pages);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const uint32_t call = __ldcg(w.calls) + 1;
+  const int32_t stack = __ldcg(p.free_count);
+  const int32_t free_now = stack < 0 ? 0 : stack > p.num_pages ? p.num_pages : stack;
+  if (tid == 0) all_taken = 0;
+  int32_t bad = stack != free_now ? KV_NVFP4_DEV_BAD_PAGE : 0;
+
+  // the sequences' numbers; one that is refused has no entries
+  uint32_t entries = 0;
+  for (int s0 = 0; s0 < S; s0 += kResizeThreads) {
+    const int s = s0 + tid;
+    uint32_t n = 0;
+    if (s < S) {
+      const int32_t keep = r.keep[s], room = r.room[s], held = p.held[s];
+      const int32_t need = (int32_t)(((int64_t)room + kPage - 1) / kPage);
+      const bool ok = keep >= 0 && room >= keep && need <= p.max_pages && held >= 0 &&
+                      held <= p.max_pages && ((int64_t)keep + kPage - 1) / kPage <= held;
+      if (!ok) bad |= KV_NVFP4_DEV_BAD_POS;
+      const int32_t full = ok ? keep / kPage : 0;
+      n = ok ? (uint32_t)(max(held, need) - full) : 0u;
+      need_of[s] = ok ? need : 0;
+      held_of[s] = ok ? held : 0;
+      demand[s] = ok ? max(0, need - held) : 0;
+      if (rank == 0) r.copies[2 * s] = r.copies[2 * s + 1] = -1;
+    }
+    uint32_t sum;
+    const uint32_t at = block_scan(n, warp_sums, sum);
+    if (s < S) before[s] = (int32_t)(entries + at);
+    entries += sum;
+  }
+  if (tid == 0) before[S] = (int32_t)entries;
+  __syncthreads();
+  // the sequence and place of entry e
+  auto seq_of = [&](uint32_t e) {
+    int lo = 0, hi = S;  // before[lo] <= e < before[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((uint32_t)before[mid] <= e) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  };
+  auto place_of = [&](int s, uint32_t e) {
+    const int last = max(held_of[s], need_of[s]);
+    return last - (before[s + 1] - (int32_t)e);
+  };
+  auto inside = [&](int32_t page) { return page >= 0 && page < p.num_pages; };
+
+  // shared entries, found by every CTA for itself (mostly one per sequence is looked at)
+  for (uint32_t e = tid; e < entries; e += kResizeThreads) {
+    const int s = seq_of(e), j = place_of(s, e);
+    if (j >= min(held_of[s], need_of[s])) continue;
+    const int32_t page = p.block_table[(int64_t)s * p.max_pages + j];
+    if (!inside(page)) {
+      bad |= KV_NVFP4_DEV_BAD_PAGE;
+    } else if (__ldcg(p.refs + page) > 1) {
+      w.shared_in[page] = call;
+      atomicAdd(&demand[s], 1);
+    }
+  }
+  __syncthreads();
+  // who gets pages: the sequences up to the first whose demand, with those before it, is not met
+  uint32_t wanted = 0;
+  for (int s0 = 0; s0 < S; s0 += kResizeThreads) {
+    const int s = s0 + tid;
+    const uint32_t d = s < S ? (uint32_t)demand[s] : 0u;
+    uint32_t sum;
+    const uint32_t upto = wanted + block_scan(d, warp_sums, sum) + d;
+    const bool ok = d == 0 || upto <= (uint32_t)free_now;
+    if (s < S) {
+      if (!ok) bad |= KV_NVFP4_DEV_NO_PAGE;
+      if (ok && d > 0) atomicMax(&all_taken, upto);
+      demand[s] = ok;
+    }
+    wanted += sum;
+  }
+  cluster_meet();
+
+  // this CTA's share
+  uint32_t share = (entries + C - 1) / C;
+  share = max(share, (uint32_t)kResizeThreads);
+  const uint32_t e_lo = min(entries, rank * share), e_hi = min(entries, e_lo + share);
+  struct Entry {
+    int s, j;
+    int32_t page;
+    bool drop, take;
+  };
+  auto entry = [&](uint32_t e) {
+    Entry x;
+    x.s = seq_of(e);
+    x.j = place_of(x.s, e);
+    const int held = held_of[x.s], need = need_of[x.s];
+    x.page = -1;
+    x.drop = x.take = false;
+    if (demand[x.s] == 0) return x;
+    if (x.j >= held) {
+      x.take = true;
+    } else {
+      x.page = p.block_table[(int64_t)x.s * p.max_pages + x.j];
+      if (x.j >= need) x.drop = true;
+      else if (inside(x.page) && __ldcg(w.shared_in + x.page) == call) x.drop = x.take = true;
+    }
+    return x;
+  };
+  auto mark_of = [&](uint32_t e) { return ((unsigned long long)call << 32) | (e + 1); };
+  for (uint32_t e = e_lo + tid; e < e_hi; e += kResizeThreads) {
+    const Entry x = entry(e);
+    if (!x.drop) continue;
+    if (inside(x.page)) {
+      atomicSub(p.refs + x.page, 1);
+      atomicMax(w.last_drop + x.page, mark_of(e));
+    } else {
+      bad |= KV_NVFP4_DEV_BAD_PAGE;
+    }
+  }
+  cluster_meet();
+
+  auto freed_by = [&](const Entry& x, uint32_t e) {
+    return x.drop && inside(x.page) && __ldcg(w.last_drop + x.page) == mark_of(e) &&
+           __ldcg(p.refs + x.page) == 0;
+  };
+  uint32_t n_freed = 0, n_taken = 0;
+  for (uint32_t e0 = e_lo; e0 < e_hi; e0 += kResizeThreads) {
+    const uint32_t e = e0 + tid;
+    bool freed = false, taken = false;
+    if (e < e_hi) {
+      const Entry x = entry(e);
+      freed = freed_by(x, e);
+      taken = x.take;
+    }
+    n_freed += __syncthreads_count(freed);
+    n_taken += __syncthreads_count(taken);
+  }
+  if (tid == 0) {
+    out_counts[0] = n_freed;
+    out_counts[1] = n_taken;
+  }
+  cluster_meet();
+  uint32_t freed_before = 0, taken_before = 0, all_freed = 0;
+  for (uint32_t c = 0; c < C; ++c) {
+    const uint32_t a = cluster_load(&out_counts[0], c), b = cluster_load(&out_counts[1], c);
+    if (c < rank) {
+      freed_before += a;
+      taken_before += b;
+    }
+    all_freed += a;
+  }
+  for (uint32_t e0 = e_lo; e0 < e_hi; e0 += kResizeThreads) {
+    const uint32_t e = e0 + tid;
+    Entry x;
+    x.drop = x.take = false;
+    bool freed = false;
+    if (e < e_hi) {
+      x = entry(e);
+      freed = freed_by(x, e);
+    }
+    uint32_t sum;
+    const uint32_t at = block_scan((freed ? 1u << 16 : 0u) + (x.take ? 1u : 0u), warp_sums, sum);
+    if (freed) w.freed[freed_before + (at >> 16)] = x.page;
+    if (x.drop || x.take) {
+      int32_t fresh = -1;
+      if (x.take) {
+        fresh = p.free_list[free_now - 1 - (int32_t)(taken_before + (at & 0xFFFFu))];
+        if (inside(fresh)) p.refs[fresh] = 1;
+        else bad |= KV_NVFP4_DEV_BAD_PAGE;
+        if (x.drop && (int64_t)x.j * kPage < r.keep[x.s]) {
+          r.copies[2 * x.s] = x.page;
+          r.copies[2 * x.s + 1] = fresh;
+        }
+      }
+      p.block_table[(int64_t)x.s * p.max_pages + x.j] = fresh;
+    }
+    freed_before += sum >> 16;
+    taken_before += sum & 0xFFFFu;
+  }
+  cluster_meet();  // the stack's top has been read, the freed pages are listed
+
+  const uint32_t left = (uint32_t)free_now - all_taken;
+  for (uint32_t i = rank * kResizeThreads + tid; i < all_freed; i += C * kResizeThreads)
+    if (left + i < (uint32_t)p.num_pages) p.free_list[left + i] = __ldcg(w.freed + i);
+  for (int s = (int)(rank * kResizeThreads) + tid; s < S; s += (int)(C * kResizeThreads))
+    if (demand[s] != 0 && (held_of[s] != need_of[s])) p.held[s] = need_of[s];
+  if (rank == 0 && tid == 0) {
+    *p.free_count = (int32_t)min(left + all_freed, (uint32_t)p.num_pages);
+    *w.calls = call;
+  }
+  if (bad != 0) flag_status(r.status, bad);
+}
+
+// One CTA per (pair, KV head's share of the page): every load before the stores.
+constexpr int kPairThreads = 192;
+constexpr int kPairWords = 9216 / 16 / kPairThreads;
+
+__global__ void __launch_bounds__(kPairThreads) copy_pages_kernel(uint8_t* pool,
+                                                                  const int32_t* pairs, int32_t n,
+                                                                  int32_t num_pages, int32_t Hkv,
+                                                                  int32_t* status) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int64_t unit = blockIdx.x; unit < (int64_t)n * Hkv; unit += gridDim.x) {
+    const int64_t i = unit / Hkv, part = unit % Hkv;
+    const int32_t src = pairs[2 * i], dst = pairs[2 * i + 1];
+    if (src == -1 && dst == -1) continue;
+    if (src < 0 || src >= num_pages || dst < 0 || dst >= num_pages) {
+      if (threadIdx.x == 0 && part == 0) flag_status(status, KV_NVFP4_DEV_BAD_PAGE);
+      continue;
+    }
+    const uint4* from =
+        reinterpret_cast<const uint4*>(pool + ((int64_t)src * Hkv + part) * 9216) + threadIdx.x;
+    uint4* to = reinterpret_cast<uint4*>(pool + ((int64_t)dst * Hkv + part) * 9216) + threadIdx.x;
+    uint4 v[kPairWords];
+#pragma unroll
+    for (int k = 0; k < kPairWords; ++k) v[k] = from[k * kPairThreads];
+#pragma unroll
+    for (int k = 0; k < kPairWords; ++k) to[k * kPairThreads] = v[k];
+  }
+}
+
+cudaError_t launch(const void* kernel, int grid, int threads, size_t shared, int cluster,
+                   void** args, cudaStream_t stream) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = shared;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+}  // namespace
+
+uint64_t pages_workspace_bytes(int32_t num_pages) { return 16ull * (uint64_t)num_pages + 16; }
+
+cudaError_t launch_pages_init(const kv_nvfp4_pages* p, int32_t num_sms, cudaStream_t stream) {
+  const int64_t most = (int64_t)p->num_seqs * p->max_pages > p->num_pages
+                           ? (int64_t)p->num_seqs * p->max_pages : p->num_pages;
+  const int64_t grid = (most + 255) / 256, full = 8ll * num_sms;
+  void* args[] = {const_cast<kv_nvfp4_pages*>(p)};
+  return launch((const void*)pages_init_kernel, (int)(grid < full ? grid : full), 256, 0, 0, args,
+                stream);
+}
+
+cudaError_t launch_pages_fork(const kv_nvfp4_pages* p, const int32_t* src, const int32_t* dst,
+                              const int32_t* lens, int32_t n, int32_t* status,
+                              cudaStream_t stream) {
+  ForkParams f{*p, src, dst, lens, n, status};
+  void* args[] = {&f};
+  return launch((const void*)pages_fork_kernel, n, kForkThreads, 0, 0, args, stream);
+}
+
+cudaError_t launch_pages_resize(const kv_nvfp4_pages* p, const int32_t* keep, const int32_t* room,
+                                int32_t* copies, int32_t* status, cudaStream_t stream) {
+  static bool attr_done[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
+  if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(pages_resize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (4 * KV_NVFP4_MAX_ACCOUNTED_SEQS + 1) * 4);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_done[dev] = true;
+  }
+  ResizeParams r{*p, keep, room, copies, status};
+  void* args[] = {&r};
+  // the lengths are on the device: sized for the most entries that the table has
+  int C = 1;
+  while (C < kResizeMaxCluster && (int64_t)C * kResizeThreads < (int64_t)p->num_seqs * p->max_pages)
+    C *= 2;
+  return launch((const void*)pages_resize_kernel, C, kResizeThreads,
+                (size_t)(4 * p->num_seqs + 1) * 4, C, args, stream);
+}
+
+cudaError_t launch_copy_pages(uint8_t* pool, const int32_t* pairs, int32_t n, int32_t num_pages,
+                              int32_t Hkv, int32_t num_sms, int32_t* status, cudaStream_t stream) {
+  void* args[] = {&pool, &pairs, &n, &num_pages, &Hkv, &status};
+  const int64_t units = (int64_t)n * Hkv, full = 8ll * num_sms;
+  return launch((const void*)copy_pages_kernel, (int)(units < full ? units : full), kPairThreads, 0,
+                0, args, stream);
+}
+
+}  // namespace kvnvfp4

@@ -146,6 +146,8 @@ struct TileParams {
   uint16_t* out16;         // [num_seqs * q_len][Hq][128]
   float2* stats;           // [num_seqs][Hkv][G * q_len]
   float* part_l;           // [num_partials][128]
+  // trees: which nodes a node sees, bit j % 32 of word j / 32; bf16 rows to out16
+  const uint32_t* mask;    // [num_seqs][q_len][ceil(q_len / 32)]
 };
 
 struct TSeg {
@@ -366,7 +368,10 @@ __device__ void t_mma_pv(const TileParams& p, uint8_t* smem, uint32_t tbase, int
 // chunk of zeros, written once at the start); zeros for a key past the sequence end or on a
 // skipped page. The 16-byte loads of a row are rotated by key so that the eight keys of a
 // quarter-warp read distinct banks.
+// kTree: also zeros for a node's key whose V row holds a NaN; the softmax warps make NaN of the rows
+// that see it, and the others take nothing from it.
 // --------------------------------------------------------------------------------------------
+template <bool kTree>
 __device__ void t_dequant(const TileParams& p, uint8_t* smem, int warp, int lane) {
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + kTOffBars;
@@ -395,13 +400,16 @@ __device__ void t_dequant(const TileParams& p, uint8_t* smem, int warp, int lane
       // V tile v is free once the P.V of block kb - 2 is complete
       if (kb >= 2) wait_bar_sleep(tbar(bars, kTbPvDone + v), ((kb - 2) >> 1) & 1, to);
       const int page = sg.lo + 2 * j + pg;
-      const bool ok = page < sg.hi && stage_pid[2 * st + pg] >= 0 && page * kPage + slot < sg.len;
+      bool ok = page < sg.hi && stage_pid[2 * st + pg] >= 0 && page * kPage + slot < sg.len;
       const uint32_t stage = sbase + kTOffStage + st * kTStageBytes;
       uint4 cw[4];
 #pragma unroll
       for (int qq = 0; qq < 4; ++qq)
         cw[qq] = lds128(stage + kStV + pg * 4096 + slot * 64 + 16 * ((qq + rot) & 3));
       const uint2 sc8 = lds64(stage + kStVs + pg * 512 + slot * 8);
+      if (kTree && page * kPage + slot >= sg.len - p.q_len &&
+          (e4m3x4_any_nan(sc8.x) || e4m3x4_any_nan(sc8.y)))
+        ok = false;
       const uint32_t dst =
           sbase + kTOffVt + v * kVtBytes + (key >> 3) * kVtGroupBytes + (key & 7) * 16;
 #pragma unroll
@@ -505,12 +513,52 @@ __device__ __forceinline__ void t_scale_o32(uint32_t taddr, float alpha) {
   tmem_st32(taddr, o);
 }
 
-//
+// kTree: which of the keys of this warp's share of a block with nodes this row sees, and which of them
+// hold a NaN in V. first: the node at the share's first key (negative: a key before the nodes, which
+// every row sees). A padding row sees all of them, a skipped page's keys nobody.
+template <int kNc>
+__device__ __forceinline__ void t_tree_window(const TileParams& p, const TSeg& sg, int first, int gr,
+                                              bool row_ok, bool valid, int32_t pid, int page,
+                                              int kofs, int lane, uint32_t (&sees)[kNc / 32],
+                                              uint32_t (&v_nan)[kNc / 32]) {
+  const int W = (p.q_len + 31) >> 5;
+  const uint32_t* row =
+      p.mask + ((int64_t)sg.seq * p.q_len + (row_ok ? gr / p.G : 0)) * W;
+  auto word = [&](int k) {  // nodes 32 k .. 32 k + 31; bits from q_len on count for nothing
+    if (k < 0) return 0xFFFFFFFFu;  // keys before the nodes
+    if (k >= W) return 0u;
+    const int left = p.q_len - 32 * k;
+    return __ldg(row + k) & (left < 32 ? (1u << left) - 1u : 0xFFFFFFFFu);
+  };
+  uint32_t lo = word(first >> 5);
+#pragma unroll
+  for (int i = 0; i < kNc / 32; ++i) {
+    const uint32_t hi = word((first >> 5) + i + 1);
+    const uint32_t bits = __funnelshift_r(lo, hi, (uint32_t)first & 31u);
+    sees[i] = !row_ok ? 0xFFFFFFFFu : valid ? bits : 0u;
+    lo = hi;
+    const int node = first + 32 * i + lane;
+    bool nan = false;
+    if (valid && node >= 0 && node < p.q_len) {
+      const uint2 sc = __ldg(reinterpret_cast<const uint2*>(
+          p.pool + (int64_t)pid * p.Hkv * 9216 + (int64_t)p.Hkv * 8704 + sg.head * 512 +
+          (kofs + 32 * i + lane) * kScaleBytes));
+      nan = e4m3x4_any_nan(sc.x) || e4m3x4_any_nan(sc.y);
+    }
+    v_nan[i] = __ballot_sync(0xffffffffu, nan);
+  }
+}
+
 // kAcc (attention with per-key weights): each thread also sums its P in fp32 before they are rounded
 // to f16. The output keeps the tensor core's sum of the rounded P (numerator and denominator then
 // round alike), but a key's weight is computed from its unrounded P, and against the rounded sum
 // every weight of a row would be off by up to 2^-12.
-template <bool kDup, bool kAcc>
+//
+// kTree (kv_nvfp4_tree_attn): a row sees every key before the step's q_len nodes, and of the nodes
+// those in its mask, a word of which covers 32 keys; a window of keys takes two neighbouring words and a
+// shift. Only the last blocks of a group hold nodes: the words and the V scales (for NaN) of the warp's
+// keys there are read from global memory while the scores are awaited.
+template <bool kDup, bool kAcc, bool kTree>
 __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, int warp,
                           int lane) {
   constexpr int kNc = kDup ? 32 : 64;  // keys of each block that one warp takes
@@ -545,8 +593,11 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
     // a quadrant whose 32 rows are all padding computes nothing (its two warps still take part
     // in every mbarrier); its rows of P and O are never read into a result
     const bool warp_live = sg.rg * kTRows + (rr & ~31) < rows_total;
-    // largest visible key position of this row (-1: no key)
-    const int limit = row_ok ? (p.causal ? sg.len - p.q_len + gr / p.G : sg.len - 1) : -1;
+    // largest key position up to which this row sees every key (-1: no key)
+    const int limit = !row_ok    ? -1
+                      : kTree    ? sg.len - p.q_len - 1
+                      : p.causal ? sg.len - p.q_len + gr / p.G
+                                 : sg.len - 1;
     float m = -INFINITY;
     float ls = 0.f;  // kAcc: this thread's sum of the row's P
     // this warp's page of each block is skipped (its keys masked) when its id lies outside the
@@ -560,6 +611,12 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
       const int32_t pid = pid_next;
       const bool valid = page < sg.hi && pid >= 0 && pid < p.num_pages;
       if (page + 2 < sg.hi) pid_next = __ldg(bt + page + 2);
+      // kTree: bit c of these words: this row sees key c of this warp's share; that key's V has a NaN
+      uint32_t sees[kNc / 32], v_nan[kNc / 32];
+      const bool nodes = kTree && (page + 1) * kPage > sg.len - p.q_len;
+      if (nodes && warp_live)
+        t_tree_window<kNc>(p, sg, page * kPage + kofs - (sg.len - p.q_len), gr, row_ok, valid, pid,
+                           page, kofs, lane, sees, v_nan);
       wait_bar_sleep(tbar(bars, kTbSFull + b), (kb >> 1) & 1, to);
       tc_fence_after();
       __syncwarp();
@@ -576,7 +633,13 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
 #pragma unroll
         for (int c = 0; c < kNc; c += 32)
           tmem_wait_ld_regs32(*reinterpret_cast<uint32_t(*)[32]>(&sv[c]));
-        if (__any_sync(0xffffffffu, nv != kNc)) {
+        if (kTree && nodes) {
+#pragma unroll
+          for (int c = 0; c < kNc; ++c) {
+            const uint32_t x = (v_nan[c >> 5] >> (c & 31)) & 1u ? 0x7FC00000u : sv[c];
+            sv[c] = (sees[c >> 5] >> (c & 31)) & 1u ? x : __float_as_uint(-INFINITY);
+          }
+        } else if (__any_sync(0xffffffffu, nv != kNc)) {
 #pragma unroll
           for (int c = 0; c < kNc; ++c) sv[c] = c < nv ? sv[c] : __float_as_uint(-INFINITY);
         }
@@ -748,7 +811,7 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
                 dst[e >> 2] = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
-            } else if (kAcc) {
+            } else if (kAcc || kTree) {
               uint16_t* dst = p.out16 + (((int64_t)sg.seq * p.q_len + tok) * p.Hq + qh) * 128 + 32 * cc;
               store_bf16x16(dst, reinterpret_cast<const float(&)[16]>(ov[0]), inv);
               store_bf16x16(dst + 16, reinterpret_cast<const float(&)[16]>(ov[16]), inv);
@@ -780,7 +843,7 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
   if (to && lane == 0) flag_status(p.status, KV_NVFP4_DEV_TIMEOUT);
 }
 
-template <bool kAcc>
+template <bool kAcc, bool kTree = false>
 __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const TileParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -819,10 +882,10 @@ __global__ void __launch_bounds__(kTThreads, 1) tile_kernel(const TileParams p) 
   } else if (warp == kTWarpMma) {
     t_mma_qk(p, smem, tbase, lane);
   } else if (warp >= kTWarpSoft0 && warp < kTWarpDeq0) {
-    if (p.G * p.q_len <= kTRows / 2) t_softmax<true, kAcc>(p, smem, tbase, warp, lane);
-    else t_softmax<false, kAcc>(p, smem, tbase, warp, lane);
+    if (p.G * p.q_len <= kTRows / 2) t_softmax<true, kAcc, kTree>(p, smem, tbase, warp, lane);
+    else t_softmax<false, kAcc, kTree>(p, smem, tbase, warp, lane);
   } else if (warp < kTWarpPv) {
-    t_dequant(p, smem, warp, lane);
+    t_dequant<kTree>(p, smem, warp, lane);
   } else {
     t_mma_pv(p, smem, tbase, lane);
   }
@@ -865,7 +928,9 @@ struct TMergeParams {
 constexpr int kTMergeSlices = 8;
 constexpr int kTMergePerRound = 8;  // partials a slice requests at once (64 per CTA and round)
 
-template <bool kAcc, int kSlices>
+// kTree: bf16 rows without statistics; a partial without a maximum may hold NaN (a row whose keys'
+// scores are all NaN) and is added rather than skipped; without a visible key it holds zeros.
+template <bool kAcc, int kSlices, bool kTree = false>
 __device__ __forceinline__ void tile_merge_row(const TMergeParams& p, int split_index, int i) {
   __shared__ float s_m[kSlices], s_l[kSlices], s_w[kSlices];
   __shared__ float4 s_o[kSlices][32];
@@ -903,15 +968,16 @@ __device__ __forceinline__ void tile_merge_row(const TMergeParams& p, int split_
     float mn = M;
 #pragma unroll
     for (int u = 0; u < kTMergePerRound; ++u) mn = fmaxf(mn, mq[u]);
-    if (mn == -INFINITY) continue;  // no visible key for this row in any partial so far
-    const float a = fast_exp2((M - mn) * p.c2);  // 0 while M is -inf
+    if (!kTree && mn == -INFINITY) continue;  // no visible key for this row in any partial so far
+    // 0 while M is -inf
+    const float a = kTree && M == -INFINITY ? 0.f : fast_exp2((M - mn) * p.c2);
     L *= a;
     if (kAcc) W *= a;
     O.x *= a; O.y *= a; O.z *= a; O.w *= a;
 #pragma unroll
     for (int u = 0; u < kTMergePerRound; ++u) {
-      if (mq[u] == -INFINITY) continue;  // a segment with no visible key for this row
-      const float f = fast_exp2((mq[u] - mn) * p.c2);
+      if (!kTree && mq[u] == -INFINITY) continue;  // a segment with no visible key for this row
+      const float f = kTree && mq[u] == -INFINITY ? 0.f : fast_exp2((mq[u] - mn) * p.c2);
       L += f * lq[u];
       if (kAcc) W += f * wq[u];
       O.x += f * ov[u].x; O.y += f * ov[u].y; O.z += f * ov[u].z; O.w += f * ov[u].w;
@@ -932,21 +998,21 @@ __device__ __forceinline__ void tile_merge_row(const TMergeParams& p, int split_
     Ot = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < kSlices; ++j) {
-      if (s_m[j] == -INFINITY) continue;
-      const float f = fast_exp2((s_m[j] - Mt) * p.c2);
+      if (!kTree && s_m[j] == -INFINITY) continue;
+      const float f = kTree && s_m[j] == -INFINITY ? 0.f : fast_exp2((s_m[j] - Mt) * p.c2);
       const float4 v = s_o[j][d4];
       Lt += f * s_l[j];
       if (kAcc) Wt += f * s_w[j];
       Ot.x += f * v.x; Ot.y += f * v.y; Ot.z += f * v.z; Ot.w += f * v.w;
     }
   }
-  if (kAcc) {
+  if (kAcc || kTree) {
     const int tok = r / p.G, qh = head * p.G + r % p.G;
     const float inv = Lt > 0.f ? 1.f / Lt : 0.f;
     *reinterpret_cast<uint2*>(
         p.out16 + (((int64_t)g0.x * p.q_len + tok) * p.Hq + qh) * 128 + 4 * d4) =
         make_uint2(pack_bf16x2(Ot.x * inv, Ot.y * inv), pack_bf16x2(Ot.z * inv, Ot.w * inv));
-    if (d4 == 0)
+    if (kAcc && d4 == 0)
       p.stats[((int64_t)g0.x * p.Hkv + head) * (p.G * p.q_len) + r] =
           make_float2(Mt, Wt > 0.f ? 1.f / Wt : 0.f);
   } else if (Lt > 0.f) {
@@ -958,19 +1024,20 @@ __device__ __forceinline__ void tile_merge_row(const TMergeParams& p, int split_
   }
 }
 
-template <bool kAcc>
+template <bool kAcc, bool kTree = false>
 __global__ void __launch_bounds__(32 * kTMergeSlices, 2) tile_merge_kernel(const TMergeParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
-  tile_merge_row<kAcc, kTMergeSlices>(p, blockIdx.x, blockIdx.y);
+  tile_merge_row<kAcc, kTMergeSlices, kTree>(p, blockIdx.x, blockIdx.y);
 }
 
 // The same with a warp per row and eight rows of a group per CTA. With many rows a group has few
 // partials, and a CTA for each row is mostly its start: 24 groups of 128 rows, 7 partials each, took
 // 15 us, this 3.
+template <bool kTree>
 __global__ void __launch_bounds__(32 * kTMergeSlices, 3)
     tile_merge_rows_kernel(const TMergeParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
-  tile_merge_row<true, 1>(p, blockIdx.x, blockIdx.y * kTMergeSlices + (threadIdx.x >> 5));
+  tile_merge_row<!kTree, 1, kTree>(p, blockIdx.x, blockIdx.y * kTMergeSlices + (threadIdx.x >> 5));
 }
 
 // The second launch of an attention call with per-key weights on a tile plan with at most 8 rows per
@@ -1003,13 +1070,14 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
                         const int32_t* split_groups, int32_t num_split, float* partials,
                         float* out, int32_t* status, int32_t Hq, int32_t Hkv, int32_t q_len,
                         int32_t causal, int32_t grid, float sm_scale, uint16_t* out16,
-                        float2* stats, float* part_l, cudaStream_t stream) {
+                        float2* stats, float* part_l, const uint32_t* mask, cudaStream_t stream) {
   // the attribute belongs to each device: set once per device
   static bool attr_done[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
   if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-    for (const void* kf : {(const void*)tile_kernel<false>, (const void*)tile_kernel<true>}) {
+    for (const void* kf : {(const void*)tile_kernel<false>, (const void*)tile_kernel<true>,
+                           (const void*)tile_kernel<false, true>}) {
       const cudaError_t e =
           cudaFuncSetAttribute(kf, cudaFuncAttributeMaxDynamicSharedMemorySize, kTSmemBytes);
       if (e != cudaSuccess) return e;
@@ -1026,7 +1094,7 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
   p.partials = partials; p.out = out; p.status = status;
   p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.q_len = q_len; p.causal = causal;
   p.c2 = sm_scale * 1.4426950408889634f;
-  p.out16 = out16; p.stats = stats; p.part_l = part_l;
+  p.out16 = out16; p.stats = stats; p.part_l = part_l; p.mask = mask;
   if (grid <= 0) return cudaSuccess;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1039,8 +1107,9 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t le = out16 ? cudaLaunchKernelEx(&cfg, tile_kernel<true>, p)
-                                 : cudaLaunchKernelEx(&cfg, tile_kernel<false>, p);
+    const cudaError_t le = mask    ? cudaLaunchKernelEx(&cfg, tile_kernel<false, true>, p)
+                           : out16 ? cudaLaunchKernelEx(&cfg, tile_kernel<true>, p)
+                                   : cudaLaunchKernelEx(&cfg, tile_kernel<false>, p);
     if (le != cudaSuccess) return le;
   }
   cudaError_t e = cudaGetLastError();
@@ -1066,8 +1135,10 @@ cudaError_t launch_tile(const uint8_t* q_codes, const uint8_t* q_scales, const u
   // are.)
   if (out16 && (int64_t)num_split * cfg.gridDim.y > 6 * (int64_t)grid) {
     cfg.gridDim.y = (cfg.gridDim.y + kTMergeSlices - 1) / kTMergeSlices;
-    return cudaLaunchKernelEx(&cfg, tile_merge_rows_kernel, mp);
+    return mask ? cudaLaunchKernelEx(&cfg, tile_merge_rows_kernel<true>, mp)
+                : cudaLaunchKernelEx(&cfg, tile_merge_rows_kernel<false>, mp);
   }
+  if (mask) return cudaLaunchKernelEx(&cfg, tile_merge_kernel<false, true>, mp);
   return out16 ? cudaLaunchKernelEx(&cfg, tile_merge_kernel<true>, mp)
                : cudaLaunchKernelEx(&cfg, tile_merge_kernel<false>, mp);
 }

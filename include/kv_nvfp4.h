@@ -69,6 +69,7 @@ typedef int32_t kv_nvfp4_status;
 #define KV_NVFP4_DEV_BAD_SEQ 0x4      /* sequence id outside [0, num_seqs) */
 #define KV_NVFP4_DEV_BAD_ROPE 0x8     /* position >= rope_max_pos for a rotated row */
 #define KV_NVFP4_DEV_TIMEOUT 0x10     /* an internal barrier wait hit its time limit */
+#define KV_NVFP4_DEV_NO_PAGE 0x20     /* fewer free pages than a sequence asked for */
 
 /* Model geometry of one attention layer. The library supports head_dim = 128 and
  * page_size = 64; num_q_heads (at most 4096) must be a multiple of num_kv_heads; rot_dim is a
@@ -344,6 +345,163 @@ kv_nvfp4_status kv_nvfp4_evict_compact(const kv_nvfp4_layout *layout, const int3
                                        const int32_t *d_dst_block_table, int32_t dst_max_pages,
                                        float *weights, int64_t weights_stride, int32_t *d_status,
                                        void *stream);
+
+/* ---- Speculative decoding with a tree of drafted tokens ---------------------------------------------
+ * No counterpart in the pages, which verify a chain of drafts (kv_nvfp4_decode_attn with q_len > 1).
+ * The n tokens that a step drafts for a sequence are the nodes of a tree, at most KV_NVFP4_MAX_TREE of
+ * them: node i hangs on node parents[i] < i, or with -1 on the cache (on the last token in it). A node
+ * with any other parent, or below such a one, is padding, for trees with fewer nodes than the call has
+ * room for. With `len` tokens in a sequence's cache before the step, node i takes cache slot len + i
+ * and the position behind its parent's. A step is
+ *   kv_nvfp4_tree_mask      parents -> masks, and the slots and positions for
+ *   kv_nvfp4_append_slots   K, V and Q of all nodes
+ *   kv_nvfp4_plan           lengths len + n, q_len = n, causal = 0
+ *   kv_nvfp4_tree_attn      every node sees the cache and its ancestors
+ *   kv_nvfp4_tree_accept    the path that the model agrees with; its rows move behind the cache
+ *
+ * Mask: bit j % 32 of word j / 32 of mask[s][i] says that node i of sequence s sees node j (itself is
+ * node i). A padding node sees none; it has slot len + i and position first_pos.
+ *   d_parents:    DEVICE int32 [num_seqs][n]
+ *   d_lens:       DEVICE int32 [num_seqs], slots before the tree
+ *   d_first_pos:  DEVICE int32 [num_seqs], position of a node that hangs on the cache, or null: d_lens
+ *                 (they differ behind an eviction)
+ *   d_mask:       DEVICE uint32 [num_seqs][n][ceil(n / 32)]
+ *   d_seq_ids, d_slots, d_positions: DEVICE int32 [num_seqs * n], as kv_nvfp4_append_slots takes them;
+ *                 or all three null
+ * A sequence whose length or position is negative, or passes 31 bits at its last node, sets
+ * KV_NVFP4_DEV_BAD_POS and is skipped. One kernel launch. num_seqs = 0 does nothing. */
+#define KV_NVFP4_MAX_TREE 256
+kv_nvfp4_status kv_nvfp4_tree_mask(const int32_t *d_parents, int32_t num_seqs, int32_t n,
+                                   const int32_t *d_lens, const int32_t *d_first_pos,
+                                   uint32_t *d_mask, int32_t *d_seq_ids, int32_t *d_slots,
+                                   int32_t *d_positions, int32_t *d_status, void *stream);
+
+/* Attention of a tree's nodes: kv_nvfp4_decode_attn where node i of sequence s sees the keys of slots
+ * t < seq_len - q_len and, of the q_len last slots, those whose bit in mask[s][i] is set (slot
+ * seq_len - q_len + j is node j; bits from q_len on count for nothing). Any mask will do, not only a
+ * tree's.
+ *   plan, d_workspace: from kv_nvfp4_plan with causal = 0 and q_len <= KV_NVFP4_MAX_TREE (same stream)
+ *   q_codes, q_scales, sm_scale, pool, num_pages, d_block_table, max_pages: as for kv_nvfp4_decode_attn
+ *   d_mask:    DEVICE uint32 [num_seqs][q_len][ceil(q_len / 32)]
+ *   out:       DEVICE bf16 [num_seqs * q_len][num_q_heads][128], 16-byte aligned: the fp32 result
+ *              rounded once. A row that sees no key (no cached token and an empty mask, or bad pages
+ *              only) gets zeros.
+ * What a row does not see does not reach it, NaN in a hidden node's K or V included. A node whose stored
+ * K or V holds a NaN makes NaN of the whole output row of those that see it. Two kernel launches, as for
+ * kv_nvfp4_decode_attn. EINVAL for a plan that is not this layout's or is causal, a null or misaligned
+ * buffer, a plan longer than max_pages * 64. */
+kv_nvfp4_status kv_nvfp4_tree_attn(const kv_nvfp4_layout *layout, const kv_nvfp4_plan_info *plan,
+                                   void *d_workspace, const uint8_t *q_codes,
+                                   const uint8_t *q_scales, const uint32_t *d_mask, float sm_scale,
+                                   const uint8_t *pool, int32_t num_pages,
+                                   const int32_t *d_block_table, int32_t max_pages, void *out,
+                                   int32_t *d_status, void *stream);
+
+/* The path of a tree that the model agrees with, and its rows moved behind the cache. From the cache
+ * on, the path goes to the lowest node that hangs on its last node (at first on the cache) and whose
+ * drafted token is the awaited one: first expected[s], then the target of the last node. It ends where
+ * there is none. Then the K and V rows of slots len + path[j] move to slots len + j, for every KV head,
+ * as if all were read before any is written. The sequence holds len + count tokens afterwards; the
+ * slots behind them, up to len + n, hold what is left of the tree.
+ *   d_parents:  DEVICE int32 [num_seqs][n], as for kv_nvfp4_tree_mask (a node that hangs nowhere is on
+ *               no path)
+ *   d_draft, d_target: DEVICE int32 [num_seqs][n], each node's drafted token and the token that the
+ *               model puts behind it
+ *   d_expected: DEVICE int32 [num_seqs], the token that the model puts behind the cache
+ *   d_lens:     DEVICE int32 [num_seqs], tokens in the cache before the tree
+ *   pool, num_pages, d_block_table, max_pages: the cache; a null pool (with num_pages, max_pages 0 and a
+ *               null table): nothing is moved
+ *   d_path:     DEVICE int32 [num_seqs][n], the path's nodes, ascending; entries from count on are
+ *               left as they were
+ *   d_count:    DEVICE int32 [num_seqs]
+ *   d_next:     DEVICE int32 [num_seqs], the token awaited behind the path; may be d_expected
+ *   d_new_lens: DEVICE int32 [num_seqs], len + count, or null; may be d_lens
+ * With d_parents null (and d_draft, d_target, d_expected, d_next too) d_path and d_count are given: a
+ * path that was chosen another way, or the moves of a further layer's pool. A sequence with a negative
+ * length, a tree that ends past max_pages * 64 or a given path that does not ascend within [0, n) sets
+ * KV_NVFP4_DEV_BAD_POS and is skipped, its outputs left as they were; a row whose old or new page lies
+ * outside the pool sets KV_NVFP4_DEV_BAD_PAGE and is not moved. Pages that the tree's slots lie in must
+ * not be shared between sequences (kv_nvfp4_pages_resize sees to it). One kernel launch. num_seqs = 0
+ * does nothing. */
+kv_nvfp4_status kv_nvfp4_tree_accept(const kv_nvfp4_layout *layout, const int32_t *d_parents,
+                                     const int32_t *d_draft, const int32_t *d_target,
+                                     const int32_t *d_expected, int32_t num_seqs, int32_t n,
+                                     const int32_t *d_lens, const int32_t *d_block_table,
+                                     int32_t max_pages, int32_t num_pages, uint8_t *pool,
+                                     int32_t *d_path, int32_t *d_count, int32_t *d_next,
+                                     int32_t *d_new_lens, int32_t *d_status, void *stream);
+
+/* ---- Pages of sequences that share a pool ------------------------------------------------------------
+ * No counterpart in the pages. The accounts say which pages every sequence holds and which are free;
+ * all of them are DEVICE memory of the caller's, so that a step that takes and returns pages needs no
+ * host. One set of accounts serves every layer whose pool has as many pages. Sequences may share pages
+ * (kv_nvfp4_pages_fork); kv_nvfp4_pages_resize makes room that is a sequence's own, so every call that
+ * writes into the cache has to come behind a resize whose room covers what it writes and whose `keep`
+ * covers what has to stay. */
+typedef struct kv_nvfp4_pages {
+  int32_t *block_table; /* [num_seqs][max_pages]; -1 from held[s] on */
+  int32_t *held;        /* [num_seqs] pages in the sequence's row of the table */
+  int32_t *refs;        /* [num_pages] rows that hold the page */
+  int32_t *free_list;   /* [num_pages] a stack: entries [0, *free_count) are the free pages, the last
+                           one is taken next; entries behind them have their old values */
+  int32_t *free_count;  /* [1] */
+  void *workspace;      /* kv_nvfp4_pages_workspace_bytes, 8-byte aligned; zero before the first call
+                           (kv_nvfp4_pages_init sees to it), then left to the library */
+  int32_t num_seqs;     /* at most KV_NVFP4_MAX_ACCOUNTED_SEQS */
+  int32_t max_pages;    /* num_seqs * max_pages is at most 2^31 - 1 */
+  int32_t num_pages;
+} kv_nvfp4_pages;
+#define KV_NVFP4_MAX_ACCOUNTED_SEQS 8192
+
+/* Bytes of the accounts' workspace; 0 for num_pages < 0. */
+size_t kv_nvfp4_pages_workspace_bytes(int32_t num_pages);
+
+/* No sequence holds a page, every page is free, page 0 is taken first. One kernel launch. */
+kv_nvfp4_status kv_nvfp4_pages_init(const kv_nvfp4_pages *pages, void *stream);
+
+/* Sequence dst[i] holds the first ceil(lens[i] / 64) pages of sequence src[i] as well, for i < n: its
+ * row of the table is that of src[i], the pages' counts rise. No page is copied: the resize before the
+ * next append replaces a shared page that is to be written.
+ *   d_src, d_dst, d_lens: DEVICE int32 [n]; n <= num_seqs
+ * Every target must hold no page, must not be a source of the call nor stand in d_dst before: else (or
+ * with a sequence outside [0, num_seqs)) KV_NVFP4_DEV_BAD_SEQ, and the fork is skipped. A length that
+ * the source has no pages for sets KV_NVFP4_DEV_BAD_POS and skips the fork; a page outside the pool is
+ * entered, not counted, and sets KV_NVFP4_DEV_BAD_PAGE. One kernel launch. n = 0 does nothing. */
+kv_nvfp4_status kv_nvfp4_pages_fork(const kv_nvfp4_pages *pages, const int32_t *d_src,
+                                    const int32_t *d_dst, const int32_t *d_lens, int32_t n,
+                                    int32_t *d_status, void *stream);
+
+/* Room for new_lens[s] tokens, of which the first keep_lens[s] stay, for every sequence s: it holds
+ * need = ceil(new_lens[s] / 64) pages afterwards. Growing reserves, shrinking frees, keep = new = 0
+ * ends a sequence.
+ *   Places below keep / 64 keep their pages, shared or not.
+ *   Places from keep / 64 on, up to min(held, need), keep theirs unless it is shared (held by more
+ *     than one row before the call): a fresh page then takes its place, and where the old one holds kept
+ *     tokens (the place keep / 64) copies[s] is {old page, fresh page}, for kv_nvfp4_copy_pages on every
+ *     layer's pool. Other entries of copies are {-1, -1}.
+ *   Places from need on are dropped (-1), places from held on take fresh pages.
+ * Fresh pages come from the stack as it stood before the call, in the order of sequences and places; a
+ * page whose last holder drops it goes onto the stack, in the order of the last drops. Where the
+ * stack does not suffice for a sequence's fresh pages together with those of the sequences before it,
+ * the sequence stays as it was and KV_NVFP4_DEV_NO_PAGE is set.
+ *   d_keep_lens, d_new_lens: DEVICE int32 [num_seqs]
+ *   d_copies:  DEVICE int32 [num_seqs][2]
+ * A sequence with keep < 0, new < keep, need > max_pages, or keep beyond the pages that it holds sets
+ * KV_NVFP4_DEV_BAD_POS and stays as it was. A page outside the pool in the table is kept or dropped
+ * uncounted and sets KV_NVFP4_DEV_BAD_PAGE. One kernel launch of one cluster; calls on the same accounts
+ * must not overlap. */
+kv_nvfp4_status kv_nvfp4_pages_resize(const kv_nvfp4_pages *pages, const int32_t *d_keep_lens,
+                                      const int32_t *d_new_lens, int32_t *d_copies,
+                                      int32_t *d_status, void *stream);
+
+/* Page copies within a pool: page pairs[i][1] <- page pairs[i][0] for i < n (kv_nvfp4_page_bytes
+ * each); {-1, -1} is skipped. A page that is written must stand nowhere else in the pairs.
+ *   d_pairs:   DEVICE int32 [n][2]
+ * A pair with a page outside the pool sets KV_NVFP4_DEV_BAD_PAGE and is skipped. One kernel launch.
+ * n = 0 does nothing. */
+kv_nvfp4_status kv_nvfp4_copy_pages(const kv_nvfp4_layout *layout, uint8_t *pool,
+                                    int32_t num_pages, const int32_t *d_pairs, int32_t n,
+                                    int32_t *d_status, void *stream);
 
 /* ---- Fused decode step [NVFP4: the decode path quantises the current K/V as it runs] -----------
  * One launch doing what kv_nvfp4_append (of the step's new tokens, with Q) followed by
