@@ -152,6 +152,101 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sums, 
   return before + x - v;
 }
 
+// A resize of at most one entry per thread, by one CTA: everything stays in registers, and the cluster
+// need not meet. A page that several rows drop is freed by whoever lowers its count to zero, in the
+// place of its last drop, which that thread looks up.
+struct FewEntries {
+  int32_t top[kResizeThreads];         // the stack from its top on
+  int32_t dropped[kResizeThreads];     // page dropped by each entry, or -1
+  uint32_t takes_before[kResizeThreads + 1];
+  uint8_t freed[kResizeThreads];
+  uint32_t warp_sums[32];
+  uint32_t all_taken;
+};
+
+template <class SeqOf, class PlaceOf>
+__device__ __forceinline__ void resize_few(const ResizeParams& r, FewEntries& sh,
+                                           const int32_t* before, const int32_t* need_of,
+                                           const int32_t* held_of, SeqOf seq_of, PlaceOf place_of,
+                                           uint32_t entries, int32_t free_now, int32_t bad) {
+  const kv_nvfp4_pages& p = r.p;
+  const int tid = threadIdx.x, S = p.num_seqs;
+  const uint32_t e = (uint32_t)tid;
+  const int32_t top = tid < free_now ? p.free_list[free_now - 1 - tid] : -1;
+  sh.freed[tid] = 0;
+  if (tid == 0) sh.all_taken = 0;
+  int s = 0, j = 0;
+  int32_t page = -1, refs = 0, keep = 0;
+  bool take = false, drop = false, in_pool = false;
+  if (e < entries) {
+    s = seq_of(e);
+    j = place_of(s, e);
+    keep = r.keep[s];
+    if (j < held_of[s]) {
+      page = p.block_table[(int64_t)s * p.max_pages + j];
+      in_pool = page >= 0 && page < p.num_pages;
+      if (in_pool) refs = p.refs[page];
+      else bad |= KV_NVFP4_DEV_BAD_PAGE;
+      drop = j >= need_of[s] || (in_pool && refs > 1);
+      take = drop && j < need_of[s];
+    } else {
+      take = true;
+    }
+  }
+  uint32_t wanted;
+  const uint32_t at = block_scan(take ? 1u : 0u, sh.warp_sums, wanted);
+  sh.takes_before[tid] = at;
+  sh.top[tid] = top;
+  if (tid == 0) sh.takes_before[entries] = wanted;
+  __syncthreads();
+  // a sequence's demand with those before it
+  auto met = [&](int seq, uint32_t& upto) {
+    upto = sh.takes_before[before[seq + 1]];
+    return upto == sh.takes_before[before[seq]] || upto <= (uint32_t)free_now;
+  };
+  uint32_t upto = 0;
+  if (e < entries) {
+    const bool ok = met(s, upto);
+    if (ok && take) atomicMax(&sh.all_taken, upto);
+    if (!ok) bad |= KV_NVFP4_DEV_NO_PAGE;
+    take = take && ok;
+    drop = drop && ok;
+  }
+  const bool lowers = drop && in_pool;
+  const int32_t was = lowers ? atomicSub(p.refs + page, 1) : 0;  // behind every read of the counts
+  sh.dropped[tid] = lowers ? page : -1;
+  __syncthreads();
+  if (lowers && was == 1) {
+    uint32_t last = e;
+    if (refs > 1)
+      for (last = entries - 1; sh.dropped[last] != page; --last) {}
+    sh.freed[last] = 1;
+  }
+  __syncthreads();
+  const bool freed = sh.freed[tid] != 0;
+  uint32_t all_freed;
+  const uint32_t rank = block_scan(freed ? 1u : 0u, sh.warp_sums, all_freed);
+  const uint32_t left = (uint32_t)free_now - sh.all_taken;
+  if (freed && left + rank < (uint32_t)p.num_pages) p.free_list[left + rank] = page;
+  if (take || drop) {
+    int32_t fresh = -1;
+    if (take) {
+      fresh = sh.top[at];
+      if (fresh >= 0 && fresh < p.num_pages) p.refs[fresh] = 1;
+      else bad |= KV_NVFP4_DEV_BAD_PAGE;
+      if (drop && (int64_t)j * kPage < keep) {
+        r.copies[2 * s] = page;
+        r.copies[2 * s + 1] = fresh;
+      }
+    }
+    p.block_table[(int64_t)s * p.max_pages + j] = fresh;
+  }
+  for (int q = tid; q < S; q += kResizeThreads)
+    if (held_of[q] != need_of[q] && met(q, upto)) p.held[q] = need_of[q];
+  if (tid == 0) *p.free_count = (int32_t)min(left + all_freed, (uint32_t)p.num_pages);
+  if (bad != 0) flag_status(r.status, bad);
+}
+
 // One cluster. The entries that a call can touch (places keep / 64 .. max(held, need) of every sequence)
 // lie end to end in the order of sequences and places; a CTA takes a contiguous share of them, and
 // every CTA knows every sequence's numbers (it works them out itself). An entry is
@@ -167,6 +262,7 @@ __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(const Resi
   __shared__ uint32_t warp_sums[32];
   __shared__ uint32_t out_counts[2];    // freed and taken entries of this CTA's share
   __shared__ uint32_t all_taken;
+  __shared__ FewEntries few;
   const kv_nvfp4_pages& p = r.p;
   const int tid = threadIdx.x, S = p.num_seqs;
   const uint32_t C = cluster_size(), rank = cluster_rank();
@@ -222,6 +318,11 @@ __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(const Resi
     return last - (before[s + 1] - (int32_t)e);
   };
   auto inside = [&](int32_t page) { return page >= 0 && page < p.num_pages; };
+
+  if (entries <= (uint32_t)kResizeThreads) {  // the same for every CTA
+    if (rank == 0) resize_few(r, few, before, need_of, held_of, seq_of, place_of, entries, free_now, bad);
+    return;
+  }
 
   // shared entries, found by every CTA for itself (mostly one per sequence is looked at)
   for (uint32_t e = tid; e < entries; e += kResizeThreads) {
