@@ -9,11 +9,14 @@ import math
 import numpy as np
 import torch
 
-from . import (_capturing, kv_nvfp4_append, kv_nvfp4_append_slots, kv_nvfp4_decode_attn,
-               kv_nvfp4_decode_attn_weights, kv_nvfp4_decode_step, kv_nvfp4_decode_step_host,
-               kv_nvfp4_evict_compact, kv_nvfp4_evict_select, kv_nvfp4_plan,
-               kv_nvfp4_plan_workspace_bytes, kv_nvfp4_pool_bytes, kv_nvfp4_rope_table_init,
-               kv_nvfp4_weights_workspace_bytes, make_layout)
+from . import (MAX_TREE, _capturing, kv_nvfp4_append, kv_nvfp4_append_slots, kv_nvfp4_copy_pages,
+               kv_nvfp4_decode_attn, kv_nvfp4_decode_attn_weights, kv_nvfp4_decode_step,
+               kv_nvfp4_decode_step_host, kv_nvfp4_evict_compact, kv_nvfp4_evict_select,
+               kv_nvfp4_pages_fork, kv_nvfp4_pages_init, kv_nvfp4_pages_resize,
+               kv_nvfp4_pages_workspace_bytes, kv_nvfp4_plan, kv_nvfp4_plan_workspace_bytes,
+               kv_nvfp4_pool_bytes, kv_nvfp4_rope_table_init, kv_nvfp4_tree_accept,
+               kv_nvfp4_tree_attn, kv_nvfp4_tree_mask, kv_nvfp4_weights_workspace_bytes, make_layout,
+               make_pages)
 
 
 class PagedNVFP4Cache:
@@ -39,6 +42,7 @@ class PagedNVFP4Cache:
         self.workspace = None
         self.weights_workspace = None
         self.plan_info = None
+        self.pages = None
         self._captured = []
 
     # -- fused quantize-append --------------------------------------------------------------
@@ -108,13 +112,7 @@ class PagedNVFP4Cache:
         if weights_in is not None and weights_in.shape != weights.shape:
             raise ValueError("weights_in must have the shape of weights")
         rows = self.plan_info.num_seqs * self.plan_info.q_len * self.layout.num_q_heads
-        if out.dtype != torch.bfloat16 or not out.is_contiguous() or out.numel() != rows * 128 or \
-                out.device != weights.device:
-            raise ValueError("out must be a contiguous device bfloat16 [rows, num_q_heads, 128]")
-        for x, each in ((q_codes, 64), (q_scales, 8)):
-            if x.device != weights.device or not x.is_contiguous() or x.nbytes < rows * each:
-                raise ValueError("q_codes and q_scales must be contiguous, on the device, and hold "
-                                 "64 and 8 bytes per row of the plan")
+        self._rows("out", out, rows, q_codes, q_scales)
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(128)
         need = kv_nvfp4_weights_workspace_bytes(self.layout, self.plan_info)
@@ -153,6 +151,140 @@ class PagedNVFP4Cache:
         kv_nvfp4_evict_compact(self.layout, index, index.shape[2], per_head, seq_lens, keep,
                                self.num_seqs, self.block_table, self.max_pages, self.num_pages,
                                self.pool, None, 0, weights, weights.shape[2], self.status, stream)
+
+    # -- trees of drafted tokens ------------------------------------------------------------------
+    def tree_buffers(self, n):
+        """Buffers of tree_mask for n nodes per sequence: the mask [num_seqs, n, ceil(n / 32)] for
+        attend_tree, and seq_ids, slots, positions [num_seqs * n] for append."""
+        if not 1 <= n <= MAX_TREE:
+            raise ValueError(f"a tree has 1 to {MAX_TREE} nodes")
+        new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=self.device)  # noqa: E731
+        rows = self.num_seqs * n
+        return new(self.num_seqs, n, (n + 31) // 32), new(rows), new(rows), new(rows)
+
+    def tree_mask(self, parents, lens, buffers, first_pos=None, stream=None):
+        """Fills the buffers of tree_buffers from parents [num_seqs, n]: node i hangs on node
+        parents[s, i] < i, or with -1 on the cache; one with any other parent, or below such a one, is
+        padding. lens [num_seqs]: tokens in the cache before the tree; first_pos [num_seqs]: the next
+        token's position where it is not the length (behind an eviction)."""
+        mask, seq_ids, slots, positions = buffers
+        n = self._nodes(parents)
+        rows = self.num_seqs * n
+        self._int32("parents", parents, rows)
+        self._int32("lens", lens, self.num_seqs)
+        self._int32("mask", mask, rows * ((n + 31) // 32))
+        for x in (seq_ids, slots, positions):
+            self._int32("seq_ids, slots and positions", x, rows)
+        if first_pos is not None:
+            self._int32("first_pos", first_pos, self.num_seqs)
+        kv_nvfp4_tree_mask(parents, self.num_seqs, n, lens, first_pos, mask, seq_ids, slots, positions,
+                           self.status, stream)
+
+    def attend_tree(self, q_codes, q_scales, out, mask, sm_scale=None, stream=None):
+        """Attention of the tree's nodes, the last q_len tokens of every sequence of the last plan()
+        (made with causal=False): each sees the cache and the nodes in its mask. out: bf16. A captured
+        call replays on the plan that it was captured with."""
+        self._check_current()
+        plan = self.plan_info
+        if plan is None or plan.causal:
+            raise ValueError("attend_tree needs a plan() with causal=False")
+        if plan.num_seqs > self.num_seqs:
+            raise ValueError("the plan has more sequences than the cache")
+        rows = plan.num_seqs * plan.q_len * self.layout.num_q_heads
+        self._int32("mask", mask, plan.num_seqs * plan.q_len * ((plan.q_len + 31) // 32))
+        self._rows("out", out, rows, q_codes, q_scales)
+        if sm_scale is None:
+            sm_scale = 1.0 / math.sqrt(128)
+        self._hold_captured(stream)
+        kv_nvfp4_tree_attn(self.layout, plan, self.workspace, q_codes, q_scales, mask, sm_scale,
+                           self.pool, self.num_pages, self.block_table, self.max_pages, out,
+                           self.status, stream)
+
+    def tree_accept(self, parents, draft, target, expected, lens, path, count, next_token,
+                    new_lens=None, stream=None):
+        """The path of each tree that the model agrees with (draft, target [num_seqs, n], expected
+        [num_seqs]: the token awaited behind the cache), its rows moved behind the cache. Fills path
+        [num_seqs, n] up to count, count, next_token and new_lens [num_seqs]; next_token may be
+        expected, new_lens lens. parents, draft, target, expected and next_token None: path and count
+        are given (a path chosen another way)."""
+        n = self._nodes(path)
+        rows = self.num_seqs * n
+        for name, x, size in (("parents", parents, rows), ("draft", draft, rows),
+                              ("target", target, rows), ("expected", expected, self.num_seqs),
+                              ("lens", lens, self.num_seqs), ("path", path, rows),
+                              ("count", count, self.num_seqs),
+                              ("next_token", next_token, self.num_seqs),
+                              ("new_lens", new_lens, self.num_seqs)):
+            if x is not None or name in ("lens", "path", "count"):
+                self._int32(name, x, size)
+        kv_nvfp4_tree_accept(self.layout, parents, draft, target, expected, self.num_seqs, n, lens,
+                             self.block_table, self.max_pages, self.num_pages, self.pool, path, count,
+                             next_token, new_lens, self.status, stream)
+
+    # -- pages that sequences take, share and give back ---------------------------------------------
+    def page_accounts(self, stream=None):
+        """Puts the cache's pages under accounts (self.pages): the block table is emptied and every page
+        is free. From then on resize() makes room and frees it, before every append."""
+        self._check_current()
+        new = lambda n: torch.empty(n, dtype=torch.int32, device=self.device)  # noqa: E731
+        with self._on(stream):
+            work = torch.empty(kv_nvfp4_pages_workspace_bytes(self.num_pages), dtype=torch.uint8,
+                               device=self.device)
+            self.copies = torch.full((self.num_seqs, 2), -1, dtype=torch.int32, device=self.device)
+            self.pages = make_pages(self.block_table, new(self.num_seqs), new(self.num_pages),
+                                    new(self.num_pages), new(1), work)
+        kv_nvfp4_pages_init(self.pages, stream)
+        return self.pages
+
+    def fork(self, src, dst, lens, stream=None):
+        """Sequences dst[i], which hold no pages, share those of the first lens[i] tokens of src[i]
+        (device int32). The next resize() replaces what a sequence is about to write."""
+        self._check_accounted()
+        for name, x in (("src", src), ("dst", dst), ("lens", lens)):
+            self._int32(name, x, dst.numel())
+        if dst.numel() > self.num_seqs:
+            raise ValueError("more forks than sequences")
+        kv_nvfp4_pages_fork(self.pages, src, dst, lens, dst.numel(), self.status, stream)
+
+    def resize(self, keep_lens, new_lens, copy=True, stream=None):
+        """Room for new_lens tokens of every sequence, of which the first keep_lens stay (device int32
+        [num_seqs]); both 0 end a sequence. Shared pages that are to be written are replaced, and with
+        `copy` the kept tokens in them copied; else self.copies says which (several layers' pools under
+        one cache's accounts: kv_nvfp4_copy_pages on each)."""
+        self._check_accounted()
+        self._int32("keep_lens", keep_lens, self.num_seqs)
+        self._int32("new_lens", new_lens, self.num_seqs)
+        kv_nvfp4_pages_resize(self.pages, keep_lens, new_lens, self.copies, self.status, stream)
+        if copy:
+            kv_nvfp4_copy_pages(self.layout, self.pool, self.num_pages, self.copies, self.num_seqs,
+                                self.status, stream)
+
+    def _nodes(self, x):
+        """Nodes per sequence of [num_seqs, n] buffers."""
+        self._check_current()
+        n = x.shape[1] if x.dim() == 2 else 0
+        if not 1 <= n <= MAX_TREE or x.shape[0] != self.num_seqs:
+            raise ValueError(f"trees are [num_seqs, n] with n from 1 to {MAX_TREE}")
+        return n
+
+    def _int32(self, name, x, numel):
+        if x is None or x.dtype != torch.int32 or not x.is_contiguous() or x.numel() != numel or \
+                x.device != self.pool.device:
+            raise ValueError(f"{name} must be contiguous device int32 of {numel} entries")
+
+    def _rows(self, name, out, rows, q_codes, q_scales):
+        if out.dtype != torch.bfloat16 or not out.is_contiguous() or out.numel() != rows * 128 or \
+                out.device != self.pool.device:
+            raise ValueError(f"{name} must be a contiguous device bfloat16 [rows, num_q_heads, 128]")
+        for x, each in ((q_codes, 64), (q_scales, 8)):
+            if x.device != self.pool.device or not x.is_contiguous() or x.nbytes < rows * each:
+                raise ValueError("q_codes and q_scales must be contiguous, on the device, and hold "
+                                 "64 and 8 bytes per row of the plan")
+
+    def _check_accounted(self):
+        self._check_current()
+        if self.pages is None:
+            raise ValueError("the cache's pages are under no accounts: page_accounts() first")
 
     def _enlarge(self, name, need, stream):
         """Replaces a workspace by one of `need` bytes, from the allocator's memory of the stream that
