@@ -152,6 +152,18 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* warp_sums, 
   return before + x - v;
 }
 
+// The number of the block's threads before this one with v set, and of all of them.
+__device__ __forceinline__ uint32_t block_rank(bool v, uint32_t* warp_sums, uint32_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t set = __ballot_sync(0xffffffffu, v);
+  __syncthreads();  // the sums of a scan before have been read
+  if (lane == 0) warp_sums[warp] = __popc(set);
+  __syncthreads();
+  const uint32_t mine = warp_sums[lane];  // 32 warps
+  total = __reduce_add_sync(0xffffffffu, mine);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0u) + __popc(set & ((1u << lane) - 1u));
+}
+
 // A resize of at most one entry per thread, by one CTA: everything stays in registers, and the cluster
 // need not meet. A page that several rows drop is freed by whoever lowers its count to zero, in the
 // place of its last drop, which that thread looks up.
@@ -194,7 +206,7 @@ __device__ __forceinline__ void resize_few(const ResizeParams& r, FewEntries& sh
     }
   }
   uint32_t wanted;
-  const uint32_t at = block_scan(take ? 1u : 0u, sh.warp_sums, wanted);
+  const uint32_t at = block_rank(take, sh.warp_sums, wanted);
   sh.takes_before[tid] = at;
   sh.top[tid] = top;
   if (tid == 0) sh.takes_before[entries] = wanted;
@@ -225,7 +237,7 @@ __device__ __forceinline__ void resize_few(const ResizeParams& r, FewEntries& sh
   __syncthreads();
   const bool freed = sh.freed[tid] != 0;
   uint32_t all_freed;
-  const uint32_t rank = block_scan(freed ? 1u : 0u, sh.warp_sums, all_freed);
+  const uint32_t rank = block_rank(freed, sh.warp_sums, all_freed);
   const uint32_t left = (uint32_t)free_now - sh.all_taken;
   if (freed && left + rank < (uint32_t)p.num_pages) p.free_list[left + rank] = page;
   if (take || drop) {
@@ -247,6 +259,133 @@ __device__ __forceinline__ void resize_few(const ResizeParams& r, FewEntries& sh
   if (bad != 0) flag_status(r.status, bad);
 }
 
+// A resize of at most kShareEntries entries per thread of the cluster whose demand the stack meets
+// (else false, with nothing changed): each entry is looked at once and stays in registers. The cluster
+// meets when the counts have been read, when the last drops of pages with several holders are noted
+// (only if there are any), when the freed entries are counted, and before it ends.
+constexpr int kShareEntries = 4;
+
+template <class SeqOf, class PlaceOf>
+__device__ __forceinline__ bool resize_shares(const ResizeParams& r, const PagesWork& w, uint32_t call,
+                                              uint32_t* warp_sums, uint32_t* out_counts,
+                                              const int32_t* before, const int32_t* need_of,
+                                              const int32_t* held_of, SeqOf seq_of, PlaceOf place_of,
+                                              uint32_t entries, int32_t free_now, int32_t bad) {
+  const kv_nvfp4_pages& p = r.p;
+  const int tid = threadIdx.x, S = p.num_seqs;
+  const uint32_t C = cluster_size(), rank = cluster_rank();
+  const uint32_t share = max((entries + C - 1) / C, (uint32_t)kResizeThreads);
+  const uint32_t e_lo = min(entries, rank * share), e_hi = min(entries, e_lo + share);
+  int32_t seq[kShareEntries], place[kShareEntries], page[kShareEntries], other[kShareEntries];
+  uint32_t at[kShareEntries];
+  bool take[kShareEntries], drop[kShareEntries];  // drop: of a page in the pool
+  bool gone[kShareEntries];                       // the place is emptied
+#pragma unroll
+  for (int u = 0; u < kShareEntries; ++u) {
+    const uint32_t e = e_lo + u * kResizeThreads + tid;
+    seq[u] = place[u] = 0;
+    page[u] = -1;
+    take[u] = drop[u] = gone[u] = false;
+    if (e >= e_hi) continue;
+    seq[u] = seq_of(e);
+    place[u] = place_of(seq[u], e);
+    take[u] = place[u] >= held_of[seq[u]];
+    gone[u] = !take[u] && place[u] >= need_of[seq[u]];
+    if (!take[u]) page[u] = p.block_table[(int64_t)seq[u] * p.max_pages + place[u]];
+  }
+  bool some = false;
+#pragma unroll
+  for (int u = 0; u < kShareEntries; ++u) {
+    const bool in_pool = page[u] >= 0 && page[u] < p.num_pages;
+    const bool real = e_lo + u * kResizeThreads + tid < e_hi;
+    other[u] = in_pool ? __ldcg(p.refs + page[u]) : 1;
+    if (real && !take[u] && !in_pool) bad |= KV_NVFP4_DEV_BAD_PAGE;
+    drop[u] = in_pool && (gone[u] || other[u] > 1);
+    if (drop[u] && !gone[u]) take[u] = true;
+    some = some || (drop[u] && other[u] > 1);
+  }
+  uint32_t taken = 0, sum;
+#pragma unroll
+  for (int u = 0; u < kShareEntries; ++u) {
+    at[u] = 0;
+    if (e_lo + u * kResizeThreads >= e_hi) continue;  // for the whole CTA
+    at[u] = taken + block_rank(take[u], warp_sums, sum);
+    taken += sum;
+  }
+  some = __syncthreads_or(some);
+  if (tid == 0) {
+    out_counts[1] = taken;
+    out_counts[2] = some;
+  }
+  cluster_meet();  // the counts of holders have been read
+  uint32_t taken_before = 0, all_taken = 0;
+  bool shared = false;
+  for (uint32_t c = 0; c < C; ++c) {
+    const uint32_t n = cluster_load(&out_counts[1], c);
+    if (c < rank) taken_before += n;
+    all_taken += n;
+    shared = shared || cluster_load(&out_counts[2], c) != 0u;
+  }
+  if (all_taken > (uint32_t)free_now) return false;  // the same for the whole cluster
+
+  int32_t fresh[kShareEntries];
+#pragma unroll
+  for (int u = 0; u < kShareEntries; ++u) {
+    const uint32_t e = e_lo + u * kResizeThreads + tid;
+    fresh[u] = take[u] ? p.free_list[free_now - 1 - (int32_t)(taken_before + at[u])] : -1;
+    if (drop[u]) {
+      atomicSub(p.refs + page[u], 1);
+      if (other[u] > 1) atomicMax(w.last_drop + page[u], ((unsigned long long)call << 32) | (e + 1));
+    }
+  }
+  if (shared) cluster_meet();  // the counts are lowered, the last drops noted
+  uint32_t freed = 0;
+#pragma unroll
+  for (int u = 0; u < kShareEntries; ++u) {
+    const uint32_t e = e_lo + u * kResizeThreads + tid;
+    if (drop[u] && other[u] > 1)  // the last holder's, in the place of the last drop
+      drop[u] = __ldcg(p.refs + page[u]) == 0 &&
+                __ldcg(w.last_drop + page[u]) == (((unsigned long long)call << 32) | (e + 1));
+    if (e_lo + u * kResizeThreads >= e_hi) continue;
+    at[u] = freed + block_rank(drop[u], warp_sums, sum);
+    freed += sum;
+  }
+  if (tid == 0) out_counts[0] = freed;
+  cluster_meet();  // the stack's top has been read
+  uint32_t freed_before = 0, all_freed = 0;
+  for (uint32_t c = 0; c < C; ++c) {
+    const uint32_t n = cluster_load(&out_counts[0], c);
+    if (c < rank) freed_before += n;
+    all_freed += n;
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // awaited at the end
+  const uint32_t left = (uint32_t)free_now - all_taken;
+#pragma unroll
+  for (int u = 0; u < kShareEntries; ++u) {
+    const uint32_t to = left + freed_before + at[u];
+    if (drop[u] && to < (uint32_t)p.num_pages) p.free_list[to] = page[u];
+    if (!take[u] && !gone[u]) continue;
+    if (take[u]) {
+      if (fresh[u] >= 0 && fresh[u] < p.num_pages) p.refs[fresh[u]] = 1;
+      else bad |= KV_NVFP4_DEV_BAD_PAGE;
+      if (page[u] >= 0 && (int64_t)place[u] * kPage < r.keep[seq[u]]) {
+        r.copies[2 * seq[u]] = page[u];
+        r.copies[2 * seq[u] + 1] = fresh[u];
+      }
+    }
+    p.block_table[(int64_t)seq[u] * p.max_pages + place[u]] = fresh[u];
+  }
+  for (int q = (int)(rank * kResizeThreads) + tid; q < S; q += (int)(C * kResizeThreads))
+    if (held_of[q] != need_of[q]) p.held[q] = need_of[q];
+  if (rank == 0 && tid == 0) {
+    *p.free_count = (int32_t)min(left + all_freed, (uint32_t)p.num_pages);
+    *w.calls = call;
+  }
+  if (bad != 0) flag_status(r.status, bad);
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  return true;
+}
+
 // One cluster. The entries that a call can touch (places keep / 64 .. max(held, need) of every sequence)
 // lie end to end in the order of sequences and places; a CTA takes a contiguous share of them, and
 // every CTA knows every sequence's numbers (it works them out itself). An entry is
@@ -260,7 +399,8 @@ __device__ __forceinline__ void resize_few(const ResizeParams& r, FewEntries& sh
 __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(const ResizeParams r) {
   extern __shared__ int32_t per_seq[];  // [num_seqs + 1] entries before, [num_seqs] need, held, demand
   __shared__ uint32_t warp_sums[32];
-  __shared__ uint32_t out_counts[2];    // freed and taken entries of this CTA's share
+  __shared__ uint32_t out_counts[3];    // freed and taken entries of this CTA's share, and whether one
+                                        // is dropped from among several holders
   __shared__ uint32_t all_taken;
   __shared__ FewEntries few;
   const kv_nvfp4_pages& p = r.p;
@@ -323,6 +463,11 @@ __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(const Resi
     if (rank == 0) resize_few(r, few, before, need_of, held_of, seq_of, place_of, entries, free_now, bad);
     return;
   }
+
+  if (entries <= C * (uint32_t)(kResizeThreads * kShareEntries) &&
+      resize_shares(r, w, call, warp_sums, out_counts, before, need_of, held_of, seq_of, place_of,
+                    entries, free_now, bad))
+    return;
 
   // shared entries, found by every CTA for itself (mostly one per sequence is looked at)
   for (uint32_t e = tid; e < entries; e += kResizeThreads) {

@@ -48,7 +48,7 @@ class Accounts:
             if k < 0 or n < k or need > P or h < 0 or h > P or (k + 63) // 64 > h:
                 self.bad_pos = True
                 continue
-            take, drop = [], []
+            take, drop = [], []  # places, ascending
             for j in range(k // 64, max(h, need)):
                 page = self.table[s, j]
                 if j >= h:
@@ -66,25 +66,24 @@ class Accounts:
             if take and demand_before > have_free:
                 self.no_page = True
                 continue
+            fresh = {j: self.free[have_free - 1 - taken - i] for i, j in enumerate(take)}
             for j in drop:
                 drops.append(int(self.table[s, j]))
-                old = drops[-1]
-                if j in take:
-                    if j * 64 < k:
-                        copies[s] = old, self.free[have_free - 1 - taken - take.index(j)]
-                else:
-                    self.table[s, j] = -1
-            for i, j in enumerate(take):
-                self.table[s, j] = self.free[have_free - 1 - taken - i]
-                self.refs[self.table[s, j]] = 1
+                if j in fresh and j * 64 < k:
+                    copies[s] = drops[-1], fresh[j]
+                self.table[s, j] = -1
+            for j in take:
+                self.table[s, j] = fresh[j]
+                self.refs[fresh[j]] = 1
             taken += len(take)
             self.held[s] = need
         drops = [p for p in drops if self.inside(p)]
         for p in drops:
             self.refs[p] -= 1
         self.count -= taken
+        last = {p: i for i, p in enumerate(drops)}
         for i, p in enumerate(drops):
-            if self.refs[p] == 0 and p not in drops[i + 1:]:
+            if self.refs[p] == 0 and last[p] == i:
                 self.free[self.count] = p
                 self.count += 1
         return copies

@@ -78,7 +78,8 @@ def test_init():
 @pytest.mark.parametrize("S,P,N,steps,seed", [(1, 3, 5, 12, 0), (4, 6, 20, 40, 1), (7, 40, 200, 30, 2),
                                               (33, 12, 300, 30, 3), (100, 100, 4000, 15, 4),
                                               (1500, 3, 3000, 6, 5), (3, 3000, 6000, 8, 6),
-                                              (8, 2500, 9000, 8, 7)])
+                                              (8, 2500, 9000, 8, 7), (16, 3000, 50000, 6, 8),
+                                              (16, 3000, 30000, 6, 9)])
 def test_any_mix(S, P, N, steps, seed):
     """Random calls, some of which ask for more pages than there are."""
     rng = np.random.default_rng(seed)
