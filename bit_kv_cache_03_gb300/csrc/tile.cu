@@ -689,7 +689,8 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
 #pragma unroll
         for (int c = 0; c < kNc; c += 2) {
           float p0, p1;
-          if (kDup) {  // (in pairs: verify 110 -> 107 us; with all of a page's columns it spills)
+          if (kDup || kTree) {  // (in pairs: verify 110 -> 107 us; with all of a page's columns it
+                                // spills, unless each part is stored as it is made)
             halves_of(fma2(pair_of(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), c2c2, mm),
                       p0, p1);
             p0 = fast_exp2(p0);
@@ -700,6 +701,10 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
           }
           pk[c >> 1] = pack_f16x2(p0, p1);
           if (kAcc) l2[(c >> 1) & 1] = add2(l2[(c >> 1) & 1], pair_of(p0, p1));
+          // trees: stored 16 keys at a time beside the next ones' exponentials (64 nodes, 4 x 131072
+          // keys: 331 us with one store of all 64, 321 with two, 317 with four)
+          if (kTree && !kDup && c % 16 == 14)
+            tmem_st8(scol + c / 16 * 8, *reinterpret_cast<uint32_t(*)[8]>(&pk[c / 16 * 8]));
         }
         if (kAcc) {
           float even, odd;
@@ -710,7 +715,7 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
           tmem_st16(scol, pk);
           // zeros over the same keys of the other page (columns no warp of this quadrant reads)
           tmem_st16_zero(sbuf + 64 * (pg ^ 1) + kofs);
-        } else {
+        } else if constexpr (!kTree) {
           tmem_st32(scol, pk);
         }
         // rows whose max was raised: this warp's half of their row of O (half 0 also l) is
