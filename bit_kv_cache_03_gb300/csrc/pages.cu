@@ -5,6 +5,9 @@
 // Everything is decided in one order, sequence by sequence and place by place, so that equal calls
 // give equal tables: counts go up and down by integer atomics, whose order does not show, and what is
 // taken from the stack or pushed onto it is ranked by prefix sums.
+//
+// Each kernel lets the launch of the next one on the stream begin while it runs; that one waits for its
+// end before it reads anything (two resizes for 4 sessions, back to back in a graph: 8.1 -> 7.0 us).
 
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -35,6 +38,7 @@ __host__ __device__ inline PagesWork pages_work(void* workspace, int64_t num_pag
 }
 
 __global__ void __launch_bounds__(256) pages_init_kernel(const kv_nvfp4_pages p) {
+  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t first = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
   const PagesWork w = pages_work(p.workspace, p.num_pages);
@@ -68,6 +72,7 @@ constexpr int kForkThreads = 512;
 __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const ForkParams f) {
   const kv_nvfp4_pages& p = f.p;
   const int tid = threadIdx.x, i = blockIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t src = f.src[i], dst = f.dst[i], len = f.lens[i];
   bool bad = src < 0 || src >= p.num_seqs || dst < 0 || dst >= p.num_seqs;
@@ -411,6 +416,7 @@ __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(const Resi
   int32_t* const held_of = need_of + S;
   int32_t* const demand = held_of + S;  // then 1: gets its pages, 0: stays as it was
   const PagesWork w = pages_work(p.workspace, p.num_pages);
+  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t call = __ldcg(w.calls) + 1;
   const int32_t stack = __ldcg(p.free_count);
@@ -618,6 +624,7 @@ __global__ void __launch_bounds__(kPairThreads) copy_pages_kernel(uint8_t* pool,
                                                                   const int32_t* pairs, int32_t n,
                                                                   int32_t num_pages, int32_t Hkv,
                                                                   int32_t* status) {
+  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int64_t unit = blockIdx.x; unit < (int64_t)n * Hkv; unit += gridDim.x) {
     const int64_t i = unit / Hkv, part = unit % Hkv;

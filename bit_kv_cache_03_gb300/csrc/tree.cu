@@ -40,6 +40,7 @@ __global__ void __launch_bounds__(32 * kWords) tree_mask_kernel(const TreeMaskPa
   __shared__ int32_t above[32 * kWords];
   const int i = threadIdx.x, n = p.n, W = (n + 31) >> 5;  // W <= kWords: every node has its thread
   const int64_t seq = blockIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t len = p.lens[seq];
   const int32_t first = p.first_pos != nullptr ? p.first_pos[seq] : len;
@@ -115,6 +116,7 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const TreeA
   __shared__ int32_t walked[2];  // the path's length, the token behind it
   const int tid = threadIdx.x, lane = tid & 31, n = p.n;
   const int64_t seq = blockIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t base = p.lens[seq];
   const bool walk = p.parents != nullptr;
