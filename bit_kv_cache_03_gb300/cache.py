@@ -224,15 +224,17 @@ class PagedNVFP4Cache:
     # -- pages that sequences take, share and give back ---------------------------------------------
     def page_accounts(self, stream=None):
         """Puts the cache's pages under accounts (self.pages): the block table is emptied and every page
-        is free. From then on resize() makes room and frees it, before every append."""
+        is free. From then on resize() makes room and frees it, before every append. Called again it
+        empties the accounts that there are, which captured calls work on."""
         self._check_current()
         new = lambda n: torch.empty(n, dtype=torch.int32, device=self.device)  # noqa: E731
-        with self._on(stream):
-            work = torch.empty(kv_nvfp4_pages_workspace_bytes(self.num_pages), dtype=torch.uint8,
-                               device=self.device)
-            self.copies = torch.full((self.num_seqs, 2), -1, dtype=torch.int32, device=self.device)
-            self.pages = make_pages(self.block_table, new(self.num_seqs), new(self.num_pages),
-                                    new(self.num_pages), new(1), work)
+        if self.pages is None:
+            with self._on(stream):
+                work = torch.empty(kv_nvfp4_pages_workspace_bytes(self.num_pages), dtype=torch.uint8,
+                                   device=self.device)
+                self.copies = torch.full((self.num_seqs, 2), -1, dtype=torch.int32, device=self.device)
+                self.pages = make_pages(self.block_table, new(self.num_seqs), new(self.num_pages),
+                                        new(self.num_pages), new(1), work)
         kv_nvfp4_pages_init(self.pages, stream)
         return self.pages
 

@@ -948,7 +948,7 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
       const int r = row0 + (lane & 7);
       if (TREE)  // the nodes that the row's node sees; bits from q_len on count for nothing
         mylim = r < rows_total
-                    ? (int)(__ldg(p.mask + (int64_t)sg.seq * p.q_len + r / p.G) & ((1u << p.q_len) - 1u))
+                    ? (int)(p.mask[(int64_t)sg.seq * p.q_len + r / p.G] & ((1u << p.q_len) - 1u))
                     : 0;
       else
         mylim = (r < rows_total) ? (p.causal ? L0 + r / p.G : sg.len - 1) : -1;
@@ -1543,9 +1543,10 @@ cudaError_t launch_merge_weights(const void* groups, const int32_t* split_groups
                               merges + (int64_t)num_seqs * Hkv * a.parts, stream);
 }
 
-// The split-K merge launch (also used by the comparator decode; with tree_out rows go there in bf16): one CTA per (split group, KV
+// The split-K merge launch (also used by the comparator decode): one CTA per (split group, KV
 // head, row of the tile), as a programmatic dependent of the attention kernel before it on the
-// stream (it waits for that grid to complete before reading the partials).
+// stream (it waits for that grid to complete before reading the partials). With tree_out the rows go
+// there, in bf16.
 cudaError_t launch_split_merge(const void* groups, const int32_t* split_groups,
                                const float* partials, float* out, int32_t Hq, int32_t Hkv,
                                int32_t G, int32_t q_len, float c2, int32_t num_split,

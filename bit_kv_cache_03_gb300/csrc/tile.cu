@@ -528,7 +528,7 @@ __device__ __forceinline__ void t_tree_window(const TileParams& p, const TSeg& s
     if (k < 0) return 0xFFFFFFFFu;  // keys before the nodes
     if (k >= W) return 0u;
     const int left = p.q_len - 32 * k;
-    return __ldg(row + k) & (left < 32 ? (1u << left) - 1u : 0xFFFFFFFFu);
+    return row[k] & (left < 32 ? (1u << left) - 1u : 0xFFFFFFFFu);
   };
   uint32_t lo = word(first >> 5);
 #pragma unroll
@@ -540,9 +540,9 @@ __device__ __forceinline__ void t_tree_window(const TileParams& p, const TSeg& s
     const int node = first + 32 * i + lane;
     bool nan = false;
     if (valid && node >= 0 && node < p.q_len) {
-      const uint2 sc = __ldg(reinterpret_cast<const uint2*>(
+      const uint2 sc = *reinterpret_cast<const uint2*>(
           p.pool + (int64_t)pid * p.Hkv * 9216 + (int64_t)p.Hkv * 8704 + sg.head * 512 +
-          (kofs + 32 * i + lane) * kScaleBytes));
+          (kofs + 32 * i + lane) * kScaleBytes);
       nan = e4m3x4_any_nan(sc.x) || e4m3x4_any_nan(sc.y);
     }
     v_nan[i] = __ballot_sync(0xffffffffu, nan);
@@ -602,15 +602,16 @@ __device__ void t_softmax(const TileParams& p, uint8_t* smem, uint32_t tbase, in
     float ls = 0.f;  // kAcc: this thread's sum of the row's P
     // this warp's page of each block is skipped (its keys masked) when its id lies outside the
     // pool, as the producer skips it; the id is read from the block table one block ahead, so that
-    // the block loop touches no shared-memory barrier but the S-full and P-full ones
+    // the block loop touches no shared-memory barrier but the S-full and P-full ones (by plain loads, as
+    // the masks: a kernel that this one was launched beside, kv_nvfp4_pages_resize, may have written it)
     const int32_t* bt = p.block_table + (int64_t)sg.seq * p.max_pages;
-    int32_t pid_next = (sg.lo + pg < sg.hi) ? __ldg(bt + sg.lo + pg) : -1;
+    int32_t pid_next = (sg.lo + pg < sg.hi) ? bt[sg.lo + pg] : -1;
     for (int j = 0; j < n; ++j, ++kb) {
       const uint32_t b = kb & 1u;
       const int page = sg.lo + 2 * j + pg;
       const int32_t pid = pid_next;
       const bool valid = page < sg.hi && pid >= 0 && pid < p.num_pages;
-      if (page + 2 < sg.hi) pid_next = __ldg(bt + page + 2);
+      if (page + 2 < sg.hi) pid_next = bt[page + 2];
       // kTree: bit c of these words: this row sees key c of this warp's share; that key's V has a NaN
       uint32_t sees[kNc / 32], v_nan[kNc / 32];
       const bool nodes = kTree && (page + 1) * kPage > sg.len - p.q_len;

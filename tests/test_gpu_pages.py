@@ -205,3 +205,40 @@ def test_captured_calls_follow_their_inputs():
         b.ref.resize(keeps, rooms)
         b.ref.fork([0], [to], [100])
         b.same()
+
+
+def test_most_sequences():
+    """As many sequences as accounts may have: forks of half of them, and more pages asked for than
+    there are."""
+    S = kv().MAX_ACCOUNTED_SEQS
+    b = Both(S, 3, 3 * S // 2)
+    half, rest = np.arange(S // 2), np.arange(S // 2, S)
+    n = np.where(half % 3 == 0, 64, 100)
+    b.resize(np.zeros(S, int), np.concatenate([n, np.zeros(S // 2, int)]))
+    b.fork(half.tolist(), rest.tolist(), n)
+    lens = np.concatenate([n, n])
+    b.resize(lens, lens + 30)
+    lens = np.minimum(lens, b.ref.held * 64)
+    b.resize(lens, np.minimum(lens + 90, 192))
+    b.resize(np.zeros(S, int), np.zeros(S, int))
+    assert b.ref.count == 3 * S // 2
+    b.ref.check()
+
+
+def test_captured_resize_outlives_emptied_accounts():
+    k = kv()
+    c = k.PagedNVFP4Cache(9, np.zeros((2, 4), np.int32), 1, 4, 2, rot_dim=0)
+    c.page_accounts()
+    keep, room = dev([0, 0]), dev([100, 70])
+    c.resize(keep, room)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        c.resize(keep, room)
+    c.page_accounts()
+    room.copy_(dev([65, 10]))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert c.block_table.tolist() == [[0, 1, -1, -1], [2, -1, -1, -1]]
+    assert int(c.status.item()) == 0

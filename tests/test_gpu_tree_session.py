@@ -165,3 +165,65 @@ def test_layers_share_accounts():
     assert (copies >= 0).all()
     for src, dst in copies:
         assert torch.equal(other.view(12, -1)[dst], before[src])
+
+
+@pytest.mark.parametrize("Hq,H,n", [(8, 4, 2), (24, 4, 8), (24, 4, 40)])
+def test_a_chain_of_calls_needs_no_waits(Hq, H, n):
+    """The same steps with and without a wait behind every call: every kernel is launched while those
+    before it run, and must not read what they have yet to write."""
+    import bit_kv_cache_03_gb300 as kv
+    S, P, N, steps = 6, 40, 300, 12
+    rng = np.random.default_rng(n)
+    held = [700, 65, 2000, 0, 129, 1500]
+    parents = [dev(np.stack([treeref.random_tree(rng, n, 0.1) for _ in range(S)])) for _ in range(steps)]
+    paths = [dev(np.stack([np.sort(rng.permutation(n)) for _ in range(S)])) for _ in range(steps)]
+    counts = [dev(rng.integers(0, n + 1, S)) for _ in range(steps)]
+    x = [[torch.tensor(rng.standard_normal((S * n, h, 128)), dtype=torch.bfloat16, device="cuda")
+          for h in (Hq, H, H)] for _ in range(steps)]
+    prompt = [torch.tensor(rng.standard_normal((sum(held), H, 128)), dtype=torch.bfloat16, device="cuda")
+              for _ in range(2)]
+    seq = dev(np.repeat(np.arange(S), held))
+    pos = dev(np.concatenate([np.arange(h) for h in held]))
+    lens, none, room, less = dev(held), dev([0] * S), dev([h + n for h in held]), dev(
+        [h // 2 for h in held])
+
+    def run(wait):
+        def done():
+            if wait:
+                torch.cuda.synchronize()
+        c = kv.PagedNVFP4Cache(N, np.zeros((S, P), np.int32), 4096, Hq, H, ROT)
+        c.page_accounts()
+        c.pool.zero_()  # pages taken anew have slots that were never written
+        c.resize(none, lens)
+        c.append(*prompt, seq, pos)
+        c.resize(less, less)
+        c.plan([h + n for h in held], n, causal=False, chunk_tokens=128)
+        buffers = c.tree_buffers(n)
+        mask, seq_ids, slots, positions = buffers
+        q_codes, q_scales = c.quantized_q_buffers(S * n)
+        outs = [torch.empty(S * n, Hq, 128, dtype=torch.bfloat16, device="cuda") for _ in range(steps)]
+        news = [torch.empty(S, dtype=torch.int32, device="cuda") for _ in range(steps)]
+        torch.cuda.synchronize()
+        for i in range(steps):
+            c.resize(lens if i % 3 else less, room)  # what the step before left
+            done()
+            c.tree_mask(parents[i], lens, buffers)
+            done()
+            q, k, v = x[i]
+            c.append(k, v, seq_ids, positions, q=q, q_codes=q_codes, q_scales=q_scales, slots=slots)
+            done()
+            c.attend_tree(q_codes, q_scales, outs[i], mask)
+            done()
+            c.tree_accept(None, None, None, None, lens, paths[i], counts[i], None, news[i])
+            done()
+            if i % 3 == 2:  # pages freed and taken anew, in another order
+                c.resize(less, less)
+                done()
+        torch.cuda.synchronize()
+        assert int(c.status.item()) == 0
+        return outs + news + [c.block_table, c.pool]
+
+    # (rows of fresh pages are what their last holder left: the same in both runs)
+    for i, (a, b) in enumerate(zip(run(True), run(False))):
+        same = bool(torch.equal(a.view(torch.uint8), b.view(torch.uint8)))
+        assert same, i

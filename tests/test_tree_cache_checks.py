@@ -114,3 +114,10 @@ def test_accounts(calls):
         with pytest.raises(ValueError):
             c.fork(*a)
     assert len(calls) == 5
+
+
+def test_accounts_are_emptied_in_place(calls):
+    c = _cache(3)
+    p, copies = c.page_accounts(), c.copies
+    assert c.page_accounts() is p and c.copies is copies  # what a captured resize works on
+    assert calls == ["kv_nvfp4_pages_init"] * 2
