@@ -356,3 +356,33 @@ def test_accept_leaves_rows_of_bad_pages():
     torch.cuda.synchronize()
     assert int(status.item()) == k.DEV_BAD_PAGE
     assert np.array_equal(pool.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("n,Hq,H", [(2, 16, 4), (33, 16, 8)])
+def test_pages_past_32_bits_of_offset(n, Hq, H):
+    """The same pages at the end of a pool of more than 4 GB: the same output, the same rows moved, the
+    same page copied."""
+    k = kv()
+    t = Tree([700, 90], n, 64, Hq, H, seed=5)
+    t.run()
+    t.check()
+    want, few = t.out.clone(), t.cache.num_pages
+    paths = dev([[0] + [0] * (n - 1), list(range(1, n)) + [0]])  # what moves: nothing, all but node 0
+    count, lens = dev([1, n - 1]), dev([700, 90])
+    moved = t.pool.clone().view(few, -1)
+    k.kv_nvfp4_tree_accept(t.layout, None, None, None, None, 2, n, lens, t.table, t.table.shape[1], few,
+                           moved, paths, count, None, None, t.status)
+    far = 2 ** 32 // (9216 * H) + 100
+    pool = torch.empty(far + few, 9216 * H, dtype=torch.uint8, device="cuda")
+    pool[far:] = t.pool.view(few, -1)
+    table = torch.where(t.table >= 0, t.table + far, t.table)
+    t.out.fill_(float("nan"))
+    k.kv_nvfp4_tree_attn(t.layout, t.plan, t.workspace, t.q_codes, t.q_scales, t.mask, SCALE, pool,
+                         far + few, table, table.shape[1], t.out, t.status)
+    assert torch.equal(t.out.view(torch.int16), want.view(torch.int16))
+    k.kv_nvfp4_tree_accept(t.layout, None, None, None, None, 2, n, lens, table, table.shape[1],
+                           far + few, pool, paths, count, None, None, t.status)
+    assert torch.equal(pool[far:], moved) and not torch.equal(moved, t.pool.view(few, -1))
+    k.kv_nvfp4_copy_pages(t.layout, pool, far + few, dev([[far, far - 1], [far + 1, 0]]), 2, t.status)
+    assert torch.equal(pool[far - 1], moved[0]) and torch.equal(pool[0], moved[1])
+    assert int(t.status.item()) == 0
