@@ -68,7 +68,8 @@ struct ForkParams {
 constexpr int kForkThreads = 512;
 
 // One CTA per fork: the row's entries copied, the pages' counts raised. A fork reads only what no fork
-// of the call writes: its own target's count of pages, and its source's, which must not be a target.
+// of the call writes: its own target's count of pages, and its source's, which must not be a target. Bounds:
+// the loads one behind the other and the counts' atomics (8 forks of 1564 pages 4.8 us).
 __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const ForkParams f) {
   const kv_nvfp4_pages& p = f.p;
   const int tid = threadIdx.x, i = blockIdx.x;
@@ -171,7 +172,8 @@ __device__ __forceinline__ uint32_t block_rank(bool v, uint32_t* warp_sums, uint
 
 // A resize of at most one entry per thread, by one CTA: everything stays in registers, and the cluster
 // need not meet. A page that several rows drop is freed by whoever lowers its count to zero, in the
-// place of its last drop, which that thread looks up.
+// place of its last drop, which that thread looks up. Bounds: about ten dependent loads and barriers, 3.5
+// us (4 sessions) to 4.4 (256) of a resize back to back; in the cluster's form below 10 to 12.
 struct FewEntries {
   int32_t top[kResizeThreads];         // the stack from its top on
   int32_t dropped[kResizeThreads];     // page dropped by each entry, or -1
@@ -267,7 +269,9 @@ __device__ __forceinline__ void resize_few(const ResizeParams& r, FewEntries& sh
 // A resize of at most kShareEntries entries per thread of the cluster whose demand the stack meets
 // (else false, with nothing changed): each entry is looked at once and stays in registers. The cluster
 // meets when the counts have been read, when the last drops of pages with several holders are noted
-// (only if there are any), when the freed entries are counted, and before it ends.
+// (only if there are any), when the freed entries are counted, and before it ends. Bounds: these meetings
+// and the loads between them, 9 us for 8192 entries of 4 sessions (12 with every entry looked at in
+// each step, as in the general form below; in a cluster of 4 the same, one CTA by the general form 35).
 constexpr int kShareEntries = 4;
 
 template <class SeqOf, class PlaceOf>
@@ -616,7 +620,8 @@ __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(const Resi
   if (bad != 0) flag_status(r.status, bad);
 }
 
-// One CTA per (pair, KV head's share of the page): every load before the stores.
+// One CTA per (pair, KV head's share of the page): every load before the stores. Bounds: the launch and
+// one round of loads (8 pages of 4 heads 3.5 us).
 constexpr int kPairThreads = 192;
 constexpr int kPairWords = 9216 / 16 / kPairThreads;
 

@@ -39,6 +39,14 @@
 // Two S buffers and two V tiles: the Q.K^T and the dequantisation of block j + 1 run while the
 // softmax and the P.V of block j do.
 //
+// Trees (kTree, kv_nvfp4_tree_attn): a row sees the keys before the step's nodes and the nodes in its
+// mask; bf16 out. 64 nodes over 4 x 131072 tokens (24/4 heads, three tiles of 128 rows per KV head): 316
+// us with its merge, 1.31 PFLOP/s of visible scores and sums, tensor pipe 35 % active. Bound: the steps of
+// a block in the softmax warps (score load, max, exchange, exponentials, stores, hand-over), about 1870
+// cycles of which the exponentials are 750 to 900; more softmax warps, halves of a block handed on
+// separately, blocks taken in turn and scores loaded ahead all measured 2 to 10 % slower. At most 64 rows:
+// 1540 cycles, of which the eight copies of a block take 1100 or more to issue.
+//
 // Warp roles (480 threads): warp 0 bulk-copy producer, warp 1 Q.K^T issuer and tensor-memory
 // owner, warps 2..9 softmax and epilogue (warp w: lane quadrant w mod 4, key half (w - 2) / 4),
 // warps 10..13 V dequantisation, warp 14 P.V issuer. The two MMA issuers sit on different SM
