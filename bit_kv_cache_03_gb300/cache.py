@@ -225,10 +225,13 @@ class PagedNVFP4Cache:
     def page_accounts(self, stream=None):
         """Puts the cache's pages under accounts (self.pages): the block table is emptied and every page
         is free. From then on resize() makes room and frees it, before every append. Called again it
-        empties the accounts that there are, which captured calls work on."""
+        empties the accounts that there are, which captured calls work on. Of several layers one cache
+        has the accounts; the others take its block_table as theirs, and copy pages by its copies."""
         self._check_current()
         new = lambda n: torch.empty(n, dtype=torch.int32, device=self.device)  # noqa: E731
-        if self.pages is None:
+        if self.pages is None or self.pages.block_table != self.block_table.data_ptr():
+            if self.pages is not None:  # another table's accounts: a captured call may work on them
+                self._captured += [self.pages, self.copies]
             with self._on(stream):
                 work = torch.empty(kv_nvfp4_pages_workspace_bytes(self.num_pages), dtype=torch.uint8,
                                    device=self.device)
@@ -240,7 +243,8 @@ class PagedNVFP4Cache:
 
     def fork(self, src, dst, lens, stream=None):
         """Sequences dst[i], which hold no pages, share those of the first lens[i] tokens of src[i]
-        (device int32). The next resize() replaces what a sequence is about to write."""
+        (device int32). The next resize() replaces what a sequence is about to write; evict() writes from
+        a sequence's first slot on and is not for sequences that share pages."""
         self._check_accounted()
         for name, x in (("src", src), ("dst", dst), ("lens", lens)):
             self._int32(name, x, dst.numel())
@@ -287,6 +291,8 @@ class PagedNVFP4Cache:
         self._check_current()
         if self.pages is None:
             raise ValueError("the cache's pages are under no accounts: page_accounts() first")
+        if self.pages.block_table != self.block_table.data_ptr():
+            raise ValueError("the cache's block table is not the one under its accounts")
 
     def _enlarge(self, name, need, stream):
         """Replaces a workspace by one of `need` bytes, from the allocator's memory of the stream that

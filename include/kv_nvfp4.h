@@ -437,7 +437,8 @@ kv_nvfp4_status kv_nvfp4_tree_accept(const kv_nvfp4_layout *layout, const int32_
  * host. One set of accounts serves every layer whose pool has as many pages. Sequences may share pages
  * (kv_nvfp4_pages_fork); kv_nvfp4_pages_resize makes room that is a sequence's own, so every call that
  * writes into the cache has to come behind a resize whose room covers what it writes and whose `keep`
- * covers what has to stay. */
+ * covers what has to stay. An eviction in place writes below `keep`: where pages there are shared it
+ * needs a destination of its own (kv_nvfp4_evict_compact). */
 typedef struct kv_nvfp4_pages {
   int32_t *block_table; /* [num_seqs][max_pages]; -1 from held[s] on */
   int32_t *held;        /* [num_seqs] pages in the sequence's row of the table */

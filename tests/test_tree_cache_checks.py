@@ -121,3 +121,15 @@ def test_accounts_are_emptied_in_place(calls):
     p, copies = c.page_accounts(), c.copies
     assert c.page_accounts() is p and c.copies is copies  # what a captured resize works on
     assert calls == ["kv_nvfp4_pages_init"] * 2
+
+
+def test_accounts_are_of_the_table_in_use(calls):
+    a, b = _cache(3), _cache(3)
+    p = a.page_accounts()
+    b.block_table = a.block_table  # another layer's pool under the same table
+    a.resize(i32(3), i32(3))
+    a.block_table = b.block_table.clone()
+    for call in (lambda: a.resize(i32(3), i32(3)), lambda: a.fork(i32(1), i32(1), i32(1))):
+        with pytest.raises(ValueError, match="block table"):
+            call()
+    assert a.page_accounts() is not p and a.pages.block_table == a.block_table.data_ptr()
