@@ -369,7 +369,8 @@ __device__ __forceinline__ void sum_weights(const WeightParams& p, const Span& s
     for (int i = 0; i < kPair; ++i) {
       const int t = (b + i) * 128 + key;
       real[i] = b + i < sp.b1 && t < sp.len;
-      const int32_t pid = real[i] ? __ldg(bt + t / kPage) : -1;
+      // (a plain load: a kernel that this one was launched beside may have written the table)
+      const int32_t pid = real[i] ? bt[t / kPage] : -1;
       valid[i] = pid >= 0 && pid < p.num_pages;  // a bad page's keys got no weight
       before[i] = real[i] && p.w_in != nullptr ? p.w_in[wrow + t] : 0.f;
       first[i] = p.causal && t > L0 ? (t - L0) * p.G : 0;  // the first row that sees the key
