@@ -20,7 +20,8 @@ namespace {
 
 // The workspace: per page, the call (high word) and the place in its order (low word) of the last
 // drop; per page, the last call that found it shared; per page, a page freed by the call; the calls
-// so far.
+// so far that left such marks. A mark counts if its call is the present one. Numbers are 1 to 2^32 - 1:
+// the call behind the last one clears the marks and is number 1 again.
 struct PagesWork {
   unsigned long long* last_drop;
   uint32_t* shared_in;
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(const Resi
   const PagesWork w = pages_work(p.workspace, p.num_pages);
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const uint32_t call = __ldcg(w.calls) + 1;
+  uint32_t call = __ldcg(w.calls) + 1;
   const int32_t stack = __ldcg(p.free_count);
   const int32_t free_now = stack < 0 ? 0 : stack > p.num_pages ? p.num_pages : stack;
   if (tid == 0) all_taken = 0;
@@ -483,6 +484,15 @@ __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(const Resi
     if (rank == 0) resize_few(r, few, before, need_of, held_of, seq_of, place_of, entries, free_now, bad);
     else cluster_wait();
     return;
+  }
+
+  if (call == 0) {  // the same for every CTA
+    for (int64_t i = rank * kResizeThreads + tid; i < p.num_pages; i += C * kResizeThreads) {
+      w.last_drop[i] = 0;
+      w.shared_in[i] = 0;
+    }
+    cluster_meet();
+    call = 1;
   }
 
   if (entries <= C * (uint32_t)(kResizeThreads * kShareEntries) &&
