@@ -166,7 +166,8 @@ class PagedNVFP4Cache:
         """Fills the buffers of tree_buffers from parents [num_seqs, n]: node i hangs on node
         parents[s, i] < i, or with -1 on the cache; one with any other parent, or below such a one, is
         padding. lens [num_seqs]: tokens in the cache before the tree; first_pos [num_seqs]: the next
-        token's position where it is not the length (behind an eviction)."""
+        token's position where it is not the length (behind an eviction). A sequence with a bad one is
+        refused: its nodes have no slot (-1), so that append skips them."""
         mask, seq_ids, slots, positions = buffers
         n = self._nodes(parents)
         rows = self.num_seqs * n

@@ -48,6 +48,8 @@ __global__ void __launch_bounds__(32 * kWords) tree_mask_kernel(const TreeMaskPa
   int32_t up = i < n ? p.parents[seq * n + i] : -2;
   if (len < 0 || first < 0 || len > 0x7FFFFFFF - n || first > 0x7FFFFFFF - n) {  // for the whole CTA
     if (i == 0) flag_status(p.status, KV_NVFP4_DEV_BAD_POS);
+    if (p.slots != nullptr && i < n)  // no place: what an earlier call left there would be appended again
+      p.seq_ids[seq * n + i] = p.slots[seq * n + i] = p.positions[seq * n + i] = -1;
     return;
   }
   if (up < -1 || up >= i) up = -2;

@@ -368,8 +368,10 @@ kv_nvfp4_status kv_nvfp4_evict_compact(const kv_nvfp4_layout *layout, const int3
  *   d_mask:       DEVICE uint32 [num_seqs][n][ceil(n / 32)]
  *   d_seq_ids, d_slots, d_positions: DEVICE int32 [num_seqs * n], as kv_nvfp4_append_slots takes them;
  *                 or all three null
- * A sequence whose length or position is negative, or passes 31 bits at its last node, sets
- * KV_NVFP4_DEV_BAD_POS and is skipped. One kernel launch. num_seqs = 0 does nothing. */
+ * A sequence whose length or position is negative, or with n added passes 31 bits, sets
+ * KV_NVFP4_DEV_BAD_POS: its nodes' sequence, slot and position are -1, which kv_nvfp4_append_slots refuses
+ * (KV_NVFP4_DEV_BAD_SEQ and BAD_POS) and skips, and its mask is left as it was. One kernel launch.
+ * num_seqs = 0 does nothing. */
 #define KV_NVFP4_MAX_TREE 256
 kv_nvfp4_status kv_nvfp4_tree_mask(const int32_t *d_parents, int32_t num_seqs, int32_t n,
                                    const int32_t *d_lens, const int32_t *d_first_pos,
