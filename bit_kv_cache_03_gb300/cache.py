@@ -207,7 +207,7 @@ class PagedNVFP4Cache:
         [num_seqs]: the token awaited behind the cache), its rows moved behind the cache. Fills path
         [num_seqs, n] up to count, count, next_token and new_lens [num_seqs]; next_token may be
         expected, new_lens lens. parents, draft, target, expected and next_token None: path and count
-        are given (a path chosen another way)."""
+        are given (a path chosen another way). The count of a tree with a bad length is 0."""
         n = self._nodes(path)
         rows = self.num_seqs * n
         for name, x, size in (("parents", parents, rows), ("draft", draft, rows),

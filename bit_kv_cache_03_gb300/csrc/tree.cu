@@ -148,7 +148,10 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const TreeA
     }
   }
   if (__syncthreads_or(bad)) {
-    if (tid == 0) flag_status(p.status, KV_NVFP4_DEV_BAD_POS);
+    if (tid == 0) {
+      flag_status(p.status, KV_NVFP4_DEV_BAD_POS);
+      if (walk) p.count[seq] = 0;  // a further layer's call moves as many rows as it finds here
+    }
     return;
   }
   const int first_page = base / kPage;

@@ -421,7 +421,8 @@ kv_nvfp4_status kv_nvfp4_tree_attn(const kv_nvfp4_layout *layout, const kv_nvfp4
  * With d_parents null (and d_draft, d_target, d_expected, d_next too) d_path and d_count are given: a
  * path that was chosen another way, or the moves of a further layer's pool. A sequence with a negative
  * length, a tree that ends past max_pages * 64 or a given path that does not ascend within [0, n) sets
- * KV_NVFP4_DEV_BAD_POS and is skipped, its outputs left as they were; a row whose old or new page lies
+ * KV_NVFP4_DEV_BAD_POS and is skipped, its outputs left as they were but for the count of a tree that
+ * was to be walked, which is 0 (a further layer's call then moves nothing); a row whose old or new page lies
  * outside the pool sets KV_NVFP4_DEV_BAD_PAGE and is not moved. Pages that the tree's slots lie in must
  * not be shared between sequences (kv_nvfp4_pages_resize sees to it). One kernel launch. num_seqs = 0
  * does nothing. */

@@ -63,3 +63,37 @@ def test_a_refused_mask_appends_nothing(bad, by):
     assert torch.equal(got, c.pool)
     assert torch.equal(got.view(3, 2, -1)[1], before.view(3, 2, -1)[1])
     assert not torch.equal(got, before)
+
+
+def test_a_refused_tree_has_no_accepted_nodes():
+    """The count of a tree that is not walked is 0, not the last step's, which a further layer's call
+    would move rows by."""
+    import evictref
+    k, rng = kv(), np.random.default_rng(1)
+    S, n, H = 4, 6, 2
+    held = [50, 60, 70, 10]
+    cache = treeref.Cache([h + n for h in held], H, 7)
+    P = cache.table.shape[1]
+    lens = np.array([50, -1, P * 64 - n + 1, 10], np.int32)
+    parents = np.tile(np.array([-1, -1, 1, 2, 3, 4], np.int32), (S, 1))
+    ones = np.ones((S, n), np.int32)
+    ones[:, 0] = 2  # not the awaited token: the path is 1, 2, 3, 4, 5
+    path = dev(np.tile(np.array([1, 2, 4, 0, 0, 0]), (S, 1)))
+    count, nxt, new = dev([3] * S), dev([-7] * S), dev([-7] * S)
+    layout, status = k.make_layout(H, H, rot_dim=0), dev([0])
+    args = (S, n, dev(lens), dev(cache.table), P, cache.num_pages)
+    pool, other = dev(cache.pool, torch.uint8), dev(cache.pool, torch.uint8)
+    k.kv_nvfp4_tree_accept(layout, dev(parents), dev(ones), dev(ones), dev([1] * S), *args, pool, path,
+                           count, nxt, new, status)
+    assert int(status.item()) == k.DEV_BAD_POS
+    assert count.tolist() == [5, 0, 0, 5]
+    assert nxt.tolist() == [1, -7, -7, 1] and new.tolist() == [55, -7, -7, 15]
+    assert path[1:3].tolist() == [[1, 2, 4, 0, 0, 0]] * 2
+    want, off = cache.pool.copy(), evictref.row_offsets(H)
+    for s in (0, 3):
+        treeref.move(cache.pool, want, cache.table[s], off, [1, 2, 3, 4, 5], held[s])
+    # a further layer, with lengths that name the sequences' tokens again
+    again = (S, n, dev(held), *args[3:])
+    k.kv_nvfp4_tree_accept(layout, None, None, None, None, *again, other, path, count, None, None, status)
+    for got in (pool, other):
+        assert np.array_equal(got.cpu().numpy(), want)
