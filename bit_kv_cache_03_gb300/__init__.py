@@ -22,7 +22,7 @@ KV_NVFP4_EINVAL = -1
 KV_NVFP4_ECUDA = -2
 KV_NVFP4_ENOSPACE = -3
 DEV_BAD_PAGE, DEV_BAD_POS, DEV_BAD_SEQ, DEV_BAD_ROPE, DEV_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x10
-DEV_NO_PAGE = 0x20
+DEV_NO_PAGE, DEV_SHARED_PAGE = 0x20, 0x40
 MAX_TREE = 256  # KV_NVFP4_MAX_TREE
 MAX_ACCOUNTED_SEQS = 8192  # KV_NVFP4_MAX_ACCOUNTED_SEQS
 NOALLOC_SCRATCH_BYTES = 32 << 20  # KV_NVFP4_NOALLOC_SCRATCH_BYTES
@@ -100,15 +100,18 @@ _SIG = {
                                _P, _I64, _P, _P], _I32),
     "kv_nvfp4_evict_compact": ([ctypes.POINTER(Layout), _P, _I64, _I32, _P, _P, _I32, _P, _I32,
                                 _I32, _P, _P, _I32, _P, _I64, _P, _P], _I32),
-    "kv_nvfp4_tree_mask": ([_P, _I32, _I32, _P, _P, _P, _P, _P, _P, _P, _P], _I32),
+    "kv_nvfp4_tree_mask": ([_P, _I32, _I32, _P, _P, _P, _P, _P, _P, ctypes.POINTER(Pages), _P, _P],
+                           _I32),
     "kv_nvfp4_tree_attn": ([ctypes.POINTER(Layout), ctypes.POINTER(PlanInfo), _P, _P, _P, _P,
                             ctypes.c_float, _P, _I32, _P, _I32, _P, _P, _P], _I32),
     "kv_nvfp4_tree_accept": ([ctypes.POINTER(Layout), _P, _P, _P, _P, _I32, _I32, _P, _P, _I32, _I32,
-                              _P, _P, _P, _P, _P, _P, _P], _I32),
+                              _P, _P, _P, _P, _P, ctypes.POINTER(Pages), _P, _P], _I32),
     "kv_nvfp4_pages_workspace_bytes": ([_I32], ctypes.c_size_t),
     "kv_nvfp4_pages_init": ([ctypes.POINTER(Pages), _P], _I32),
     "kv_nvfp4_pages_fork": ([ctypes.POINTER(Pages), _P, _P, _P, _I32, _P, _P], _I32),
-    "kv_nvfp4_pages_resize": ([ctypes.POINTER(Pages), _P, _P, _P, _P, _P], _I32),
+    "kv_nvfp4_pages_resize": ([ctypes.POINTER(Pages), _P, _P, _P, _P, _P, _P], _I32),
+    "kv_nvfp4_pages_append": ([ctypes.POINTER(Layout), ctypes.POINTER(Pages), _P, _P, _P, _P, _P, _P,
+                               _I32, _P, _I32, _P, _P, _P, _P, _P], _I32),
     "kv_nvfp4_copy_pages": ([ctypes.POINTER(Layout), _P, _I32, _P, _I32, _P, _P], _I32),
     "kv_cmp_page_bytes": ([ctypes.POINTER(Layout), _I32], ctypes.c_size_t),
     "kv_cmp_append": ([ctypes.POINTER(Layout), _I32, _P, _P, _P, _P, _P, _I32, _P, _I32, _P, _I32,
@@ -166,6 +169,10 @@ def _ptr(x) -> int | None:
     if hasattr(x, "ctypes"):
         return x.ctypes.data
     raise TypeError(f"cannot take the address of {type(x)}")
+
+
+def _by_ref(struct):
+    return None if struct is None else ctypes.byref(struct)
 
 
 _current_raw_stream = None  # torch's current stream as an integer, without a Stream object
@@ -354,12 +361,14 @@ def kv_nvfp4_evict_compact(layout, index, index_stride, per_head, seq_lens, keep
 
 
 def kv_nvfp4_tree_mask(parents, num_seqs, n, lens, first_pos, mask, seq_ids=None, slots=None,
-                       positions=None, status=None, stream=None):
+                       positions=None, status=None, stream=None, pages: Pages | None = None):
     """Masks of drafted trees from their parents, with each node's sequence, slot and position as
-    kv_nvfp4_append_slots takes them (first_pos None: the position is counted from the length)."""
+    kv_nvfp4_append_slots takes them (first_pos None: the position is counted from the length); -1 for
+    a sequence that is refused, as is, with `pages`, one whose slots lie in pages that others hold."""
     _check(lib().kv_nvfp4_tree_mask(
         _ptr(parents), num_seqs, n, _ptr(lens), _ptr(first_pos), _ptr(mask), _ptr(seq_ids),
-        _ptr(slots), _ptr(positions), _ptr(status), _stream(stream)), "kv_nvfp4_tree_mask")
+        _ptr(slots), _ptr(positions), _by_ref(pages), _ptr(status), _stream(stream)),
+        "kv_nvfp4_tree_mask")
 
 
 def kv_nvfp4_tree_attn(layout, plan: PlanInfo, workspace, q_codes, q_scales, mask, sm_scale, pool,
@@ -373,13 +382,15 @@ def kv_nvfp4_tree_attn(layout, plan: PlanInfo, workspace, q_codes, q_scales, mas
 
 def kv_nvfp4_tree_accept(layout, parents, draft, target, expected, num_seqs, n, lens, block_table,
                          max_pages, num_pages, pool, path, count, next_token, new_lens=None,
-                         status=None, stream=None):
+                         status=None, stream=None, pages: Pages | None = None):
     """The path that the model agrees with, and its rows moved behind the cache (pool None: not
-    moved; parents, draft, target, expected, next_token None: path and count are given)."""
+    moved; parents, draft, target, expected, next_token None: path and count are given). With `pages`
+    nothing is accepted of a tree whose slots lie in pages that other sequences hold."""
     _check(lib().kv_nvfp4_tree_accept(
         ctypes.byref(layout), _ptr(parents), _ptr(draft), _ptr(target), _ptr(expected), num_seqs, n,
         _ptr(lens), _ptr(block_table), max_pages, num_pages, _ptr(pool), _ptr(path), _ptr(count),
-        _ptr(next_token), _ptr(new_lens), _ptr(status), _stream(stream)), "kv_nvfp4_tree_accept")
+        _ptr(next_token), _ptr(new_lens), _by_ref(pages), _ptr(status), _stream(stream)),
+        "kv_nvfp4_tree_accept")
 
 
 def kv_nvfp4_pages_workspace_bytes(num_pages) -> int:
@@ -415,12 +426,23 @@ def kv_nvfp4_pages_fork(pages: Pages, src, dst, lens, n, status=None, stream=Non
                                      _ptr(status), _stream(stream)), "kv_nvfp4_pages_fork")
 
 
-def kv_nvfp4_pages_resize(pages: Pages, keep_lens, new_lens, copies, status=None, stream=None):
+def kv_nvfp4_pages_resize(pages: Pages, keep_lens, new_lens, copies, status=None, stream=None,
+                          kept=None):
     """Room for new_lens tokens of each sequence, of which keep_lens stay; copies receives the page
-    pairs for kv_nvfp4_copy_pages."""
+    pairs for kv_nvfp4_copy_pages, kept (or None) keep_lens, with -1 for a sequence that is refused."""
     _check(lib().kv_nvfp4_pages_resize(ctypes.byref(pages), _ptr(keep_lens), _ptr(new_lens),
-                                       _ptr(copies), _ptr(status), _stream(stream)),
+                                       _ptr(copies), _ptr(kept), _ptr(status), _stream(stream)),
            "kv_nvfp4_pages_resize")
+
+
+def kv_nvfp4_pages_append(layout, pages: Pages, q, k, v, seq_ids, slots, positions, T, rope_table,
+                          rope_max_pos, pool, q_codes=None, q_scales=None, status=None, stream=None):
+    """kv_nvfp4_append_slots (slots None: the positions) into the pages under the accounts: a row that
+    belongs into a page with more than one holder is not written."""
+    _check(lib().kv_nvfp4_pages_append(
+        ctypes.byref(layout), ctypes.byref(pages), _ptr(q), _ptr(k), _ptr(v), _ptr(seq_ids), _ptr(slots),
+        _ptr(positions), T, _ptr(rope_table), rope_max_pos, _ptr(pool), _ptr(q_codes), _ptr(q_scales),
+        _ptr(status), _stream(stream)), "kv_nvfp4_pages_append")
 
 
 def kv_nvfp4_copy_pages(layout, pool, num_pages, pairs, n, status=None, stream=None):

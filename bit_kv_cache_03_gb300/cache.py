@@ -12,11 +12,11 @@ import torch
 from . import (MAX_TREE, _capturing, kv_nvfp4_append, kv_nvfp4_append_slots, kv_nvfp4_copy_pages,
                kv_nvfp4_decode_attn, kv_nvfp4_decode_attn_weights, kv_nvfp4_decode_step,
                kv_nvfp4_decode_step_host, kv_nvfp4_evict_compact, kv_nvfp4_evict_select,
-               kv_nvfp4_pages_fork, kv_nvfp4_pages_init, kv_nvfp4_pages_resize,
-               kv_nvfp4_pages_workspace_bytes, kv_nvfp4_plan, kv_nvfp4_plan_workspace_bytes,
-               kv_nvfp4_pool_bytes, kv_nvfp4_rope_table_init, kv_nvfp4_tree_accept,
-               kv_nvfp4_tree_attn, kv_nvfp4_tree_mask, kv_nvfp4_weights_workspace_bytes, make_layout,
-               make_pages)
+               kv_nvfp4_pages_append, kv_nvfp4_pages_fork, kv_nvfp4_pages_init,
+               kv_nvfp4_pages_resize, kv_nvfp4_pages_workspace_bytes, kv_nvfp4_plan,
+               kv_nvfp4_plan_workspace_bytes, kv_nvfp4_pool_bytes, kv_nvfp4_rope_table_init,
+               kv_nvfp4_tree_accept, kv_nvfp4_tree_attn, kv_nvfp4_tree_mask,
+               kv_nvfp4_weights_workspace_bytes, make_layout, make_pages)
 
 
 class PagedNVFP4Cache:
@@ -49,13 +49,19 @@ class PagedNVFP4Cache:
     def append(self, k, v, seq_ids, positions, q=None, q_codes=None, q_scales=None, stream=None,
                slots=None):
         """slots: int32 cache slots of the tokens where they differ from the positions (behind an
-        eviction)."""
+        eviction). Under accounts rows into pages that several sequences hold are not written."""
         T = int(k.shape[0])
         if slots is not None:
             self._check_current()
             if slots.dtype != torch.int32 or not slots.is_contiguous() or slots.numel() != T or \
                     slots.device != self.pool.device:
                 raise ValueError("slots must be device int32, one per token")
+        pages = self._accounts()
+        if pages is not None:
+            kv_nvfp4_pages_append(self.layout, pages, q, k, v, seq_ids, slots, positions, T, self.rope,
+                                  self.max_pos, self.pool, q_codes, q_scales, self.status, stream)
+            return
+        if slots is not None:
             kv_nvfp4_append_slots(self.layout, q, k, v, seq_ids, slots, positions, T, self.rope,
                                   self.max_pos, self.block_table, self.num_seqs, self.max_pages,
                                   self.num_pages, self.pool, q_codes, q_scales, self.status, stream)
@@ -167,7 +173,8 @@ class PagedNVFP4Cache:
         parents[s, i] < i, or with -1 on the cache; one with any other parent, or below such a one, is
         padding. lens [num_seqs]: tokens in the cache before the tree; first_pos [num_seqs]: the next
         token's position where it is not the length (behind an eviction). A sequence with a bad one is
-        refused: its nodes have no slot (-1), so that append skips them."""
+        refused, and one whose slots lie in pages that others hold (under accounts; a resize that was
+        refused): its nodes have no slot (-1), so that append skips them."""
         mask, seq_ids, slots, positions = buffers
         n = self._nodes(parents)
         rows = self.num_seqs * n
@@ -179,7 +186,7 @@ class PagedNVFP4Cache:
         if first_pos is not None:
             self._int32("first_pos", first_pos, self.num_seqs)
         kv_nvfp4_tree_mask(parents, self.num_seqs, n, lens, first_pos, mask, seq_ids, slots, positions,
-                           self.status, stream)
+                           self.status, stream, self._accounts())
 
     def attend_tree(self, q_codes, q_scales, out, mask, sm_scale=None, stream=None):
         """Attention of the tree's nodes, the last q_len tokens of every sequence of the last plan()
@@ -207,7 +214,8 @@ class PagedNVFP4Cache:
         [num_seqs]: the token awaited behind the cache), its rows moved behind the cache. Fills path
         [num_seqs, n] up to count, count, next_token and new_lens [num_seqs]; next_token may be
         expected, new_lens lens. parents, draft, target, expected and next_token None: path and count
-        are given (a path chosen another way). The count of a tree with a bad length is 0."""
+        are given (a path chosen another way). The count of a tree with a bad length is 0, and nothing is
+        accepted of one in pages that other sequences hold (under accounts)."""
         n = self._nodes(path)
         rows = self.num_seqs * n
         for name, x, size in (("parents", parents, rows), ("draft", draft, rows),
@@ -220,23 +228,25 @@ class PagedNVFP4Cache:
                 self._int32(name, x, size)
         kv_nvfp4_tree_accept(self.layout, parents, draft, target, expected, self.num_seqs, n, lens,
                              self.block_table, self.max_pages, self.num_pages, self.pool, path, count,
-                             next_token, new_lens, self.status, stream)
+                             next_token, new_lens, self.status, stream, self._accounts())
 
     # -- pages that sequences take, share and give back ---------------------------------------------
     def page_accounts(self, stream=None):
         """Puts the cache's pages under accounts (self.pages): the block table is emptied and every page
         is free. From then on resize() makes room and frees it, before every append. Called again it
         empties the accounts that there are, which captured calls work on. Of several layers one cache
-        has the accounts; the others take its block_table as theirs, and copy pages by its copies."""
+        has the accounts; the others take its block_table and pages as theirs, and copy pages by its
+        copies."""
         self._check_current()
         new = lambda n: torch.empty(n, dtype=torch.int32, device=self.device)  # noqa: E731
         if self.pages is None or self.pages.block_table != self.block_table.data_ptr():
             if self.pages is not None:  # another table's accounts: a captured call may work on them
-                self._captured += [self.pages, self.copies]
+                self._captured += [self.pages, self.copies, self.kept]
             with self._on(stream):
                 work = torch.empty(kv_nvfp4_pages_workspace_bytes(self.num_pages), dtype=torch.uint8,
                                    device=self.device)
                 self.copies = torch.full((self.num_seqs, 2), -1, dtype=torch.int32, device=self.device)
+                self.kept = torch.zeros(self.num_seqs, dtype=torch.int32, device=self.device)
                 self.pages = make_pages(self.block_table, new(self.num_seqs), new(self.num_pages),
                                         new(self.num_pages), new(1), work)
         kv_nvfp4_pages_init(self.pages, stream)
@@ -257,11 +267,15 @@ class PagedNVFP4Cache:
         """Room for new_lens tokens of every sequence, of which the first keep_lens stay (device int32
         [num_seqs]); both 0 end a sequence. Shared pages that are to be written are replaced, and with
         `copy` the kept tokens in them copied; else self.copies says which (several layers' pools under
-        one cache's accounts: kv_nvfp4_copy_pages on each)."""
+        one cache's accounts: kv_nvfp4_copy_pages on each). self.kept holds keep_lens, or -1 where a
+        sequence is refused and stays as it was, maybe with shared pages where it is to be written.
+        append, tree_mask and tree_accept leave those as they are; decode_step does not look, and is for
+        plans all of whose sequences were served."""
         self._check_accounted()
         self._int32("keep_lens", keep_lens, self.num_seqs)
         self._int32("new_lens", new_lens, self.num_seqs)
-        kv_nvfp4_pages_resize(self.pages, keep_lens, new_lens, self.copies, self.status, stream)
+        kv_nvfp4_pages_resize(self.pages, keep_lens, new_lens, self.copies, self.status, stream,
+                              self.kept)
         if copy:
             kv_nvfp4_copy_pages(self.layout, self.pool, self.num_pages, self.copies, self.num_seqs,
                                 self.status, stream)
@@ -294,6 +308,15 @@ class PagedNVFP4Cache:
             raise ValueError("the cache's pages are under no accounts: page_accounts() first")
         if self.pages.block_table != self.block_table.data_ptr():
             raise ValueError("the cache's block table is not the one under its accounts")
+
+    def _accounts(self):
+        """The accounts that the block table is under (another layer's cache may have them), or None."""
+        p = self.pages
+        if p is None or p.block_table != self.block_table.data_ptr():
+            return None
+        if (p.num_seqs, p.max_pages, p.num_pages) != (self.num_seqs, self.max_pages, self.num_pages):
+            raise ValueError("the accounts are not of as many sequences and pages as the cache has")
+        return p
 
     def _enlarge(self, name, need, stream):
         """Replaces a workspace by one of `need` bytes, from the allocator's memory of the stream that
@@ -339,7 +362,8 @@ class PagedNVFP4Cache:
     def decode_step(self, q, k, v, out, q_codes=None, q_scales=None, sm_scale=None, stream=None):
         """New tokens of every sequence (sequence-major rows, at the last q_len positions of the
         lengths given to the last plan) appended and attended in one kernel launch. The positions are
-        the slots too: not for a cache that evict() compacted, whose tokens have other positions."""
+        the slots too: not for a cache that evict() compacted, whose tokens have other positions. Every
+        sequence of the plan is written: under accounts all have to be ones that resize() served."""
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(128)
         self._hold_captured(stream)

@@ -17,8 +17,8 @@ cudaError_t launch_append(const uint16_t* q, const uint16_t* k, const uint16_t* 
                           int64_t T, const float* rope, int32_t rope_max_pos, int32_t rot_dim,
                           const int32_t* block_table, int32_t num_seqs, int32_t max_pages,
                           int32_t num_pages, uint8_t* pool, uint8_t* q_codes,
-                          uint8_t* q_scales, int32_t Hq, int32_t Hkv, int32_t* status,
-                          int32_t num_sms, cudaStream_t stream);
+                          uint8_t* q_scales, int32_t Hq, int32_t Hkv, const int32_t* refs,
+                          int32_t* status, int32_t num_sms, cudaStream_t stream);
 cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const uint8_t* pool,
                           const int32_t* block_table, int32_t max_pages, int32_t num_pages,
                           const void* groups, const void* segments, const int32_t* cta_seg,
@@ -92,21 +92,22 @@ cudaError_t launch_step_inputs(const void* const src[3], void* const dst[3],
 int inline_plan_bytes();
 cudaError_t launch_tree_mask(const int32_t* parents, int32_t num_seqs, int32_t n,
                              const int32_t* lens, const int32_t* first_pos, uint32_t* mask,
-                             int32_t* seq_ids, int32_t* slots, int32_t* positions, int32_t* status,
-                             cudaStream_t stream);
+                             int32_t* seq_ids, int32_t* slots, int32_t* positions,
+                             const kv_nvfp4_pages* pages, int32_t* status, cudaStream_t stream);
 cudaError_t launch_tree_accept(const int32_t* parents, const int32_t* draft, const int32_t* target,
                                const int32_t* expected, int32_t num_seqs, int32_t n,
                                const int32_t* lens, const int32_t* block_table, int32_t max_pages,
                                int32_t num_pages, uint8_t* pool, int32_t* path, int32_t* count,
-                               int32_t* next, int32_t* new_lens, int32_t Hkv, int32_t* status,
-                               cudaStream_t stream);
+                               int32_t* next, int32_t* new_lens, const kv_nvfp4_pages* pages,
+                               int32_t Hkv, int32_t* status, cudaStream_t stream);
 uint64_t pages_workspace_bytes(int32_t num_pages);
 cudaError_t launch_pages_init(const kv_nvfp4_pages* p, int32_t num_sms, cudaStream_t stream);
 cudaError_t launch_pages_fork(const kv_nvfp4_pages* p, const int32_t* src, const int32_t* dst,
                               const int32_t* lens, int32_t n, int32_t* status,
                               cudaStream_t stream);
 cudaError_t launch_pages_resize(const kv_nvfp4_pages* p, const int32_t* keep, const int32_t* room,
-                                int32_t* copies, int32_t* status, cudaStream_t stream);
+                                int32_t* copies, int32_t* kept, int32_t* status,
+                                cudaStream_t stream);
 cudaError_t launch_copy_pages(uint8_t* pool, const int32_t* pairs, int32_t n, int32_t num_pages,
                               int32_t Hkv, int32_t num_sms, int32_t* status, cudaStream_t stream);
 }  // namespace kvnvfp4
@@ -517,15 +518,15 @@ static kv_nvfp4_status decode_step_impl(const kv_nvfp4_layout* L, const kv_nvfp4
   return cuda_status(e);
 }
 
-// The append; d_slots null: every token's slot is its position.
+// The append; d_slots null: every token's slot is its position; refs null: pages are not under accounts.
 static kv_nvfp4_status append_impl(const kv_nvfp4_layout* L, const void* q, const void* k,
                                    const void* v, const int32_t* d_seq_ids, const int32_t* d_slots,
                                    const int32_t* d_positions, int32_t T,
                                    const float* d_rope_table, int32_t rope_max_pos,
                                    const int32_t* d_block_table, int32_t num_seqs,
                                    int32_t max_pages, int32_t num_pages, uint8_t* pool,
-                                   uint8_t* q_codes, uint8_t* q_scales, int32_t* d_status,
-                                   void* stream) {
+                                   uint8_t* q_codes, uint8_t* q_scales, const int32_t* refs,
+                                   int32_t* d_status, void* stream) {
   if (kv_nvfp4_layout_check(L) != KV_NVFP4_OK) return KV_NVFP4_EINVAL;
   if (T < 0 || num_seqs <= 0 || max_pages <= 0 || num_pages <= 0) return KV_NVFP4_EINVAL;
   if (T == 0) return KV_NVFP4_OK;
@@ -538,7 +539,7 @@ static kv_nvfp4_status append_impl(const kv_nvfp4_layout* L, const void* q, cons
   const cudaError_t e = kvnvfp4::launch_append(
       (const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, d_seq_ids, d_positions, d_slots, T,
       d_rope_table, rope_max_pos, L->rot_dim, d_block_table, num_seqs, max_pages, num_pages,
-      pool, q_codes, q_scales, L->num_q_heads, L->num_kv_heads,
+      pool, q_codes, q_scales, L->num_q_heads, L->num_kv_heads, refs,
       d_status, num_sms_current_device(), (cudaStream_t)stream);
   return cuda_status(e);
 }
@@ -688,7 +689,7 @@ kv_nvfp4_status kv_nvfp4_append(const kv_nvfp4_layout* L, const void* q, const v
                                 int32_t* d_status, void* stream) {
   return append_impl(L, q, k, v, d_seq_ids, nullptr, d_positions, T, d_rope_table, rope_max_pos,
                      d_block_table, num_seqs, max_pages, num_pages, pool, q_codes, q_scales,
-                     d_status, stream);
+                     nullptr, d_status, stream);
 }
 
 kv_nvfp4_status kv_nvfp4_append_slots(const kv_nvfp4_layout* L, const void* q, const void* k,
@@ -702,7 +703,7 @@ kv_nvfp4_status kv_nvfp4_append_slots(const kv_nvfp4_layout* L, const void* q, c
   if (T > 0 && d_slots == nullptr) return KV_NVFP4_EINVAL;
   return append_impl(L, q, k, v, d_seq_ids, d_slots, d_positions, T, d_rope_table, rope_max_pos,
                      d_block_table, num_seqs, max_pages, num_pages, pool, q_codes, q_scales,
-                     d_status, stream);
+                     nullptr, d_status, stream);
 }
 
 kv_nvfp4_status kv_nvfp4_plan_workspace_bytes(const kv_nvfp4_layout* L, const int32_t* h_seq_lens,
@@ -925,9 +926,11 @@ kv_nvfp4_status kv_nvfp4_evict_compact(const kv_nvfp4_layout* L, const int32_t* 
 kv_nvfp4_status kv_nvfp4_tree_mask(const int32_t* d_parents, int32_t num_seqs, int32_t n,
                                    const int32_t* d_lens, const int32_t* d_first_pos,
                                    uint32_t* d_mask, int32_t* d_seq_ids, int32_t* d_slots,
-                                   int32_t* d_positions, int32_t* d_status, void* stream) {
+                                   int32_t* d_positions, const kv_nvfp4_pages* pages,
+                                   int32_t* d_status, void* stream) {
   if (num_seqs < 0 || n < 1 || n > KV_NVFP4_MAX_TREE) return KV_NVFP4_EINVAL;
   if (num_seqs == 0) return KV_NVFP4_OK;
+  if (pages != nullptr && (!pages_valid(pages) || num_seqs > pages->num_seqs)) return KV_NVFP4_EINVAL;
   if (!d_parents || !d_lens || !d_mask) return KV_NVFP4_EINVAL;
   const bool some = d_seq_ids || d_slots || d_positions;
   if (some && !(d_seq_ids && d_slots && d_positions)) return KV_NVFP4_EINVAL;
@@ -935,7 +938,7 @@ kv_nvfp4_status kv_nvfp4_tree_mask(const int32_t* d_parents, int32_t num_seqs, i
   for (const void* p : words)
     if (!aligned4(p)) return KV_NVFP4_EINVAL;
   return cuda_status(kvnvfp4::launch_tree_mask(d_parents, num_seqs, n, d_lens, d_first_pos, d_mask,
-                                               d_seq_ids, d_slots, d_positions, d_status,
+                                               d_seq_ids, d_slots, d_positions, pages, d_status,
                                                (cudaStream_t)stream));
 }
 
@@ -981,10 +984,12 @@ kv_nvfp4_status kv_nvfp4_tree_accept(const kv_nvfp4_layout* L, const int32_t* d_
                                      const int32_t* d_lens, const int32_t* d_block_table,
                                      int32_t max_pages, int32_t num_pages, uint8_t* pool,
                                      int32_t* d_path, int32_t* d_count, int32_t* d_next,
-                                     int32_t* d_new_lens, int32_t* d_status, void* stream) {
+                                     int32_t* d_new_lens, const kv_nvfp4_pages* pages,
+                                     int32_t* d_status, void* stream) {
   if (kv_nvfp4_layout_check(L) != KV_NVFP4_OK || num_seqs < 0 || n < 1 || n > KV_NVFP4_MAX_TREE)
     return KV_NVFP4_EINVAL;
   if (num_seqs == 0) return KV_NVFP4_OK;
+  if (pages != nullptr && (!pages_valid(pages) || num_seqs > pages->num_seqs)) return KV_NVFP4_EINVAL;
   if (!d_lens || !d_path || !d_count) return KV_NVFP4_EINVAL;
   const bool walk = d_parents != nullptr;
   if ((d_draft != nullptr) != walk || (d_target != nullptr) != walk ||
@@ -1000,7 +1005,7 @@ kv_nvfp4_status kv_nvfp4_tree_accept(const kv_nvfp4_layout* L, const int32_t* d_
     if (!aligned4(p)) return KV_NVFP4_EINVAL;
   return cuda_status(kvnvfp4::launch_tree_accept(
       d_parents, d_draft, d_target, d_expected, num_seqs, n, d_lens, d_block_table, max_pages,
-      num_pages, pool, d_path, d_count, d_next, d_new_lens, L->num_kv_heads, d_status,
+      num_pages, pool, d_path, d_count, d_next, d_new_lens, pages, L->num_kv_heads, d_status,
       (cudaStream_t)stream));
 }
 
@@ -1028,13 +1033,26 @@ kv_nvfp4_status kv_nvfp4_pages_fork(const kv_nvfp4_pages* pages, const int32_t* 
 }
 
 kv_nvfp4_status kv_nvfp4_pages_resize(const kv_nvfp4_pages* pages, const int32_t* d_keep_lens,
-                                      const int32_t* d_new_lens, int32_t* d_copies,
+                                      const int32_t* d_new_lens, int32_t* d_copies, int32_t* d_kept,
                                       int32_t* d_status, void* stream) {
   if (!pages_valid(pages) || !d_keep_lens || !d_new_lens || !d_copies) return KV_NVFP4_EINVAL;
-  if (!aligned4(d_keep_lens) || !aligned4(d_new_lens) || !aligned4(d_copies))
+  if (!aligned4(d_keep_lens) || !aligned4(d_new_lens) || !aligned4(d_copies) || !aligned4(d_kept))
     return KV_NVFP4_EINVAL;
-  return cuda_status(kvnvfp4::launch_pages_resize(pages, d_keep_lens, d_new_lens, d_copies,
+  return cuda_status(kvnvfp4::launch_pages_resize(pages, d_keep_lens, d_new_lens, d_copies, d_kept,
                                                   d_status, (cudaStream_t)stream));
+}
+
+kv_nvfp4_status kv_nvfp4_pages_append(const kv_nvfp4_layout* L, const kv_nvfp4_pages* pages,
+                                      const void* q, const void* k, const void* v,
+                                      const int32_t* d_seq_ids, const int32_t* d_slots,
+                                      const int32_t* d_positions, int32_t T,
+                                      const float* d_rope_table, int32_t rope_max_pos, uint8_t* pool,
+                                      uint8_t* q_codes, uint8_t* q_scales, int32_t* d_status,
+                                      void* stream) {
+  if (!pages_valid(pages)) return KV_NVFP4_EINVAL;
+  return append_impl(L, q, k, v, d_seq_ids, d_slots, d_positions, T, d_rope_table, rope_max_pos,
+                     pages->block_table, pages->num_seqs, pages->max_pages, pages->num_pages, pool,
+                     q_codes, q_scales, pages->refs, d_status, stream);
 }
 
 kv_nvfp4_status kv_nvfp4_copy_pages(const kv_nvfp4_layout* L, uint8_t* pool, int32_t num_pages,

@@ -58,6 +58,7 @@ struct AppendParams {
   int32_t Hq;            // 0 when q is absent
   int32_t Hkv;
   int32_t* status;
+  const int32_t* refs;   // [num_pages] rows of the table that hold a page, or null
 };
 
 // Where one row goes. kind: 0 = nothing to do (padding row, or a row flagged and skipped),
@@ -75,7 +76,8 @@ static_assert(sizeof(RowMeta) == 32, "metadata slot");
 // Resolves row w (Q heads, then K heads, then V heads) of token t: source row and destination,
 // with the checks and status bits of the call's definition (a bad sequence id, position or slot skips
 // every row of the token; a bad page skips the K/V row; a rotated row past the RoPE table is
-// skipped). Status bits are set only when `report` (one caller per row).
+// skipped; so is, where `refs` are given, a K/V row whose page several rows of the table hold). Status
+// bits are set only when `report` (one caller per row).
 __device__ __forceinline__ const uint16_t* locate_row(const AppendParams& p, int32_t t, int32_t w,
                                                       bool report, RowMeta& m) {
   m.codes = nullptr; m.scales = nullptr; m.hi_step = 4; m.code_step = 16; m.pos = 0; m.kind = 0;
@@ -109,6 +111,10 @@ __device__ __forceinline__ const uint16_t* locate_row(const AppendParams& p, int
     const int32_t page = p.block_table[(int64_t)seq * p.max_pages + slot / kPage];
     if (page < 0 || page >= p.num_pages) {
       if (report) flag_status(p.status, KV_NVFP4_DEV_BAD_PAGE);
+      return nullptr;
+    }
+    if (p.refs != nullptr && p.refs[page] > 1) {
+      if (report) flag_status(p.status, KV_NVFP4_DEV_SHARED_PAGE);
       return nullptr;
     }
     // page block: [K codes H*4096 (tile order)][K scales H*512 (scale-copy order)][V codes
@@ -434,8 +440,8 @@ cudaError_t launch_append(const uint16_t* q, const uint16_t* k, const uint16_t* 
                           int64_t T, const float* rope, int32_t rope_max_pos, int32_t rot_dim,
                           const int32_t* block_table, int32_t num_seqs, int32_t max_pages,
                           int32_t num_pages, uint8_t* pool, uint8_t* q_codes,
-                          uint8_t* q_scales, int32_t Hq, int32_t Hkv, int32_t* status,
-                          int32_t num_sms, cudaStream_t stream) {
+                          uint8_t* q_scales, int32_t Hq, int32_t Hkv, const int32_t* refs,
+                          int32_t* status, int32_t num_sms, cudaStream_t stream) {
   static bool attr_done[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
@@ -474,7 +480,8 @@ cudaError_t launch_append(const uint16_t* q, const uint16_t* k, const uint16_t* 
                    q ? q_scales + t0 * Hq * kScaleBytes : nullptr,
                    hq,
                    Hkv,
-                   status};
+                   status,
+                   refs};
     const int64_t rows = n * per_tok;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;

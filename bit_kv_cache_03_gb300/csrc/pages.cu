@@ -112,6 +112,7 @@ struct ResizeParams {
   const int32_t* keep;   // [num_seqs]
   const int32_t* room;   // [num_seqs]
   int32_t* copies;       // [num_seqs][2]
+  int32_t* kept;         // [num_seqs] keep, or -1 for a refused sequence; or null
   int32_t* status;
 };
 
@@ -268,8 +269,13 @@ __device__ __forceinline__ void resize_few(const ResizeParams& r, FewEntries& sh
     }
     p.block_table[(int64_t)s * p.max_pages + j] = fresh;
   }
-  for (int q = tid; q < S; q += kResizeThreads)
-    if (held_of[q] != need_of[q] && met(q, upto)) p.held[q] = need_of[q];
+  for (int q = tid; q < S; q += kResizeThreads) {
+    if (!met(q, upto)) {
+      if (r.kept != nullptr) r.kept[q] = -1;
+    } else if (held_of[q] != need_of[q]) {
+      p.held[q] = need_of[q];
+    }
+  }
   if (tid == 0) *p.free_count = (int32_t)min(left + all_freed, (uint32_t)p.num_pages);
   if (bad != 0) flag_status(r.status, bad);
 }
@@ -452,7 +458,10 @@ __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(const Resi
       need_of[s] = ok ? need : 0;
       held_of[s] = ok ? held : 0;
       demand[s] = ok ? max(0, need - held) : 0;
-      if (rank == 0) r.copies[2 * s] = r.copies[2 * s + 1] = -1;
+      if (rank == 0) {
+        r.copies[2 * s] = r.copies[2 * s + 1] = -1;
+        if (r.kept != nullptr) r.kept[s] = ok ? keep : -1;  // (who gets pages is found out below)
+      }
     }
     uint32_t sum;
     const uint32_t at = block_scan(n, warp_sums, sum);
@@ -522,7 +531,10 @@ __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(const Resi
     const uint32_t upto = wanted + block_scan(d, warp_sums, sum) + d;
     const bool ok = d == 0 || upto <= (uint32_t)free_now;
     if (s < S) {
-      if (!ok) bad |= KV_NVFP4_DEV_NO_PAGE;
+      if (!ok) {
+        bad |= KV_NVFP4_DEV_NO_PAGE;
+        if (rank == 0 && r.kept != nullptr) r.kept[s] = -1;
+      }
       if (ok && d > 0) atomicMax(&all_taken, upto);
       demand[s] = ok;
     }
@@ -711,7 +723,8 @@ cudaError_t launch_pages_fork(const kv_nvfp4_pages* p, const int32_t* src, const
 }
 
 cudaError_t launch_pages_resize(const kv_nvfp4_pages* p, const int32_t* keep, const int32_t* room,
-                                int32_t* copies, int32_t* status, cudaStream_t stream) {
+                                int32_t* copies, int32_t* kept, int32_t* status,
+                                cudaStream_t stream) {
   static bool attr_done[64] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return cudaGetLastError();
@@ -722,7 +735,7 @@ cudaError_t launch_pages_resize(const kv_nvfp4_pages* p, const int32_t* keep, co
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_done[dev] = true;
   }
-  ResizeParams r{*p, keep, room, copies, status};
+  ResizeParams r{*p, keep, room, copies, kept, status};
   void* args[] = {&r};
   // the lengths are on the device: sized for the most entries that the table has
   int C = 1;

@@ -15,6 +15,23 @@ namespace {
 
 constexpr int kMaxNodes = KV_NVFP4_MAX_TREE;
 constexpr int kMaxWords = kMaxNodes / 32;
+constexpr int kTreePages = kMaxNodes / kPage + 1;  // pages that a tree's slots can touch
+
+// The accounts that the block table is under (refs null: none).
+struct Accounts {
+  const int32_t* block_table;  // [.][max_pages]
+  const int32_t* refs;         // [num_pages]
+  int32_t max_pages, num_pages;
+};
+
+// Whether the j-th page from the one of slot `base` on is another sequence's as well and takes one of n
+// slots from there.
+__device__ __forceinline__ bool shared_page(const Accounts& a, int64_t seq, int32_t base, int n, int j) {
+  const int64_t place = base / kPage + j;
+  if (place * kPage >= (int64_t)base + n || place >= a.max_pages) return false;
+  const int32_t page = a.block_table[seq * a.max_pages + place];
+  return page >= 0 && page < a.num_pages && a.refs[page] > 1;
+}
 
 struct TreeMaskParams {
   const int32_t* parents;    // [num_seqs][n]
@@ -24,6 +41,7 @@ struct TreeMaskParams {
   int32_t* seq_ids;          // [num_seqs * n], as the next two, or all null
   int32_t* slots;
   int32_t* positions;
+  Accounts accounts;
   int32_t n;
   int32_t* status;
 };
@@ -46,12 +64,18 @@ __global__ void __launch_bounds__(32 * kWords) tree_mask_kernel(const TreeMaskPa
   const int32_t len = p.lens[seq];
   const int32_t first = p.first_pos != nullptr ? p.first_pos[seq] : len;
   int32_t up = i < n ? p.parents[seq * n + i] : -2;
+  auto no_place = [&]() {  // what an earlier call left there would be appended again
+    if (p.slots != nullptr && i < n)
+      p.seq_ids[seq * n + i] = p.slots[seq * n + i] = p.positions[seq * n + i] = -1;
+  };
   if (len < 0 || first < 0 || len > 0x7FFFFFFF - n || first > 0x7FFFFFFF - n) {  // for the whole CTA
     if (i == 0) flag_status(p.status, KV_NVFP4_DEV_BAD_POS);
-    if (p.slots != nullptr && i < n)  // no place: what an earlier call left there would be appended again
-      p.seq_ids[seq * n + i] = p.slots[seq * n + i] = p.positions[seq * n + i] = -1;
+    no_place();
     return;
   }
+  // (a thread per page: there are at least 32)
+  const bool shared = p.accounts.refs != nullptr && i < kTreePages &&
+                      shared_page(p.accounts, seq, len, n, i);
   if (up < -1 || up >= i) up = -2;
   uint32_t set[kWords];
 #pragma unroll
@@ -76,7 +100,11 @@ __global__ void __launch_bounds__(32 * kWords) tree_mask_kernel(const TreeMaskPa
     depth += __popc(set[w]);
     sets[w][i] = set[w];
   }
-  __syncthreads();
+  if (__syncthreads_or(shared)) {
+    if (i == 0) flag_status(p.status, KV_NVFP4_DEV_SHARED_PAGE);
+    no_place();
+    return;
+  }
   for (int x = i; x < n * W; x += 32 * kWords) p.mask[seq * n * W + x] = sets[x % W][x / W];
   if (p.slots != nullptr && i < n) {
     p.seq_ids[seq * n + i] = (int32_t)seq;
@@ -98,11 +126,11 @@ struct TreeAcceptParams {
   int32_t* count;           // [num_seqs]
   int32_t* next;            // [num_seqs]
   int32_t* new_lens;        // [num_seqs], or null
+  Accounts accounts;
   int32_t* status;
 };
 
 constexpr int kAcceptThreads = 256;
-constexpr int kTreePages = kMaxNodes / kPage + 1;  // pages that a tree's slots can touch
 static_assert(kAcceptThreads >= kMaxNodes, "a thread per node");
 
 // One CTA per sequence. One warp walks the tree, each lane holding eight nodes: the next node is the
@@ -155,40 +183,45 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const TreeA
     return;
   }
   const int first_page = base / kPage;
+  bool shared = false;
   if (tid >= 32 && tid < 32 + kTreePages) {
     const int j = tid - 32;
     pages[j] = p.pool != nullptr && first_page + j < p.max_pages
                    ? p.block_table[seq * p.max_pages + first_page + j] : -1;
+    shared = p.accounts.refs != nullptr && shared_page(p.accounts, seq, base, n, j);
+  }
+  const int32_t awaited = token;
+  if (walk && tid < 32) {
+    int at = -1, length = 0;
+    while (true) {
+      uint32_t best = 0xFFFFFFFFu;
+#pragma unroll
+      for (int k = kMaxNodes / 32 - 1; k >= 0; --k)
+        if (parent[k] == at && draft[k] == token) best = (uint32_t)(lane + 32 * k);
+      best = __reduce_min_sync(0xffffffffu, best);
+      if (best == 0xFFFFFFFFu) break;  // nodes lie above their parents: at most n steps
+      at = (int)best;
+      if (lane == 0) path[length] = at;
+      ++length;
+      token = target[at];
+    }
+    if (lane == 0) {
+      walked[0] = length;
+      walked[1] = token;
+    }
+  }
+  const bool none = __syncthreads_or(shared);  // in pages that others hold nothing is moved or accepted
+  if (walk) count = walked[0];
+  if (none) {
+    count = 0;
+    if (tid == 0) flag_status(p.status, KV_NVFP4_DEV_SHARED_PAGE);
   }
   if (walk) {
-    if (tid < 32) {
-      int at = -1, length = 0;
-      while (true) {
-        uint32_t best = 0xFFFFFFFFu;
-#pragma unroll
-        for (int k = kMaxNodes / 32 - 1; k >= 0; --k)
-          if (parent[k] == at && draft[k] == token) best = (uint32_t)(lane + 32 * k);
-        best = __reduce_min_sync(0xffffffffu, best);
-        if (best == 0xFFFFFFFFu) break;  // nodes lie above their parents: at most n steps
-        at = (int)best;
-        if (lane == 0) path[length] = at;
-        ++length;
-        token = target[at];
-      }
-      if (lane == 0) {
-        walked[0] = length;
-        walked[1] = token;
-      }
-    }
-    __syncthreads();
-    count = walked[0];
     if (tid < count) p.path[seq * n + tid] = path[tid];
     if (tid == 0) {
       p.count[seq] = count;
-      p.next[seq] = walked[1];
+      p.next[seq] = none ? awaited : walked[1];
     }
-  } else {
-    __syncthreads();
   }
   if (tid == 0 && p.new_lens != nullptr) p.new_lens[seq] = base + count;
   if (p.pool == nullptr) return;
@@ -242,6 +275,11 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const TreeA
   if (bad_page != 0) flag_status(p.status, bad_page);
 }
 
+Accounts accounts_of(const kv_nvfp4_pages* p) {
+  if (p == nullptr) return Accounts{nullptr, nullptr, 0, 0};
+  return Accounts{p->block_table, p->refs, p->max_pages, p->num_pages};
+}
+
 cudaLaunchAttribute programmatic() {
   cudaLaunchAttribute a;
   a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -253,9 +291,10 @@ cudaLaunchAttribute programmatic() {
 
 cudaError_t launch_tree_mask(const int32_t* parents, int32_t num_seqs, int32_t n,
                              const int32_t* lens, const int32_t* first_pos, uint32_t* mask,
-                             int32_t* seq_ids, int32_t* slots, int32_t* positions, int32_t* status,
-                             cudaStream_t stream) {
-  const TreeMaskParams p{parents, lens, first_pos, mask, seq_ids, slots, positions, n, status};
+                             int32_t* seq_ids, int32_t* slots, int32_t* positions,
+                             const kv_nvfp4_pages* pages, int32_t* status, cudaStream_t stream) {
+  const TreeMaskParams p{parents,   lens, first_pos, mask, seq_ids, slots,
+                         positions, accounts_of(pages), n, status};
   cudaLaunchAttribute attr[1] = {programmatic()};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)num_seqs);
@@ -276,10 +315,10 @@ cudaError_t launch_tree_accept(const int32_t* parents, const int32_t* draft, con
                                const int32_t* expected, int32_t num_seqs, int32_t n,
                                const int32_t* lens, const int32_t* block_table, int32_t max_pages,
                                int32_t num_pages, uint8_t* pool, int32_t* path, int32_t* count,
-                               int32_t* next, int32_t* new_lens, int32_t Hkv, int32_t* status,
-                               cudaStream_t stream) {
-  const TreeAcceptParams p{parents, draft, target, expected, lens, block_table, n,   max_pages, num_pages,
-                           Hkv,     pool,  path,   count,    next, new_lens,    status};
+                               int32_t* next, int32_t* new_lens, const kv_nvfp4_pages* pages,
+                               int32_t Hkv, int32_t* status, cudaStream_t stream) {
+  const TreeAcceptParams p{parents, draft, target, expected, lens, block_table, n, max_pages, num_pages,
+                           Hkv, pool, path, count, next, new_lens, accounts_of(pages), status};
   cudaLaunchAttribute attr[1] = {programmatic()};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)num_seqs);

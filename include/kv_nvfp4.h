@@ -70,6 +70,7 @@ typedef int32_t kv_nvfp4_status;
 #define KV_NVFP4_DEV_BAD_ROPE 0x8     /* position >= rope_max_pos for a rotated row */
 #define KV_NVFP4_DEV_TIMEOUT 0x10     /* an internal barrier wait hit its time limit */
 #define KV_NVFP4_DEV_NO_PAGE 0x20     /* fewer free pages than a sequence asked for */
+#define KV_NVFP4_DEV_SHARED_PAGE 0x40 /* a slot to be written lies in a page that others hold as well */
 
 /* Model geometry of one attention layer. The library supports head_dim = 128 and
  * page_size = 64; num_q_heads (at most 4096) must be a multiple of num_kv_heads; rot_dim is a
@@ -346,6 +347,22 @@ kv_nvfp4_status kv_nvfp4_evict_compact(const kv_nvfp4_layout *layout, const int3
                                        float *weights, int64_t weights_stride, int32_t *d_status,
                                        void *stream);
 
+/* Accounts of pages that sequences share ("Pages of sequences that share a pool" below). */
+typedef struct kv_nvfp4_pages {
+  int32_t *block_table; /* [num_seqs][max_pages]; -1 from held[s] on */
+  int32_t *held;        /* [num_seqs] pages in the sequence's row of the table */
+  int32_t *refs;        /* [num_pages] rows that hold the page */
+  int32_t *free_list;   /* [num_pages] a stack: entries [0, *free_count) are the free pages, the last
+                           one is taken next; entries behind them have their old values */
+  int32_t *free_count;  /* [1] */
+  void *workspace;      /* kv_nvfp4_pages_workspace_bytes, 8-byte aligned; zero before the first call
+                           (kv_nvfp4_pages_init sees to it), then left to the library */
+  int32_t num_seqs;     /* at most KV_NVFP4_MAX_ACCOUNTED_SEQS */
+  int32_t max_pages;    /* num_seqs * max_pages is at most 2^31 - 1 */
+  int32_t num_pages;
+} kv_nvfp4_pages;
+#define KV_NVFP4_MAX_ACCOUNTED_SEQS 8192
+
 /* ---- Speculative decoding with a tree of drafted tokens ---------------------------------------------
  * No counterpart in the pages, which verify a chain of drafts (kv_nvfp4_decode_attn with q_len > 1).
  * The n tokens that a step drafts for a sequence are the nodes of a tree, at most KV_NVFP4_MAX_TREE of
@@ -368,15 +385,19 @@ kv_nvfp4_status kv_nvfp4_evict_compact(const kv_nvfp4_layout *layout, const int3
  *   d_mask:       DEVICE uint32 [num_seqs][n][ceil(n / 32)]
  *   d_seq_ids, d_slots, d_positions: DEVICE int32 [num_seqs * n], as kv_nvfp4_append_slots takes them;
  *                 or all three null
+ *   pages:        the accounts that the cache's pages are under (HOST; num_seqs at most theirs), or null
  * A sequence whose length or position is negative, or with n added passes 31 bits, sets
  * KV_NVFP4_DEV_BAD_POS: its nodes' sequence, slot and position are -1, which kv_nvfp4_append_slots refuses
- * (KV_NVFP4_DEV_BAD_SEQ and BAD_POS) and skips, and its mask is left as it was. One kernel launch.
- * num_seqs = 0 does nothing. */
+ * (KV_NVFP4_DEV_BAD_SEQ and BAD_POS) and skips, and its mask is left as it was. The same, with
+ * KV_NVFP4_DEV_SHARED_PAGE, for a sequence whose slots len .. len + n - 1 lie in a page that by the
+ * accounts other sequences hold too (it was forked, and no resize has made room since, or one was
+ * refused). One kernel launch. num_seqs = 0 does nothing. */
 #define KV_NVFP4_MAX_TREE 256
 kv_nvfp4_status kv_nvfp4_tree_mask(const int32_t *d_parents, int32_t num_seqs, int32_t n,
                                    const int32_t *d_lens, const int32_t *d_first_pos,
                                    uint32_t *d_mask, int32_t *d_seq_ids, int32_t *d_slots,
-                                   int32_t *d_positions, int32_t *d_status, void *stream);
+                                   int32_t *d_positions, const kv_nvfp4_pages *pages,
+                                   int32_t *d_status, void *stream);
 
 /* Attention of a tree's nodes: kv_nvfp4_decode_attn where node i of sequence s sees the keys of slots
  * t < seq_len - q_len and, of the q_len last slots, those whose bit in mask[s][i] is set (slot
@@ -418,21 +439,24 @@ kv_nvfp4_status kv_nvfp4_tree_attn(const kv_nvfp4_layout *layout, const kv_nvfp4
  *   d_count:    DEVICE int32 [num_seqs]
  *   d_next:     DEVICE int32 [num_seqs], the token awaited behind the path; may be d_expected
  *   d_new_lens: DEVICE int32 [num_seqs], len + count, or null; may be d_lens
+ *   pages:      the accounts that the cache's pages are under (HOST; num_seqs at most theirs), or null
  * With d_parents null (and d_draft, d_target, d_expected, d_next too) d_path and d_count are given: a
  * path that was chosen another way, or the moves of a further layer's pool. A sequence with a negative
  * length, a tree that ends past max_pages * 64 or a given path that does not ascend within [0, n) sets
  * KV_NVFP4_DEV_BAD_POS and is skipped, its outputs left as they were but for the count of a tree that
  * was to be walked, which is 0 (a further layer's call then moves nothing); a row whose old or new page lies
  * outside the pool sets KV_NVFP4_DEV_BAD_PAGE and is not moved. Pages that the tree's slots lie in must
- * not be shared between sequences (kv_nvfp4_pages_resize sees to it). One kernel launch. num_seqs = 0
- * does nothing. */
+ * not be shared between sequences (kv_nvfp4_pages_resize sees to it): where the accounts say that one
+ * is, nothing is accepted and moved (count 0 of a tree that is walked, d_next the awaited token, d_new_lens
+ * the old length) and KV_NVFP4_DEV_SHARED_PAGE is set. One kernel launch. num_seqs = 0 does nothing. */
 kv_nvfp4_status kv_nvfp4_tree_accept(const kv_nvfp4_layout *layout, const int32_t *d_parents,
                                      const int32_t *d_draft, const int32_t *d_target,
                                      const int32_t *d_expected, int32_t num_seqs, int32_t n,
                                      const int32_t *d_lens, const int32_t *d_block_table,
                                      int32_t max_pages, int32_t num_pages, uint8_t *pool,
                                      int32_t *d_path, int32_t *d_count, int32_t *d_next,
-                                     int32_t *d_new_lens, int32_t *d_status, void *stream);
+                                     int32_t *d_new_lens, const kv_nvfp4_pages *pages,
+                                     int32_t *d_status, void *stream);
 
 /* ---- Pages of sequences that share a pool ------------------------------------------------------------
  * No counterpart in the pages. The accounts say which pages every sequence holds and which are free;
@@ -441,21 +465,14 @@ kv_nvfp4_status kv_nvfp4_tree_accept(const kv_nvfp4_layout *layout, const int32_
  * (kv_nvfp4_pages_fork); kv_nvfp4_pages_resize makes room that is a sequence's own, so every call that
  * writes into the cache has to come behind a resize whose room covers what it writes and whose `keep`
  * covers what has to stay. An eviction in place writes below `keep`: where pages there are shared it
- * needs a destination of its own (kv_nvfp4_evict_compact). */
-typedef struct kv_nvfp4_pages {
-  int32_t *block_table; /* [num_seqs][max_pages]; -1 from held[s] on */
-  int32_t *held;        /* [num_seqs] pages in the sequence's row of the table */
-  int32_t *refs;        /* [num_pages] rows that hold the page */
-  int32_t *free_list;   /* [num_pages] a stack: entries [0, *free_count) are the free pages, the last
-                           one is taken next; entries behind them have their old values */
-  int32_t *free_count;  /* [1] */
-  void *workspace;      /* kv_nvfp4_pages_workspace_bytes, 8-byte aligned; zero before the first call
-                           (kv_nvfp4_pages_init sees to it), then left to the library */
-  int32_t num_seqs;     /* at most KV_NVFP4_MAX_ACCOUNTED_SEQS */
-  int32_t max_pages;    /* num_seqs * max_pages is at most 2^31 - 1 */
-  int32_t num_pages;
-} kv_nvfp4_pages;
-#define KV_NVFP4_MAX_ACCOUNTED_SEQS 8192
+ * needs a destination of its own (kv_nvfp4_evict_compact).
+ *
+ * A resize may refuse a sequence (d_kept: -1). Its room may then be missing, and where it is to be written
+ * it may hold pages that others hold as well, so that nothing may be written for it. The calls that are
+ * given the accounts leave such pages as they are and set KV_NVFP4_DEV_SHARED_PAGE: kv_nvfp4_pages_append,
+ * kv_nvfp4_tree_mask and kv_nvfp4_tree_accept (several layers: each one's calls). The others do not look:
+ * kv_nvfp4_append(_slots) takes sequence id -1 for such a token, and kv_nvfp4_decode_step(_host) writes
+ * every sequence of its plan, all of which must have been served. */
 
 /* Bytes of the accounts' workspace; 0 for num_pages < 0. */
 size_t kv_nvfp4_pages_workspace_bytes(int32_t num_pages);
@@ -490,12 +507,28 @@ kv_nvfp4_status kv_nvfp4_pages_fork(const kv_nvfp4_pages *pages, const int32_t *
  * the sequence stays as it was and KV_NVFP4_DEV_NO_PAGE is set.
  *   d_keep_lens, d_new_lens: DEVICE int32 [num_seqs]
  *   d_copies:  DEVICE int32 [num_seqs][2]
+ *   d_kept:    DEVICE int32 [num_seqs], not d_keep_lens, that receives keep_lens[s], or -1 where
+ *              sequence s is refused and stays as it was; or null
  * A sequence with keep < 0, new < keep, need > max_pages, or keep beyond the pages that it holds sets
  * KV_NVFP4_DEV_BAD_POS and stays as it was. A page outside the pool in the table is kept or dropped
  * uncounted and sets KV_NVFP4_DEV_BAD_PAGE. One kernel launch of one cluster; calls on the same accounts
  * must not overlap. */
 kv_nvfp4_status kv_nvfp4_pages_resize(const kv_nvfp4_pages *pages, const int32_t *d_keep_lens,
-                                      const int32_t *d_new_lens, int32_t *d_copies,
+                                      const int32_t *d_new_lens, int32_t *d_copies, int32_t *d_kept,
+                                      int32_t *d_status, void *stream);
+
+/* kv_nvfp4_append_slots into the pages under the accounts, whose table, sequences and pages are the
+ * cache's: a K or V row that belongs into a page with more than one holder is not written and sets
+ * KV_NVFP4_DEV_SHARED_PAGE.
+ *   pool:      DEVICE pool of the accounts' num_pages pages
+ *   d_slots:   as for kv_nvfp4_append_slots, or null: the positions
+ * Everything else is kv_nvfp4_append_slots's. One kernel launch. T = 0 does nothing. */
+kv_nvfp4_status kv_nvfp4_pages_append(const kv_nvfp4_layout *layout, const kv_nvfp4_pages *pages,
+                                      const void *q, const void *k, const void *v,
+                                      const int32_t *d_seq_ids, const int32_t *d_slots,
+                                      const int32_t *d_positions, int32_t T,
+                                      const float *d_rope_table, int32_t rope_max_pos,
+                                      uint8_t *pool, uint8_t *q_codes, uint8_t *q_scales,
                                       int32_t *d_status, void *stream);
 
 /* Page copies within a pool: page pairs[i][1] <- page pairs[i][0] for i < n (kv_nvfp4_page_bytes
