@@ -68,9 +68,10 @@ struct ForkParams {
 
 constexpr int kForkThreads = 512;
 
-// One CTA per fork: the row's entries copied, the pages' counts raised. A fork reads only what no fork
-// of the call writes: its own target's count of pages, and its source's, which must not be a target. Bounds:
-// the loads one behind the other and the counts' atomics (8 forks of 1564 pages 4.8 us).
+// One CTA per fork: the row's entries copied, the pages' counts raised. A fork reads only what no other
+// fork of the call writes: its own target's count of pages, and its source's row, which must not be any
+// fork's target (of two that name the same target only the first is carried out). Bounds: the loads one
+// behind the other and the counts' atomics (8 forks of 1564 pages 4.8 us).
 __global__ void __launch_bounds__(kForkThreads) pages_fork_kernel(const ForkParams f) {
   const kv_nvfp4_pages& p = f.p;
   const int tid = threadIdx.x, i = blockIdx.x;

@@ -484,8 +484,9 @@ kv_nvfp4_status kv_nvfp4_pages_init(const kv_nvfp4_pages *pages, void *stream);
  * row of the table is that of src[i], the pages' counts rise. No page is copied: the resize before the
  * next append replaces a shared page that is to be written.
  *   d_src, d_dst, d_lens: DEVICE int32 [n]; n <= num_seqs
- * Every target must hold no page, must not be a source of the call nor stand in d_dst before: else (or
- * with a sequence outside [0, num_seqs)) KV_NVFP4_DEV_BAD_SEQ, and the fork is skipped. A length that
+ * A fork is skipped, with KV_NVFP4_DEV_BAD_SEQ, if its target holds pages or stands in d_dst before it, if
+ * its source stands anywhere in d_dst (as the target of a fork that is skipped itself, too), or if one of
+ * them lies outside [0, num_seqs): so that no fork reads what another of the call writes. A length that
  * the source has no pages for sets KV_NVFP4_DEV_BAD_POS and skips the fork; a page outside the pool is
  * entered, not counted, and sets KV_NVFP4_DEV_BAD_PAGE. One kernel launch. n = 0 does nothing. */
 kv_nvfp4_status kv_nvfp4_pages_fork(const kv_nvfp4_pages *pages, const int32_t *d_src,
