@@ -42,7 +42,7 @@ class PagedNVFP4Cache:
         self.workspace = None
         self.weights_workspace = None
         self.plan_info = None
-        self.pages = None
+        self.pages = self._fitting = None
         self._captured = []
 
     # -- fused quantize-append --------------------------------------------------------------
@@ -190,8 +190,9 @@ class PagedNVFP4Cache:
 
     def attend_tree(self, q_codes, q_scales, out, mask, sm_scale=None, stream=None):
         """Attention of the tree's nodes, the last q_len tokens of every sequence of the last plan()
-        (made with causal=False): each sees the cache and the nodes in its mask. out: bf16. A captured
-        call replays on the plan that it was captured with."""
+        (made with causal=False): each sees the cache and the nodes in its mask. out: bf16. The lengths
+        are the plan's: when tree_accept has advanced them, the next step needs a new plan(). A captured
+        call replays on the plan, and at the lengths, that it was captured with."""
         self._check_current()
         plan = self.plan_info
         if plan is None or plan.causal:
@@ -315,8 +316,10 @@ class PagedNVFP4Cache:
         p = self.pages
         if p is None or p.block_table != self.block_table.data_ptr():
             return None
-        if (p.num_seqs, p.max_pages, p.num_pages) != (self.num_seqs, self.max_pages, self.num_pages):
-            raise ValueError("the accounts are not of as many sequences and pages as the cache has")
+        if p is not self._fitting:  # (looked at once: 0.5 us of a call)
+            if (p.num_seqs, p.max_pages, p.num_pages) != (self.num_seqs, self.max_pages, self.num_pages):
+                raise ValueError("the accounts are not of as many sequences and pages as the cache has")
+            self._fitting = p
         return p
 
     def _enlarge(self, name, need, stream):

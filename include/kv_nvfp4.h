@@ -409,6 +409,10 @@ kv_nvfp4_status kv_nvfp4_tree_mask(const int32_t *d_parents, int32_t num_seqs, i
  *   out:       DEVICE bf16 [num_seqs * q_len][num_q_heads][128], 16-byte aligned: the fp32 result
  *              rounded once. A row that sees no key (no cached token and an empty mask, or bad pages
  *              only) gets zeros.
+ * The sequences' lengths are the plan's, from the host: d_lens of the other calls must be seq_len - q_len.
+ * Behind a kv_nvfp4_tree_accept, whose lengths are on the device, the next step needs a new plan with them:
+ * a captured step that is replayed attends at the lengths that it was captured with, whatever its other
+ * calls find in d_lens.
  * What a row does not see does not reach it, NaN in a hidden node's K or V included. A node whose stored
  * K or V holds a NaN makes NaN of the whole output row of those that see it. Two kernel launches, as for
  * kv_nvfp4_decode_attn. EINVAL for a plan that is not this layout's or is causal, a null or misaligned
@@ -460,8 +464,8 @@ kv_nvfp4_status kv_nvfp4_tree_accept(const kv_nvfp4_layout *layout, const int32_
 
 /* ---- Pages of sequences that share a pool ------------------------------------------------------------
  * No counterpart in the pages. The accounts say which pages every sequence holds and which are free;
- * all of them are DEVICE memory of the caller's, so that a step that takes and returns pages needs no
- * host. One set of accounts serves every layer whose pool has as many pages. Sequences may share pages
+ * all of them are DEVICE memory of the caller's, so that taking and returning pages needs no host (the
+ * attention's plan does, whenever a length has changed). One set of accounts serves every layer whose pool has as many pages. Sequences may share pages
  * (kv_nvfp4_pages_fork); kv_nvfp4_pages_resize makes room that is a sequence's own, so every call that
  * writes into the cache has to come behind a resize whose room covers what it writes and whose `keep`
  * covers what has to stay. An eviction in place writes below `keep`: where pages there are shared it
