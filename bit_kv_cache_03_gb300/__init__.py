@@ -112,6 +112,9 @@ _SIG = {
     "kv_nvfp4_pages_resize": ([ctypes.POINTER(Pages), _P, _P, _P, _P, _P, _P], _I32),
     "kv_nvfp4_pages_append": ([ctypes.POINTER(Layout), ctypes.POINTER(Pages), _P, _P, _P, _P, _P, _P,
                                _I32, _P, _I32, _P, _P, _P, _P, _P], _I32),
+    "kv_nvfp4_pages_decode_step": ([ctypes.POINTER(Layout), ctypes.POINTER(Pages),
+                                    ctypes.POINTER(PlanInfo), _P, _P, _P, _P, _P, _I32, _P, _P, _P,
+                                    ctypes.c_float, _P, _P, _P], _I32),
     "kv_nvfp4_copy_pages": ([ctypes.POINTER(Layout), _P, _I32, _P, _I32, _P, _P], _I32),
     "kv_cmp_page_bytes": ([ctypes.POINTER(Layout), _I32], ctypes.c_size_t),
     "kv_cmp_append": ([ctypes.POINTER(Layout), _I32, _P, _P, _P, _P, _P, _I32, _P, _I32, _P, _I32,
@@ -460,6 +463,17 @@ def kv_nvfp4_decode_step(layout, plan: PlanInfo, workspace, q, k, v, rope, rope_
         _ptr(rope), rope_max_pos, _ptr(block_table), max_pages, num_pages, _ptr(pool),
         _ptr(q_codes_out), _ptr(q_scales_out), float(sm_scale), _ptr(out), _ptr(status),
         _stream(stream)), "kv_nvfp4_decode_step")
+
+
+def kv_nvfp4_pages_decode_step(layout, pages: Pages, plan: PlanInfo, workspace, q, k, v, rope,
+                               rope_max_pos, pool, q_codes_out, q_scales_out, sm_scale, out,
+                               status=None, stream=None):
+    """kv_nvfp4_decode_step in the pages under the accounts: a new row that belongs into a page with more
+    than one holder is not written."""
+    _check(lib().kv_nvfp4_pages_decode_step(
+        ctypes.byref(layout), ctypes.byref(pages), ctypes.byref(plan), _ptr(workspace), _ptr(q), _ptr(k),
+        _ptr(v), _ptr(rope), rope_max_pos, _ptr(pool), _ptr(q_codes_out), _ptr(q_scales_out),
+        float(sm_scale), _ptr(out), _ptr(status), _stream(stream)), "kv_nvfp4_pages_decode_step")
 
 
 def kv_nvfp4_decode_step_host(layout, seq_lens, q_len, causal, chunk_tokens, workspace, ws_bytes,

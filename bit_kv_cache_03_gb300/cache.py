@@ -12,11 +12,11 @@ import torch
 from . import (MAX_TREE, _capturing, kv_nvfp4_append, kv_nvfp4_append_slots, kv_nvfp4_copy_pages,
                kv_nvfp4_decode_attn, kv_nvfp4_decode_attn_weights, kv_nvfp4_decode_step,
                kv_nvfp4_decode_step_host, kv_nvfp4_evict_compact, kv_nvfp4_evict_select,
-               kv_nvfp4_pages_append, kv_nvfp4_pages_fork, kv_nvfp4_pages_init,
-               kv_nvfp4_pages_resize, kv_nvfp4_pages_workspace_bytes, kv_nvfp4_plan,
-               kv_nvfp4_plan_workspace_bytes, kv_nvfp4_pool_bytes, kv_nvfp4_rope_table_init,
-               kv_nvfp4_tree_accept, kv_nvfp4_tree_attn, kv_nvfp4_tree_mask,
-               kv_nvfp4_weights_workspace_bytes, make_layout, make_pages)
+               kv_nvfp4_pages_append, kv_nvfp4_pages_decode_step, kv_nvfp4_pages_fork,
+               kv_nvfp4_pages_init, kv_nvfp4_pages_resize, kv_nvfp4_pages_workspace_bytes,
+               kv_nvfp4_plan, kv_nvfp4_plan_workspace_bytes, kv_nvfp4_pool_bytes,
+               kv_nvfp4_rope_table_init, kv_nvfp4_tree_accept, kv_nvfp4_tree_attn,
+               kv_nvfp4_tree_mask, kv_nvfp4_weights_workspace_bytes, make_layout, make_pages)
 
 
 class PagedNVFP4Cache:
@@ -271,8 +271,8 @@ class PagedNVFP4Cache:
         `copy` the kept tokens in them copied; else self.copies says which (several layers' pools under
         one cache's accounts: kv_nvfp4_copy_pages on each). self.kept holds keep_lens, or -1 where a
         sequence is refused and stays as it was, maybe with shared pages where it is to be written.
-        append, tree_mask and tree_accept leave those as they are; decode_step does not look, and is for
-        plans all of whose sequences were served."""
+        append, decode_step, tree_mask and tree_accept leave those as they are; decode_step_host does not
+        look, and is for steps all of whose sequences were served."""
         self._check_accounted()
         self._int32("keep_lens", keep_lens, self.num_seqs)
         self._int32("new_lens", new_lens, self.num_seqs)
@@ -366,11 +366,18 @@ class PagedNVFP4Cache:
     def decode_step(self, q, k, v, out, q_codes=None, q_scales=None, sm_scale=None, stream=None):
         """New tokens of every sequence (sequence-major rows, at the last q_len positions of the
         lengths given to the last plan) appended and attended in one kernel launch. The positions are
-        the slots too: not for a cache that evict() compacted, whose tokens have other positions. Every
-        sequence of the plan is written: under accounts all have to be ones that resize() served."""
+        the slots too: not for a cache that evict() compacted, whose tokens have other positions. Under
+        accounts rows into pages that several sequences hold are not written (a sequence that resize()
+        refused; its output is then of no use)."""
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(128)
         self._hold_captured(stream)
+        pages = self._accounts()
+        if pages is not None:
+            kv_nvfp4_pages_decode_step(self.layout, pages, self.plan_info, self.workspace, q, k, v,
+                                       self.rope, self.max_pos, self.pool, q_codes, q_scales, sm_scale,
+                                       out, self.status, stream)
+            return
         kv_nvfp4_decode_step(self.layout, self.plan_info, self.workspace, q, k, v, self.rope,
                              self.max_pos, self.block_table, self.max_pages, self.num_pages,
                              self.pool, q_codes, q_scales, sm_scale, out, self.status, stream)
@@ -380,7 +387,8 @@ class PagedNVFP4Cache:
                          causal=True, chunk_tokens=1024, sm_scale=None, stream=None):
         """Plan, host-to-device copies of the new tokens, the fused step and the device-to-host
         copy of the output, enqueued by one library call (the workspace must already be large
-        enough: call plan() once with the same shape first)."""
+        enough: call plan() once with the same shape first). Every sequence is written, whoever else
+        holds its pages."""
         if sm_scale is None:
             sm_scale = 1.0 / math.sqrt(128)
         kv_nvfp4_decode_step_host(self.layout, seq_lens, q_len, causal, chunk_tokens,

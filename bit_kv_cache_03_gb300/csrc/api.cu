@@ -29,7 +29,8 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
                           const uint16_t* v_new, const float* rope, int32_t rope_max_pos,
                           int32_t rot_dim, uint8_t* pool_w, uint8_t* q_codes_out,
                           uint8_t* q_scales_out, bool late_tables, uint16_t* out16, float2* stats,
-                          float* scores, float* part_l, const uint32_t* mask, cudaStream_t stream);
+                          float* scores, float* part_l, const uint32_t* mask, const int32_t* refs,
+                          cudaStream_t stream);
 cudaError_t launch_merge_weights(const void* groups, const int32_t* split_groups,
                                  int32_t num_split, const float* partials, uint16_t* out16,
                                  const float2* stats, const float* scores, const float* w_in,
@@ -476,7 +477,7 @@ kv_nvfp4_status page_copy(const kv_nvfp4_layout* L, bool spill, const uint8_t* p
 }  // namespace
 
 // The fused decode step; late_tables: the plan tables are written by a kernel of the same step
-// (the merge reads them only after its wait).
+// (the merge reads them only after its wait). refs: as in append_impl.
 static kv_nvfp4_status decode_step_impl(const kv_nvfp4_layout* L, const kv_nvfp4_plan_info* plan,
                                      void* d_workspace, const void* q, const void* k,
                                      const void* v, const float* d_rope_table,
@@ -484,7 +485,7 @@ static kv_nvfp4_status decode_step_impl(const kv_nvfp4_layout* L, const kv_nvfp4
                                      int32_t max_pages, int32_t num_pages, uint8_t* pool,
                                      uint8_t* q_codes_out, uint8_t* q_scales_out, float sm_scale,
                                      float* out, int32_t* d_status, bool late_tables,
-                                     void* stream) {
+                                     const int32_t* refs, void* stream) {
   if (kv_nvfp4_layout_check(L) != KV_NVFP4_OK || plan == nullptr) return KV_NVFP4_EINVAL;
   if (L->num_kv_heads > kMaxAttnKvHeads) return KV_NVFP4_EINVAL;
   if (plan->num_kv_heads != L->num_kv_heads || plan->num_seqs <= 0 || plan->q_len <= 0 ||
@@ -514,7 +515,7 @@ static kv_nvfp4_status decode_step_impl(const kv_nvfp4_layout* L, const kv_nvfp4
       L->num_q_heads, L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
       (const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, d_rope_table, rope_max_pos,
       L->rot_dim, pool, q_codes_out, q_scales_out, late_tables, nullptr, nullptr,
-      nullptr, nullptr, nullptr, (cudaStream_t)stream);
+      nullptr, nullptr, nullptr, refs, (cudaStream_t)stream);
   return cuda_status(e);
 }
 
@@ -797,7 +798,7 @@ kv_nvfp4_status kv_nvfp4_decode_attn(const kv_nvfp4_layout* L, const kv_nvfp4_pl
         (float*)(ws + plan->off_partials), out, d_status,
         L->num_q_heads, L->num_kv_heads, plan->q_len, plan->causal, plan->grid, sm_scale,
         nullptr, nullptr, nullptr, nullptr, 0, 0, nullptr, nullptr, nullptr, false, nullptr,
-        nullptr, nullptr, nullptr, nullptr, (cudaStream_t)stream);
+        nullptr, nullptr, nullptr, nullptr, nullptr, (cudaStream_t)stream);
   }
   return cuda_status(e);
 }
@@ -856,7 +857,7 @@ kv_nvfp4_status kv_nvfp4_decode_attn_weights(
         plan->num_split_groups, partials, nullptr, d_status, L->num_q_heads, L->num_kv_heads,
         plan->q_len, plan->causal, plan->grid, sm_scale, nullptr, nullptr, nullptr, nullptr, 0, 0,
         nullptr, nullptr, nullptr, false, (uint16_t*)out, stats, scores, part_l,
-        nullptr, (cudaStream_t)stream);
+        nullptr, nullptr, (cudaStream_t)stream);
     if (e == cudaSuccess)
       e = tile ? kvnvfp4::launch_tile_merge_weights(
                      ws + plan->off_groups, split, plan->num_split_groups, partials, part_l,
@@ -974,7 +975,7 @@ kv_nvfp4_status kv_nvfp4_tree_attn(const kv_nvfp4_layout* L, const kv_nvfp4_plan
       (const int32_t*)(ws + plan->off_split), plan->num_split_groups,
       (float*)(ws + plan->off_partials), nullptr, d_status, L->num_q_heads, L->num_kv_heads,
       plan->q_len, 0, plan->grid, sm_scale, nullptr, nullptr, nullptr, nullptr, 0, 0, nullptr,
-      nullptr, nullptr, false, (uint16_t*)out, nullptr, nullptr, nullptr, d_mask,
+      nullptr, nullptr, false, (uint16_t*)out, nullptr, nullptr, nullptr, d_mask, nullptr,
       (cudaStream_t)stream));
 }
 
@@ -1077,7 +1078,20 @@ kv_nvfp4_status kv_nvfp4_decode_step(const kv_nvfp4_layout* L, const kv_nvfp4_pl
                                      float* out, int32_t* d_status, void* stream) {
   return decode_step_impl(L, plan, d_workspace, q, k, v, d_rope_table, rope_max_pos,
                           d_block_table, max_pages, num_pages, pool, q_codes_out, q_scales_out,
-                          sm_scale, out, d_status, false, stream);
+                          sm_scale, out, d_status, false, nullptr, stream);
+}
+
+kv_nvfp4_status kv_nvfp4_pages_decode_step(
+    const kv_nvfp4_layout* L, const kv_nvfp4_pages* pages, const kv_nvfp4_plan_info* plan,
+    void* d_workspace, const void* q, const void* k, const void* v, const float* d_rope_table,
+    int32_t rope_max_pos, uint8_t* pool, uint8_t* q_codes_out, uint8_t* q_scales_out,
+    float sm_scale, float* out, int32_t* d_status, void* stream) {
+  if (!pages_valid(pages) || (plan != nullptr && plan->num_seqs > pages->num_seqs))
+    return KV_NVFP4_EINVAL;
+  return decode_step_impl(L, plan, d_workspace, q, k, v, d_rope_table, rope_max_pos,
+                          pages->block_table, pages->max_pages, pages->num_pages, pool,
+                          q_codes_out, q_scales_out, sm_scale, out, d_status, false, pages->refs,
+                          stream);
 }
 
 kv_nvfp4_status kv_nvfp4_decode_step_host(
@@ -1142,7 +1156,7 @@ kv_nvfp4_status kv_nvfp4_decode_step_host(
   float* out = zero_copy ? static_cast<float*>(const_cast<void*>(mo)) : d_out;
   s = decode_step_impl(L, &info, d_workspace, d_q, d_k, d_v, d_rope_table, rope_max_pos,
                        d_block_table, max_pages, num_pages, pool, nullptr, nullptr, sm_scale, out,
-                       d_status, zero_copy, stream);
+                       d_status, zero_copy, nullptr, stream);
   if (s != KV_NVFP4_OK) return s;
   if (!zero_copy) {
     e = cudaMemcpyAsync(h_out, d_out, ob, cudaMemcpyDeviceToHost, st);

@@ -163,6 +163,7 @@ struct DecodeParams {
   const float* rope;       // [rope_max_pos][rot_dim]
   int32_t rope_max_pos, rot_dim;
   uint8_t* pool_w;         // the pool, receiving the new K/V rows
+  const int32_t* refs;     // [num_pages] rows of the table that hold a page, or null (no accounts)
   uint8_t* q_codes_out;    // optional copy of the encoded Q rows, or null
   uint8_t* q_scales_out;
   // 1 when the plan tables (cta_seg, segments, groups) were written before the launch (not by the
@@ -704,6 +705,10 @@ __device__ __forceinline__ void new_kv_fetch(const DecodeParams& p, const SegInf
 __device__ __forceinline__ void new_kv_store(const DecodeParams& p, const NewKvRow& r, int lane) {
   if (r.pid < 0 || r.pid >= p.num_pages) {  // the producer skips (and flags) the page as well
     if (lane == 0) flag_status(p.status, KV_NVFP4_DEV_BAD_PAGE);
+    return;
+  }
+  if (p.refs != nullptr && p.refs[r.pid] > 1) {
+    if (lane == 0) flag_status(p.status, KV_NVFP4_DEV_SHARED_PAGE);
     return;
   }
   if (r.is_k && p.rot_dim > 0 && r.pos >= p.rope_max_pos) {
@@ -1451,7 +1456,8 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
                           const uint16_t* v_new, const float* rope, int32_t rope_max_pos,
                           int32_t rot_dim, uint8_t* pool_w, uint8_t* q_codes_out,
                           uint8_t* q_scales_out, bool late_tables, uint16_t* out16, float2* stats,
-                          float* scores, float* part_l, const uint32_t* mask, cudaStream_t stream) {
+                          float* scores, float* part_l, const uint32_t* mask, const int32_t* refs,
+                          cudaStream_t stream) {
   // the attribute belongs to each instantiation and each device: set once per device
   static bool attr_done[64] = {};
   int dev = 0;
@@ -1488,7 +1494,7 @@ cudaError_t launch_decode(const uint8_t* q_codes, const uint8_t* q_scales, const
   p.q_codes_out = q_codes_out; p.q_scales_out = q_scales_out;
   p.early_tables = late_tables ? 0 : 1;
   p.out16 = out16; p.stats = stats; p.scores = scores; p.part_l = part_l;
-  p.mask = mask;
+  p.mask = mask; p.refs = refs;
   const bool fused = q_new != nullptr;
   if (grid <= 0) return cudaSuccess;
   // programmatic dependent launch: the kernel is set up while the previous kernel on the stream

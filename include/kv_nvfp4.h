@@ -474,9 +474,9 @@ kv_nvfp4_status kv_nvfp4_tree_accept(const kv_nvfp4_layout *layout, const int32_
  * A resize may refuse a sequence (d_kept: -1). Its room may then be missing, and where it is to be written
  * it may hold pages that others hold as well, so that nothing may be written for it. The calls that are
  * given the accounts leave such pages as they are and set KV_NVFP4_DEV_SHARED_PAGE: kv_nvfp4_pages_append,
- * kv_nvfp4_tree_mask and kv_nvfp4_tree_accept (several layers: each one's calls). The others do not look:
- * kv_nvfp4_append(_slots) takes sequence id -1 for such a token, and kv_nvfp4_decode_step(_host) writes
- * every sequence of its plan, all of which must have been served. */
+ * kv_nvfp4_pages_decode_step, kv_nvfp4_tree_mask and kv_nvfp4_tree_accept (several layers: each one's
+ * calls). The others do not look: kv_nvfp4_append(_slots) takes sequence id -1 for such a token, and
+ * kv_nvfp4_decode_step(_host) writes every sequence of its plan, all of which must have been served. */
 
 /* Bytes of the accounts' workspace; 0 for num_pages < 0. */
 size_t kv_nvfp4_pages_workspace_bytes(int32_t num_pages);
@@ -571,6 +571,16 @@ kv_nvfp4_status kv_nvfp4_decode_step(const kv_nvfp4_layout *layout,
                                      int32_t num_pages, uint8_t *pool, uint8_t *q_codes_out,
                                      uint8_t *q_scales_out, float sm_scale, float *out,
                                      int32_t *d_status, void *stream);
+
+/* kv_nvfp4_decode_step in the pages under the accounts (kv_nvfp4_pages), whose table and pages are the
+ * cache's: a new K or V row that belongs into a page with more than one holder is not written and sets
+ * KV_NVFP4_DEV_SHARED_PAGE; that sequence's output is then of no use, the others' are as they would be.
+ * EINVAL also for a plan of more sequences than the accounts'. */
+kv_nvfp4_status kv_nvfp4_pages_decode_step(
+    const kv_nvfp4_layout *layout, const kv_nvfp4_pages *pages, const kv_nvfp4_plan_info *plan,
+    void *d_workspace, const void *q, const void *k, const void *v, const float *d_rope_table,
+    int32_t rope_max_pos, uint8_t *pool, uint8_t *q_codes_out, uint8_t *q_scales_out,
+    float sm_scale, float *out, int32_t *d_status, void *stream);
 
 /* ---- One decode step from host buffers ------------------------------------------------------
  * No counterpart in the pages: kv_nvfp4_plan followed by kv_nvfp4_decode_step, with the step's

@@ -49,6 +49,23 @@ def test_pages_append_of_nothing(kv):
     kv.kv_nvfp4_pages_append(kv.make_layout(24, 4), _pages(kv), None, 0, 0, 0, 0, 0, 0, 0, 0, 0, stream=0)
 
 
+@pytest.mark.parametrize("change", [
+    dict(refs=0), dict(workspace=0), dict(q=0), dict(k=0), dict(v=0), dict(pool=0), dict(out=0),
+    dict(rope=0), dict(rope_max_pos=0), dict(max_pages=1), dict(num_seqs=1), dict(q_codes_out=A),
+    dict(out=A + 8), dict(heads=(32, 8)), dict(q_len=2),
+])
+def test_pages_decode_step_refuses(kv, change):
+    change = dict(change)
+    pages = _pages(kv, **{x: change.pop(x) for x in ("refs", "max_pages", "num_seqs") if x in change})
+    L = kv.make_layout(*change.pop("heads", (24, 4)))
+    plan = kv.kv_nvfp4_plan_host(L, [100, 70], change.pop("q_len", 1), True, 64, 8)[0]
+    a = dict(layout=L, pages=pages, plan=plan, workspace=A, q=A, k=A, v=A, rope=A, rope_max_pos=200,
+             pool=A, q_codes_out=None, q_scales_out=None, sm_scale=0.0, out=A, status=None, stream=0)
+    a.update(change)
+    with pytest.raises(kv.KVNVFP4Error, match=r"\(-1\)"):
+        kv.kv_nvfp4_pages_decode_step(**a)
+
+
 def test_resize_refuses_an_unaligned_result(kv):
     with pytest.raises(kv.KVNVFP4Error, match=r"\(-1\)"):
         kv.kv_nvfp4_pages_resize(_pages(kv), A, A, A, None, 0, kept=A + 2)
@@ -64,9 +81,10 @@ def test_the_cache_hands_its_accounts_on(kv, monkeypatch):
     import bit_kv_cache_03_gb300.cache as cache
     seen = []
     for name in ("append", "append_slots", "pages_append", "tree_mask", "tree_accept", "pages_init",
-                 "pages_resize", "copy_pages"):
+                 "pages_resize", "copy_pages", "decode_step", "pages_decode_step"):
         monkeypatch.setattr(cache, "kv_nvfp4_" + name, lambda *a, name=name: seen.append((name, a)))
     monkeypatch.setattr(cache.PagedNVFP4Cache, "_check_current", lambda self: None)
+    monkeypatch.setattr(cache.PagedNVFP4Cache, "_hold_captured", lambda self, stream: None)
     monkeypatch.setattr(cache.PagedNVFP4Cache, "_on", staticmethod(lambda s: contextlib.nullcontext()))
 
     def make(pages=6):
@@ -79,18 +97,20 @@ def test_the_cache_hands_its_accounts_on(kv, monkeypatch):
         c.append(k, k, i32(3), i32(3), slots=i32(3))
         c.tree_mask(i32(3, 5), i32(3), c.tree_buffers(5))
         c.tree_accept(None, None, None, None, i32(3), i32(3, 5), i32(3), None)
+        c.decode_step(k, k, k, k)
         return [name for name, _ in seen], [any(x is c.pages for x in a) for _, a in seen]
 
+    without = ["append", "append_slots", "tree_mask", "tree_accept", "decode_step"]
     c, layer = make(), make()
-    assert calls(c)[0] == ["append", "append_slots", "tree_mask", "tree_accept"]
+    assert calls(c)[0] == without
     c.page_accounts()
-    with_accounts = (["pages_append"] * 2 + ["tree_mask", "tree_accept"], [True] * 4)
+    with_accounts = (["pages_append"] * 2 + ["tree_mask", "tree_accept", "pages_decode_step"], [True] * 5)
     assert calls(c) == with_accounts
     del seen[:]
     c.resize(i32(3), i32(3))
     assert seen[0][0] == "pages_resize" and seen[0][1][-1] is c.kept and c.kept.tolist() == [0] * 3
     layer.block_table = c.block_table  # a further layer without the accounts, and with them
-    assert calls(layer)[0] == ["append", "append_slots", "tree_mask", "tree_accept"]
+    assert calls(layer)[0] == without
     layer.pages = c.pages
     assert calls(layer) == with_accounts
     c.block_table = c.block_table.clone()  # no longer the accounts' table

@@ -262,3 +262,56 @@ def test_appends_beside_refused_rows(T):
     assert torch.equal(codes, codes2) and torch.equal(scales, scales2)
     assert int(c.status.item()) == (k.DEV_SHARED_PAGE * bool(bad.any())
                                     | k.DEV_BAD_PAGE * bool(missing.any()))
+
+
+@pytest.mark.parametrize("Hq,H,q_len", [(24, 4, 1), (8, 4, 3), (3, 3, 1)])
+def test_a_decode_step_beside_a_refused_sequence(Hq, H, q_len):
+    """The fused step of forked sequences that got no page of their own: the shared page stays, the other
+    sequences' rows and outputs are those of a step without it."""
+    k, rng = kv(), np.random.default_rng(Hq)
+    S, P, lens = 4, 4, [100, 100, 100, 30]
+    c = k.PagedNVFP4Cache(4, np.zeros((S, P), np.int32), 300, Hq, H, 32)
+    c.page_accounts()
+    c.pool.copy_(torch.tensor(rng.integers(0x20, 0x40, c.pool.numel(), dtype=np.uint8)))
+    c.resize(dev([0] * S), dev([100, 0, 0, 30]))
+    c.fork(dev([0, 0]), dev([1, 2]), dev([100, 100]))
+    c.resize(dev(lens), dev([x + q_len for x in lens]))
+    assert c.kept.tolist() == [100, -1, -1, 30]
+    c.status.zero_()
+    before, table = c.pool.clone(), c.block_table.clone()
+    q, kk, v = (bf16(rng, S * q_len, h, 128) for h in (Hq, H, H))
+    c.plan([x + q_len for x in lens], q_len, chunk_tokens=64)
+    out = torch.empty(S * q_len, Hq, 128, device="cuda")
+    c.decode_step(q, kk, v, out)
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == k.DEV_SHARED_PAGE
+    # the same without the refused ones
+    at = torch.cat([torch.arange(q_len), torch.arange(3 * q_len, 4 * q_len)]).cuda()
+    want = k.PagedNVFP4Cache(4, table[[0, 3]].cpu().numpy(), 300, Hq, H, 32)
+    want.pool.copy_(before)
+    want.plan([lens[0] + q_len, lens[3] + q_len], q_len, chunk_tokens=64)
+    out2 = torch.empty(2 * q_len, Hq, 128, device="cuda")
+    want.decode_step(q[at], kk[at], v[at], out2)
+    torch.cuda.synchronize()
+    assert int(want.status.item()) == 0
+    assert torch.equal(c.pool, want.pool) and not torch.equal(c.pool, before)
+    # (another plan may split a sequence elsewhere: P is rounded to f16 about another maximum, half a
+    # step of 2^-11 on either side, and |V| is at most 6 times a scale of 1.875)
+    assert torch.allclose(out[at], out2, rtol=0, atol=2.0 ** -10 * 11.25 + 2.0 ** -12)
+    # one of them ends, the other is served: as without accounts (the ended one has no pages)
+    c.resize(dev([100, 0, 100, 30]), dev([100, 0, 100, 30]))
+    lens = [100 + q_len, 64, 100 + q_len, 30 + q_len]
+    c.resize(dev([100, 0, 100, 30]), dev([100 + q_len, 0, 100 + q_len, 30 + q_len]))
+    assert c.kept.tolist() == [100, 0, 100, 30]
+    c.status.zero_()
+    c.plan(lens, q_len, chunk_tokens=64)
+    want = k.PagedNVFP4Cache(4, c.block_table.cpu().numpy(), 300, Hq, H, 32)
+    want.pool.copy_(c.pool)
+    want.plan(lens, q_len, chunk_tokens=64)
+    out.zero_()
+    out3 = torch.zeros_like(out)
+    c.decode_step(q, kk, v, out)
+    want.decode_step(q, kk, v, out3)
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == int(want.status.item()) == k.DEV_BAD_PAGE
+    assert torch.equal(c.pool, want.pool) and torch.equal(out, out3)
