@@ -92,34 +92,6 @@ struct alignas(16) SelectShared {
   uint32_t listed;          // its keys that share them
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The word at this CTA's shared address `a`, of the cluster's CTA `rank`.
-__device__ __forceinline__ uint32_t cluster_peer(uint32_t a, uint32_t rank) {
-  uint32_t remote;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(a), "r"(rank));
-  return remote;
-}
-__device__ __forceinline__ uint32_t cluster_load(uint32_t remote) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
-  return v;
-}
-
 // Four weights from slot t on (16-byte aligned when kVec); slots from `end` on read as 0.
 template <bool kVec>
 __device__ __forceinline__ float4 load_weights4(const float* w, int64_t t, int64_t end) {

@@ -120,33 +120,15 @@ struct ResizeParams {
 constexpr int kResizeThreads = 1024;
 constexpr int kResizeMaxCluster = 8;
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // Every thread of the cluster meets; what was written before is read after it.
 __device__ __forceinline__ void cluster_meet() {
   __syncthreads();
   cluster_arrive();
   cluster_wait();
 }
-__device__ __forceinline__ uint32_t cluster_load(const void* shared, uint32_t rank) {
-  uint32_t remote, v;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(shared)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
-  return v;
+// A word of this CTA's shared memory as the cluster's CTA `rank` has it.
+__device__ __forceinline__ uint32_t peer_word(const void* shared, uint32_t rank) {
+  return cluster_load(cluster_peer(smem_u32(shared), rank));
 }
 
 // Exclusive sum over the block's threads, and the block's sum; v < 2^31 in all.
@@ -180,9 +162,10 @@ __device__ __forceinline__ uint32_t block_rank(bool v, uint32_t* warp_sums, uint
 }
 
 // A resize of at most one entry per thread, by one CTA: everything stays in registers. The cluster meets
-// once, before the first write, so that no CTA reads the sequences' numbers behind it. A page that several rows drop is freed by whoever lowers its count to zero, in the
-// place of its last drop, which that thread looks up. Bounds: about ten dependent loads and barriers, 3.5
-// us (4 sessions) to 4.4 (256) of a resize back to back; in the cluster's form below 10 to 12.
+// once, before the first write, so that no CTA reads the sequences' numbers behind it. A page that
+// several rows drop is freed by whoever lowers its count to zero, in the place of its last drop, which
+// that thread looks up. Bounds: about ten dependent loads and barriers, 3.5 us (4 sessions) to 4.4 (256)
+// of a resize back to back; in the cluster's form below 10 to 12.
 struct FewEntries {
   int32_t top[kResizeThreads];         // the stack from its top on
   int32_t dropped[kResizeThreads];     // page dropped by each entry, or -1
@@ -345,10 +328,10 @@ __device__ __forceinline__ bool resize_shares(const ResizeParams& r, const Pages
   uint32_t taken_before = 0, all_taken = 0;
   bool shared = false;
   for (uint32_t c = 0; c < C; ++c) {
-    const uint32_t n = cluster_load(&out_counts[1], c);
+    const uint32_t n = peer_word(&out_counts[1], c);
     if (c < rank) taken_before += n;
     all_taken += n;
-    shared = shared || cluster_load(&out_counts[2], c) != 0u;
+    shared = shared || peer_word(&out_counts[2], c) != 0u;
   }
   if (all_taken > (uint32_t)free_now) return false;  // the same for the whole cluster
 
@@ -378,7 +361,7 @@ __device__ __forceinline__ bool resize_shares(const ResizeParams& r, const Pages
   cluster_meet();  // the stack's top has been read
   uint32_t freed_before = 0, all_freed = 0;
   for (uint32_t c = 0; c < C; ++c) {
-    const uint32_t n = cluster_load(&out_counts[0], c);
+    const uint32_t n = peer_word(&out_counts[0], c);
     if (c < rank) freed_before += n;
     all_freed += n;
   }
@@ -605,7 +588,7 @@ __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(const Resi
   cluster_meet();
   uint32_t freed_before = 0, taken_before = 0, all_freed = 0;
   for (uint32_t c = 0; c < C; ++c) {
-    const uint32_t a = cluster_load(&out_counts[0], c), b = cluster_load(&out_counts[1], c);
+    const uint32_t a = peer_word(&out_counts[0], c), b = peer_word(&out_counts[1], c);
     if (c < rank) {
       freed_before += a;
       taken_before += b;
