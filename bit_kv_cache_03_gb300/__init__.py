@@ -163,11 +163,13 @@ def _check(status: int, what: str):
 
 def _ptr(x) -> int | None:
     """Device/host address of a tensor-like (torch tensor, numpy array) or None."""
+    if x is None:  # (an exception in the place of this test takes 0.5 us)
+        return None
     try:
         return x.data_ptr()  # a tensor, first: every call passes a dozen
     except AttributeError:
         pass
-    if x is None or isinstance(x, int):
+    if isinstance(x, int):
         return x
     if hasattr(x, "ctypes"):
         return x.ctypes.data

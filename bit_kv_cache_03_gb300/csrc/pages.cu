@@ -219,7 +219,10 @@ __device__ __forceinline__ void resize_few(const ResizeParams& r, FewEntries& sh
   if (e < entries) {
     const bool ok = met(s, upto);
     if (ok && take) atomicMax(&sh.all_taken, upto);
-    if (!ok) bad |= KV_NVFP4_DEV_NO_PAGE;
+    if (!ok) {
+      bad |= KV_NVFP4_DEV_NO_PAGE;
+      if (r.kept != nullptr) r.kept[s] = -1;  // (one that is not met has entries)
+    }
     take = take && ok;
     drop = drop && ok;
   }
@@ -253,13 +256,8 @@ __device__ __forceinline__ void resize_few(const ResizeParams& r, FewEntries& sh
     }
     p.block_table[(int64_t)s * p.max_pages + j] = fresh;
   }
-  for (int q = tid; q < S; q += kResizeThreads) {
-    if (!met(q, upto)) {
-      if (r.kept != nullptr) r.kept[q] = -1;
-    } else if (held_of[q] != need_of[q]) {
-      p.held[q] = need_of[q];
-    }
-  }
+  for (int q = tid; q < S; q += kResizeThreads)
+    if (held_of[q] != need_of[q] && met(q, upto)) p.held[q] = need_of[q];
   if (tid == 0) *p.free_count = (int32_t)min(left + all_freed, (uint32_t)p.num_pages);
   if (bad != 0) flag_status(r.status, bad);
 }
@@ -403,6 +401,12 @@ __device__ __forceinline__ bool resize_shares(const ResizeParams& r, const Pages
 // summed up, so that it is known who gets pages; counts lowered, each page's last drop noted; freed
 // (dropped last, nobody left) and taken entries counted; the freed pages listed and the fresh ones
 // entered by rank; the list pushed onto the stack.
+//
+// Two shorter forms above: at most 1024 entries, and at most 4096 per CTA that the stack can serve. What is
+// left, tens of thousands of entries or a stack that runs out, is bound by the search for an entry's
+// sequence, its page and its count in four passes, the first of them over all entries in every CTA: 31
+// of 32 sessions on one prompt of 100000 tokens end (48453 shared entries) in 46 us, 63 of 64 (98469) in
+// 93; 8 of 9 (12504, the form above) in 11.
 __global__ void __launch_bounds__(kResizeThreads) pages_resize_kernel(const ResizeParams r) {
   extern __shared__ int32_t per_seq[];  // [num_seqs + 1] entries before, [num_seqs] need, held, demand
   __shared__ uint32_t warp_sums[32];
