@@ -1221,8 +1221,8 @@ __device__ void attention_warps(const DecodeParams& p, uint8_t* smem, uint32_t t
 // softmax statistics, for the weights after it (kv_nvfp4_decode_attn_weights); WIDE: groups of one KV
 // head, four pages per stage; TREE: the new tokens are the nodes of a tree (kv_nvfp4_tree_attn), rows
 // go out in bf16. Only pages that hold nodes take more than the plain path: 4 x 131072 tokens, 4 KV heads,
-// one node of 24 heads 64.5 us with its merge (the plain call 62), two of 16 or eight of 4 heads 67.2; two
-// of 24 heads, 12 rows, are the tile kernel's 88.6
+// one node of 24 heads 64.1 us with its merge (the plain call 62), two of 16 or eight of 4 heads 66.7; two
+// of 24 heads, 12 rows, are the tile kernel's 88.0
 template <int NR, bool FUSED, bool ACC, bool WIDE = false, bool TREE = false>
 __global__ void __launch_bounds__(kBoundThreads, 1) decode_kernel(const DecodeParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];

@@ -45,7 +45,9 @@
 // a block in the softmax warps (score load, max, exchange, exponentials, stores, hand-over), about 1870
 // cycles of which the exponentials are 750 to 900; more softmax warps, halves of a block handed on
 // separately, blocks taken in turn and scores loaded ahead all measured 2 to 10 % slower. At most 64 rows:
-// 1540 cycles, of which the eight copies of a block take 1100 or more to issue.
+// 1540 cycles a block (8 nodes, 8 KV heads, 2 x 131072: 88 to 90 us), in which two chains of about
+// that length run side by side: one lane issues the block's eight copies (1100 to 1500), and the roles hand
+// the block on. With the arithmetic left out it is 88 us, with the issue spread over two warps as well 73.
 //
 // Warp roles (480 threads): warp 0 bulk-copy producer, warp 1 Q.K^T issuer and tensor-memory
 // owner, warps 2..9 softmax and epilogue (warp w: lane quadrant w mod 4, key half (w - 2) / 4),

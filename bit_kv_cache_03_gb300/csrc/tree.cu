@@ -52,7 +52,8 @@ struct TreeMaskParams {
 // pointer ends at the cache (-1) or, for a node that hangs nowhere, at -2, whose set is empty.
 //
 // Bounds: the launch, and log2 of the depth pairs of barriers. Replayed from a graph a tree of 8 takes
-// 1.3 us, 128 trees of 256 (1.4 MB written, 0.2 us of HBM time) 3.2; called, both take the host's 5.3.
+// 1.3 to 1.5 us, 128 trees of 256 (1.4 MB written, 0.2 us of HBM time) 3.2 to 3.4, each 0.3 more with
+// accounts (two dependent loads beside the first steps); called, both take the host's 5.3.
 template <int kWords>
 __global__ void __launch_bounds__(32 * kWords) tree_mask_kernel(const TreeMaskParams p) {
   __shared__ uint32_t sets[kWords][32 * kWords];
@@ -142,7 +143,8 @@ static_assert(kAcceptThreads >= kMaxNodes, "a thread per node");
 // wave reads.
 //
 // Bounds: the chain of dependent loads (lengths, tokens and page ids, then rows) and the launch. Replayed
-// from a graph a tree of 16 takes 1.8 us, 64 trees of 64 with 4 KV heads 3.4; called, the host's 6.4 to 6.6.
+// from a graph a tree of 16 takes 1.8 us, 64 trees of 64 with 4 KV heads 2.9, with 8 heads 3.4; called, the
+// host's 6.4 to 6.6.
 __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const TreeAcceptParams p) {
   __shared__ int32_t path[kMaxNodes], target[kMaxNodes], pages[kTreePages];
   __shared__ int32_t walked[2];  // the path's length, the token behind it
