@@ -1039,6 +1039,8 @@ kv_nvfp4_status kv_nvfp4_pages_resize(const kv_nvfp4_pages* pages, const int32_t
   if (!pages_valid(pages) || !d_keep_lens || !d_new_lens || !d_copies) return KV_NVFP4_EINVAL;
   if (!aligned4(d_keep_lens) || !aligned4(d_new_lens) || !aligned4(d_copies) || !aligned4(d_kept))
     return KV_NVFP4_EINVAL;
+  // written while other CTAs may still read these
+  if (d_kept != nullptr && (d_kept == d_keep_lens || d_kept == d_new_lens)) return KV_NVFP4_EINVAL;
   return cuda_status(kvnvfp4::launch_pages_resize(pages, d_keep_lens, d_new_lens, d_copies, d_kept,
                                                   d_status, (cudaStream_t)stream));
 }

@@ -512,8 +512,8 @@ kv_nvfp4_status kv_nvfp4_pages_fork(const kv_nvfp4_pages *pages, const int32_t *
  * the sequence stays as it was and KV_NVFP4_DEV_NO_PAGE is set.
  *   d_keep_lens, d_new_lens: DEVICE int32 [num_seqs]
  *   d_copies:  DEVICE int32 [num_seqs][2]
- *   d_kept:    DEVICE int32 [num_seqs], not d_keep_lens, that receives keep_lens[s], or -1 where
- *              sequence s is refused and stays as it was; or null
+ *   d_kept:    DEVICE int32 [num_seqs] that receives keep_lens[s], or -1 where sequence s is refused and
+ *              stays as it was; or null. It must not overlap d_keep_lens or d_new_lens
  * A sequence with keep < 0, new < keep, need > max_pages, or keep beyond the pages that it holds sets
  * KV_NVFP4_DEV_BAD_POS and stays as it was. A page outside the pool in the table is kept or dropped
  * uncounted and sets KV_NVFP4_DEV_BAD_PAGE. One kernel launch of one cluster; calls on the same accounts

@@ -66,9 +66,10 @@ def test_pages_decode_step_refuses(kv, change):
         kv.kv_nvfp4_pages_decode_step(**a)
 
 
-def test_resize_refuses_an_unaligned_result(kv):
+@pytest.mark.parametrize("kept", [A + 2, A, A + 64])
+def test_resize_refuses_a_result_that_is_unaligned_or_an_input(kv, kept):
     with pytest.raises(kv.KVNVFP4Error, match=r"\(-1\)"):
-        kv.kv_nvfp4_pages_resize(_pages(kv), A, A, A, None, 0, kept=A + 2)
+        kv.kv_nvfp4_pages_resize(_pages(kv), A, A + 64, A + 128, None, 0, kept=kept)
 
 
 def i32(*shape):
