@@ -256,8 +256,9 @@ class PagedNVFP4Cache:
     def fork(self, src, dst, lens, stream=None):
         """Sequences dst[i], which hold no pages, share those of the first lens[i] tokens of src[i]
         (device int32). A fork whose source stands anywhere in dst is refused, as is one whose target
-        holds pages or stands in dst before. The next resize() replaces what a sequence is about to write; evict() writes from
-        a sequence's first slot on and is not for sequences that share pages."""
+        holds pages or stands in dst before. The next resize() replaces what a sequence is about to
+        write; evict() writes from a sequence's first slot on and is not for sequences that share
+        pages."""
         self._check_accounted()
         for name, x in (("src", src), ("dst", dst), ("lens", lens)):
             self._int32(name, x, dst.numel())
